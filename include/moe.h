@@ -472,6 +472,118 @@ moe_status_t moe_layer_forward_w8a8(const uint16_t* x, const float* W_r, const f
                                     moe_w8_t Wgu_s, moe_w8_t Wd_s, uint16_t* out, void* ws,
                                     size_t ws_bytes, void* stream);
 
+/* ============================================================================
+ * The attention next to the layer: a paged key/value cache, written and read
+ * back in bf16, E4M3 or int4 rows, and the attention of each sequence's new
+ * tokens over it -- one token of a decode step, a few drafted tokens, a chunk
+ * of a prompt, or any mix of them in one call.
+ *
+ * The cache is a pool of n_pages pages of `page` token slots for H_kv heads.
+ * Slot s of page p is named p * page + s.  Row (p, h, s) of the keys starts at
+ * k + p * page_stride + h * head_stride + s * slot_stride bytes, the values
+ * likewise at v, so a pool may lie page by page, head-major or token-major, or
+ * be a slice of a larger one.  The row scales are fp32 [n_pages][H_kv][page].
+ * Rows, with the library's weight recipes and one scale per row:
+ *   MOE_KV_BF16  D bf16 values; ks and vs are not used (NULL)
+ *   MOE_KV_E4M3  D codes: s = absmax / 448, code = e4m3(x / s)
+ *   MOE_KV_INT4  D/2 bytes: s = absmax / 7, q = clamp(rint(x / s), -8, 7); byte
+ *                j holds element 2j in bits 0-3 and 2j+1 in bits 4-7
+ * (fp32 divisions, ties to even, conversions saturate; s = 0 gives codes 0.)
+ * A stored element stands for code * s.
+ * ========================================================================= */
+typedef enum { MOE_KV_BF16 = 0, MOE_KV_E4M3 = 1, MOE_KV_INT4 = 2 } moe_kv_format_t;
+
+/* Sizes of one call on a cache.  Supported: D 64 or 128; page 16, 32, 64, 128
+   or 256; H a multiple of H_kv with H / H_kv <= 128; B <= 8192; n_pages * page,
+   max_pages * page and T * H below 2^31. */
+typedef struct {
+    int32_t T;         /* tokens of the call: rows of q, k, v, out and slots      */
+    int32_t B;         /* sequences                                              */
+    int32_t H;         /* query heads                                            */
+    int32_t H_kv;      /* key/value heads; query head h reads head h / (H / H_kv) */
+    int32_t D;         /* head width                                             */
+    int32_t page;      /* token slots per page                                   */
+    int32_t n_pages;   /* pages in the pool                                      */
+    int32_t max_pages; /* row length of the page table                           */
+    int32_t max_new;   /* most new tokens of one sequence, 0 if not known: chooses
+                          the kernels, the results hold for any value             */
+    int32_t window;    /* keys a token sees at most, itself included; 0: all      */
+    int32_t format;    /* moe_kv_format_t                                        */
+    uint32_t flags;    /* 0                                                      */
+} moe_kv_dims_t;
+
+/* A cache pool.  k, v 16-byte aligned, the strides (bytes) positive multiples
+   of 16 below 2^40; ks, vs 4-byte aligned (NULL for MOE_KV_BF16). */
+typedef struct {
+    void* k;
+    void* v;
+    float* ks;
+    float* vs;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+} moe_kv_t;
+
+/* moe_kv_write -- new keys and values into the cache, quantised as they are
+ * written (one launch).
+ *   k, v   (device) bf16 [T][H_kv][D], token t at k + t * ldk (v + t * ldv)
+ *          elements; 16-byte aligned, ldk and ldv multiples of 8, at least
+ *          H_kv * D when T > 1 (so slices of a fused projection's output serve)
+ *   slots  (device) int32 [T], each token's slot; negative: not written.  A
+ *          slot past the pool is not written and sets the device check flag.
+ *          Slots of one call are distinct.
+ *   ws     a workspace of at least 256 bytes, zero-filled before its first use
+ *          (its header takes the device check flags)
+ * Quantised rows must be finite.  B, H, max_pages, max_new and window are not
+ * used beyond their checks. */
+moe_status_t moe_kv_write(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                          const int32_t* slots, const moe_kv_dims_t* dims, const moe_kv_t* cache,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* moe_kv_read -- the named slots back, each element's fp32 code * s rounded to bf16.
+ *   slots  (device) int32 [T]; negative: a row of zeros; past the pool: a row
+ *          of zeros and the device check flag
+ *   k, v   (device) out: bf16 [T][H_kv][D], contiguous, 16-byte aligned
+ * The other arguments as moe_kv_write. */
+moe_status_t moe_kv_read(const int32_t* slots, const moe_kv_dims_t* dims, const moe_kv_t* cache,
+                         uint16_t* k, uint16_t* v, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of moe_attn_paged (0 on invalid dims); serves the two calls above. */
+size_t moe_attn_workspace_bytes(const moe_kv_dims_t* dims);
+
+/* moe_attn_paged -- attention of the new tokens over the cache, which already
+ * holds their own keys and values (moe_kv_write first).  Sequence b has the
+ * tokens q_off[b] .. q_off[b+1] - 1 of the batch, n of them, and kv_len[b] keys,
+ * the new tokens' included; token i of it sits at position
+ * pos = kv_len[b] - n + i and sees the keys max(0, pos - window + 1) .. pos
+ * (window = 0: 0 .. pos).  With s_j = scale * (q . k_j) over those keys,
+ *   out = bf16( sum_j e^(s_j) v_j / sum_j e^(s_j) ),   lse = ln sum_j e^(s_j);
+ * a token that sees no key (kv_len[b] < n) gets out = 0 and lse = -inf.
+ *   q       (device) bf16 [T][H][D], token t at q + t * ldq elements; 16-byte
+ *           aligned, ldq a multiple of 8, at least H * D when T > 1
+ *   q_off   (device) int32 [B+1], ascending from 0 to T; n = 0 is an idle slot
+ *   kv_len  (device) int32 [B]
+ *   pages   (device) int32 [B][max_pages]: key j of sequence b is slot j % page
+ *           of page pages[b][j / page].  Only the entries of pages that hold a
+ *           key some token sees are read.
+ *   scale   factor of the scores, finite
+ *   out     (device) out: bf16 [T][H][D], contiguous, 16-byte aligned
+ *   lse     (device) out, nullable: fp32 [T][H]
+ *   ws      workspace of moe_attn_workspace_bytes(dims), zero-filled before its
+ *           first use; every call leaves it ready for the next, on these or
+ *           smaller dims
+ * Numerics: products and sums in fp32; a weight e^(s_j - m) (times the value
+ * row's scale) is rounded to bf16 before it meets the value codes, its
+ * unrounded value enters the denominator.  Keys and values that some token sees
+ * must be finite; what lies in slots that no token sees never matters.
+ * Device checks (moe_check_device_status): a sequence with q_off descending or
+ * past T, or kv_len outside [0, max_pages * page], is left out; a page id
+ * outside the pool is read as page 0. */
+moe_status_t moe_attn_paged(const uint16_t* q, int64_t ldq, const int32_t* q_off,
+                            const int32_t* kv_len, const int32_t* pages,
+                            const moe_kv_dims_t* dims, const moe_kv_t* cache, float scale,
+                            uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,6 +26,10 @@ MOE_ERR_WORKSPACE = 3
 MOE_ERR_CUDA = 4
 MOE_ERR_DEVICE_CHECK = 5
 
+MOE_KV_BF16 = 0
+MOE_KV_E4M3 = 1
+MOE_KV_INT4 = 2
+
 MOE_FLAG_FORCE_GEMV = 0x1
 MOE_FLAG_FORCE_GROUPED = 0x2
 MOE_FLAG_NO_SCHED = 0x4
@@ -40,7 +44,8 @@ EXPORTS = (
     "moe_combine_shared_residual", "moe_layer_forward_residual", "moe_import_q4_blocks",
     "moe_down_combine_w4a16", "moe_pack_w8", "moe_quant_rows_fp8",
     "moe_layer_workspace_bytes_w8a8", "moe_layer_forward_w8a8", "moe_gateup_swiglu_w8a8",
-    "moe_down_w8a8", "moe_debug_set_waits",
+    "moe_down_w8a8", "moe_debug_set_waits", "moe_kv_write", "moe_kv_read",
+    "moe_attn_workspace_bytes", "moe_attn_paged",
 )
 
 
@@ -72,6 +77,27 @@ class W8(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
 
 
+class KvDims(ctypes.Structure):
+    """moe_kv_dims_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "B", "H", "H_kv", "D", "page", "n_pages", "max_pages", "max_new", "window",
+                 "format")] + [("flags", ctypes.c_uint32)]
+
+    def replace(self, **kw) -> "KvDims":
+        vals = {f: getattr(self, f) for f, _ in self._fields_}
+        vals.update(kw)
+        return KvDims(**vals)
+
+
+class Kv(ctypes.Structure):
+    """moe_kv_t: a cache pool's codes, row scales (device pointers) and strides in bytes.
+    kv_cache makes one and records its shape for the calls' checks."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p),
+                ("vs", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+    shape = None
+
+
 _lib = None
 
 
@@ -85,6 +111,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(Dims)
+    KD, KC, f32 = ctypes.POINTER(KvDims), ctypes.POINTER(Kv), ctypes.c_float
     sigs = {
         "moe_status_string": ([i32], ctypes.c_char_p),
         "moe_pack_w4": ([p, i64, i64, i32, p, p, p], i32),
@@ -111,6 +138,10 @@ def lib() -> ctypes.CDLL:
         "moe_layer_forward_host": ([p, p, p, D, W4, W4, W4, W4, p, p, sz, p], i32),
         "moe_check_device_status": ([p, sz, p], i32),
         "moe_router_topk_noalloc": ([p, p, p, D, p, p, p, p], i32),
+        "moe_kv_write": ([p, i64, p, i64, p, KD, KC, p, sz, p], i32),
+        "moe_kv_read": ([p, KD, KC, p, p, p, sz, p], i32),
+        "moe_attn_workspace_bytes": ([KD], sz),
+        "moe_attn_paged": ([p, i64, p, p, p, KD, KC, f32, p, p, p, sz, p], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -387,3 +418,118 @@ def moe_check_device_status(ws, stream=None) -> int:
     """Synchronises the stream; returns the status (MOE_ERR_DEVICE_CHECK if a device check
     tripped since the last call) without raising."""
     return lib().moe_check_device_status(_ptr(ws), ws.numel(), _stream(stream))
+
+
+# ------------------------------------------------------- the paged cache and its attention
+
+_KV_DTYPES = {MOE_KV_BF16: (torch.bfloat16, torch.int16), MOE_KV_E4M3: (torch.uint8,),
+              MOE_KV_INT4: (torch.uint8,)}
+
+
+def _kv_row(fmt: int, D: int) -> int:
+    """Elements of a cache row: D values, D codes or D/2 bytes."""
+    return D // 2 if fmt == MOE_KV_INT4 else D
+
+
+def kv_cache(k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor | None = None,
+             vs: torch.Tensor | None = None) -> Kv:
+    """A cache pool from its tensors: k and v [n_pages][H_kv][page][row], bf16 rows of D values
+    or uint8 rows of D (E4M3) or D/2 (int4) bytes.  The first three dimensions may have any
+    strides that are multiples of 16 bytes, the same for k and v; the rows are contiguous.
+    ks and vs: fp32 [n_pages][H_kv][page], contiguous; for uint8 rows only.  The tensors must
+    outlive the handle."""
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("k and v must be CUDA tensors")
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be 4-dimensional, of one shape and type")
+    if k.dtype not in (torch.bfloat16, torch.int16, torch.uint8):
+        raise ValueError(f"k and v must be bf16 or uint8, got {k.dtype}")
+    if k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("the rows of k and v must be contiguous")
+    size = k.element_size()
+    row = k.shape[3] * size
+
+    def strides(t):  # a dimension of one element has no stride of its own
+        return [t.stride(i) * size if t.shape[i] > 1 else row for i in range(3)]
+
+    if strides(k) != strides(v):
+        raise ValueError("k and v must have the same strides")
+    quantised = k.dtype == torch.uint8
+    if quantised != (ks is not None) or quantised != (vs is not None):
+        raise ValueError("ks and vs belong to uint8 rows, both of them")
+    for t, n in ((ks, "ks"), (vs, "vs")):
+        if t is not None and tuple(t.shape) != tuple(k.shape[:3]):
+            raise ValueError(f"{n} must be [n_pages][H_kv][page]")
+    c = Kv(k.data_ptr(), v.data_ptr(), _dev(ks, torch.float32, "ks") if quantised else None,
+           _dev(vs, torch.float32, "vs") if quantised else None, *strides(k))
+    c.shape, c.dtype = tuple(k.shape), k.dtype
+    return c
+
+
+def _kv_check(dims: KvDims, cache: Kv):
+    if cache.shape is not None and (
+            cache.shape != (dims.n_pages, dims.H_kv, dims.page, _kv_row(dims.format, dims.D)) or
+            cache.dtype not in _KV_DTYPES.get(dims.format, (cache.dtype,))):
+        raise ValueError("the cache's shape or type is not that of dims")
+
+
+def _rows(t: torch.Tensor, T: int, H: int, D: int, name: str):
+    """Pointer and token stride of bf16 [T][H][D] whose tokens may lie apart."""
+    if not t.is_cuda or t.dtype not in _ALIASES[torch.int16]:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must be [T][H][D] with contiguous tokens, got {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def _ints(t: torch.Tensor, n: int, name: str):
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return _dev(t, torch.int32, name)
+
+
+def moe_attn_workspace_bytes(dims: KvDims) -> int:
+    return lib().moe_attn_workspace_bytes(ctypes.byref(dims))
+
+
+def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, dims: KvDims, cache: Kv, ws,
+                 stream=None):
+    """New keys and values bf16 [T][H_kv][D] (tokens may lie apart) into the cache's slots
+    int32 [T]; a negative slot is not written."""
+    _kv_check(dims, cache)
+    kp, ldk = _rows(k, dims.T, dims.H_kv, dims.D, "k")
+    vp, ldv = _rows(v, dims.T, dims.H_kv, dims.D, "v")
+    _check(lib().moe_kv_write(kp, ldk, vp, ldv, _ints(slots, dims.T, "slots"), ctypes.byref(dims),
+                              ctypes.byref(cache), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_kv_write")
+
+
+def moe_kv_read(slots: torch.Tensor, dims: KvDims, cache: Kv, k: torch.Tensor, v: torch.Tensor, ws,
+                stream=None):
+    """The slots int32 [T] back as bf16 rows k, v [T][H_kv][D]; a negative slot gives zeros."""
+    _kv_check(dims, cache)
+    n = dims.T * dims.H_kv * dims.D
+    if k.numel() != n or v.numel() != n:
+        raise ValueError("k and v must be [T][H_kv][D]")
+    _check(lib().moe_kv_read(_ints(slots, dims.T, "slots"), ctypes.byref(dims), ctypes.byref(cache),
+                             _dev(k, torch.int16, "k"), _dev(v, torch.int16, "v"), _ptr(ws),
+                             ws.numel(), _stream(stream)), "moe_kv_read")
+
+
+def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor,
+                   dims: KvDims, cache: Kv, scale: float, out: torch.Tensor,
+                   lse: torch.Tensor | None, ws, stream=None):
+    """Attention of the new tokens q bf16 [T][H][D] (tokens may lie apart) over the cache, which
+    holds their keys and values: out bf16 [T][H][D], lse fp32 [T][H] or None.  q_off int32
+    [B+1], kv_len int32 [B], pages int32 [B][max_pages]; see include/moe.h."""
+    _kv_check(dims, cache)
+    T, H, D = dims.T, dims.H, dims.D
+    qp, ldq = _rows(q, T, H, D, "q")
+    if out.numel() != T * H * D or (lse is not None and lse.numel() != T * H):
+        raise ValueError("out must be [T][H][D] and lse [T][H]")
+    _check(lib().moe_attn_paged(
+        qp, ldq, _ints(q_off, dims.B + 1, "q_off"), _ints(kv_len, dims.B, "kv_len"),
+        _ints(pages, dims.B * dims.max_pages, "pages"), ctypes.byref(dims), ctypes.byref(cache),
+        scale, _dev(out, torch.int16, "out"),
+        None if lse is None else _dev(lse, torch.float32, "lse"), _ptr(ws), ws.numel(),
+        _stream(stream)), "moe_attn_paged")

@@ -20,6 +20,9 @@ enum : int32_t {
     kErrCountMismatch = 1 << 1,  // descriptor counts do not add up to T*k
     kErrWaitTimeout = 1 << 2,    // a bounded spin-wait gave up
     kErrBadTile = 1 << 3,        // a tile index outside its bounds
+    kErrBadSlot = 1 << 4,        // a cache slot past the pool
+    kErrBadSeq = 1 << 5,         // a sequence's token range or length outside its bounds
+    kErrBadPage = 1 << 6,        // a page id outside the pool
 };
 
 // Workspace header: the first 256 bytes of every workspace.

@@ -153,10 +153,10 @@ def reference(b: Batch):
     Bounds, from the stated numerics.  A score is a sum of D exact products in fp32: off by at
     most e = D * 2^-23 * S + |s| * 2^-22, S the sum of the products' magnitudes (2^-23, as a
     tensor core may cut instead of rounding).  Each weight e^s is then off by the factor e of
-    its own score and the maximum's, by 2^-21 in the exponential, and by 2^-9 when it is
-    rounded to bf16; the sums add n * 2^-24 at most.  So out is off by at most
-    A * (2^-9 + 2 * (2 e + 2^-21 + n * 2^-23)) with A = sum p |v|, and its own rounding adds
-    2^-9 * A; lse by 2 e + 2^-20 + n * 2^-24.  A weight, or its product with a value's scale,
+    its own score and the maximum's, by 2^-21 in the exponential, and by 2^-8 when it is
+    rounded to bf16 (eight significant bits: half of the last is 2^-8 of the first); the sums
+    add n * 2^-24 at most.  So out is off by at most A * (2^-8 + 2 * (2 e + 2^-21 + n * 2^-23))
+    with A = sum p |v|, and its own rounding adds 2^-8 * A; lse by 2 e + 2^-20 + n * 2^-24.  A weight, or its product with a value's scale,
     below the smallest normal number 2^-126 may vanish before it meets a code of up to 448:
     n * 2^-117 * max(1, |v|) at most."""
     T, G = sum(b.new), b.H // b.H_kv
@@ -184,7 +184,7 @@ def reference(b: Batch):
             A = torch.einsum("hgj,jhd->hgd", p, v.abs())
             out[t0 + r] = torch.einsum("hgj,jhd->hgd", p, v).reshape(b.H, b.D)
             lse[t0 + r] = z.reshape(-1)
-            rel = 2.0 ** -8 + 2 * (2 * e + 2.0 ** -21 + len(j) * 2.0 ** -23)
+            rel = 2.0 ** -7 + 2 * (2 * e + 2.0 ** -21 + len(j) * 2.0 ** -23)
             tiny = len(j) * 2.0 ** -117 * v.abs().max().clamp(min=1.0)
             bo[t0 + r] = (A * rel[..., None] + tiny).reshape(b.H, b.D)
             bl[t0 + r] = (2 * e + 2.0 ** -20 + len(j) * 2.0 ** -24).reshape(-1)

@@ -512,8 +512,8 @@ typedef struct {
     uint32_t flags;    /* 0                                                      */
 } moe_kv_dims_t;
 
-/* A cache pool.  k, v 16-byte aligned, the strides (bytes) positive multiples
-   of 16 below 2^40; ks, vs 4-byte aligned (NULL for MOE_KV_BF16). */
+/* A cache pool.  k, v, ks, vs 16-byte aligned (ks, vs NULL for MOE_KV_BF16), the
+   strides (bytes) positive multiples of 16 below 2^40. */
 typedef struct {
     void* k;
     void* v;

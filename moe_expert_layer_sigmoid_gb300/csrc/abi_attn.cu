@@ -31,8 +31,7 @@ bool kv_ok(const moe_kv_t* c, const moe_kv_dims_t& d) {
     for (const int64_t s : {c->page_stride, c->head_stride, c->slot_stride})
         if (s <= 0 || s % 16 || s >= (int64_t)1 << 40) return false;
     if (d.format == MOE_KV_BF16) return true;
-    return c->ks && c->vs && reinterpret_cast<uintptr_t>(c->ks) % 4 == 0 &&
-           reinterpret_cast<uintptr_t>(c->vs) % 4 == 0;
+    return act_ok(c->ks) && act_ok(c->vs);
 }
 
 // Rows of `width` elements, ld elements apart, read with 16-byte loads.
@@ -53,7 +52,7 @@ extern "C" {
 
 size_t moe_attn_workspace_bytes(const moe_kv_dims_t* dims) {
     if (check_kv_dims(dims) != MOE_OK) return 0;
-    return sizeof(WsHeader);
+    return attn_workspace_bytes(*dims);
 }
 
 moe_status_t moe_kv_write(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,

@@ -45,6 +45,7 @@ cudaError_t launch_kv_write(const uint16_t* k, int64_t ldk, const uint16_t* v, i
                             WsHeader* hdr, cudaStream_t st);
 cudaError_t launch_kv_read(const int32_t* slots, const moe_kv_dims_t& d, const moe_kv_t& cache,
                            uint16_t* k, uint16_t* v, WsHeader* hdr, cudaStream_t st);
+size_t attn_workspace_bytes(const moe_kv_dims_t& d);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace moe

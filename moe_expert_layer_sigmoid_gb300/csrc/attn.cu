@@ -5,14 +5,37 @@
 namespace moe {
 namespace {
 
+// Sequences of at most this many rows (new tokens x query heads per key/value
+// head) run on the warp-level kernel, longer ones on the tcgen05 kernel.
+constexpr int64_t kFewRows = 16;
+
+// Which kernels a call needs, from what the host knows of its sequences.  A
+// sequence's rows are only known on the device, so with both launched each
+// kernel takes its own; a single one takes all.
+struct Kernels {
+    bool rows, tiles;
+};
+Kernels kernels_for(const moe_kv_dims_t& d) {
+    const int64_t G = d.H / d.H_kv;
+    int64_t most = d.max_new > 0 ? std::min(d.max_new, d.T) : d.T;
+    if (most * G <= kFewRows) return {true, false};
+    if (d.B == 1) return {false, true};
+    return {true, true};
+}
+
 // Workspace: the header, the arrival counters of the joins (at a place that no
-// size moves, zero between calls), the partial results.
+// size moves, zero between calls; one set for each kernel), the partial results.
 constexpr size_t kCountersAt = sizeof(WsHeader);
-size_t part_at() { return kCountersAt + align256(sizeof(unsigned) * 2 * (size_t)sm_count()); }
+size_t counters_bytes() { return align256(sizeof(unsigned) * 2 * (size_t)sm_count()); }
+size_t part_at() { return kCountersAt + 2 * counters_bytes(); }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const moe_kv_dims_t& d) { return part_at() + align256(attn_rows_part_bytes(d)); }
+size_t attn_workspace_bytes(const moe_kv_dims_t& d) {
+    const Kernels k = kernels_for(d);
+    return part_at() + (k.rows ? align256(attn_rows_part_bytes(d)) : 0) +
+           (k.tiles ? align256(attn_tiles_part_bytes(d)) : 0);
+}
 
 bool make_kv_map(CUtensorMap* m, const void* base, const AttnArgs& a, int box_bytes, int box_rows) {
     const bool wide = a.d.format == kKvBf16;
@@ -30,9 +53,20 @@ bool make_kv_map(CUtensorMap* m, const void* base, const AttnArgs& a, int box_by
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
+    const Kernels k = kernels_for(a.d);
     uint8_t* ws = reinterpret_cast<uint8_t*>(a.hdr);
-    return launch_attn_rows(a, 0, (int64_t)1 << 62, reinterpret_cast<float*>(ws + part_at()),
-                            reinterpret_cast<unsigned*>(ws + kCountersAt), st);
+    const int64_t most = (int64_t)1 << 62;
+    size_t at = part_at();
+    cudaError_t e = cudaSuccess;
+    if (k.tiles) {
+        e = launch_attn_tiles(a, k.rows ? kFewRows : 0, most, reinterpret_cast<float*>(ws + at),
+                              reinterpret_cast<unsigned*>(ws + kCountersAt + counters_bytes()), st);
+        at += align256(attn_tiles_part_bytes(a.d));
+    }
+    if (k.rows && e == cudaSuccess)
+        e = launch_attn_rows(a, 0, k.tiles ? kFewRows : most, reinterpret_cast<float*>(ws + at),
+                             reinterpret_cast<unsigned*>(ws + kCountersAt), st);
+    return e;
 }
 
 }  // namespace moe

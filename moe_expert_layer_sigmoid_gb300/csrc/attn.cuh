@@ -207,5 +207,8 @@ bool make_kv_map(CUtensorMap* m, const void* base, const AttnArgs& a, int box_by
 size_t attn_rows_part_bytes(const moe_kv_dims_t& d);
 cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
                              unsigned* counters, cudaStream_t st);
+size_t attn_tiles_part_bytes(const moe_kv_dims_t& d);
+cudaError_t launch_attn_tiles(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+                              unsigned* counters, cudaStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,756 @@
+// Attention of many rows (chunks of a prompt, drafts) on the tcgen05 tensor
+// cores: 128 rows (tokens x query heads of one key/value head) per accumulator,
+// two accumulators per CTA, one CTA per SM.
+//
+// A key tile of 128 keys is two products, S = Q K^T (128 x 128 x D, both operands
+// in shared memory) and O += P V (P in TMEM, V in shared memory, row-major as the
+// cache holds it: the MN-major operand form).  At D = 128 each takes 512 tensor
+// cycles, so the softmax of a tile (128 exponentials per row) has to hide behind
+// the other accumulator's products: while warpgroup A turns its S into P, the
+// tensor core works on B's P V and next Q K^T, and the other way round.
+// Streams A and B are
+//   - two row tiles of one unit walking the same key tiles, when the unit has
+//     more than 128 rows (each K and V tile is read once for both), or
+//   - even and odd key tiles of one row tile, joined at the end, when it has not.
+//
+// TMEM (512 columns): S of A and B at 0 and 128, O at 256 and 384.  P (bf16, two
+// keys per column) overwrites S in place; the next S of a stream is issued after the
+// P V that reads P, and the tensor core runs one thread's products in order.
+//
+// One thread owns one row: maximum and sum need no exchange.  The running maximum
+// is raised only when a score exceeds it by 2^8, so O is rescaled (read, scaled and
+// written back in TMEM) in few tiles; when S of tile i is ready, P V of tile i - 1 is
+// too, so the row's thread may touch O without a further wait.
+//
+// Quantised caches: TMA brings the codes, a warpgroup turns them into bf16 in
+// place (the codes of a row lie where only the thread that converts it writes, or
+// the group synchronises between reading and writing).  Key scales multiply the
+// scores, value scales the weights, so codes enter the products exactly.
+//
+// Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-7 stream A, 8-11 stream B,
+// 12-15 conversion.
+#include <atomic>
+
+#include "attn.cuh"
+#include "umma.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kTk = 128;  // keys of a tile
+constexpr int kSlots = 4;  // tiles of keys or values in shared memory
+
+template <int FMT, int D>
+struct TilesShape {
+    static constexpr bool kQuant = FMT != kKvBf16;
+    static constexpr int kThreads = kQuant ? 512 : 384;
+    static constexpr int kRowB = kv_row_bytes(FMT, D);
+    static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;
+    static constexpr int kTileB = kTk * D * 2;                // a bf16 tile
+    // where the codes land in a slot: in the place of the second column block (E4M3, D = 128: row
+    // r's codes under row r's values), over the tile (int4, D = 128), behind it (D = 64)
+    static constexpr bool kInPlace = kQuant && D == 128;
+    static constexpr bool kSyncInPlace = kInPlace && FMT == kKvInt4;
+    static constexpr int kRawOff = FMT == kKvE4m3 && D == 128 ? kTileB / 2 : kInPlace ? 0 : kTileB;
+    static constexpr int kSlotB = kTileB + (kQuant && !kInPlace ? kTk * kRowB : 0);
+    static constexpr int kScB = kQuant ? 2 * kTk * 4 : 0;     // key and value scales of a tile
+    static constexpr int kScSlots = 4;
+    // registers per thread: control, streams, conversion; in 128-thread groups they add up to
+    // what the launch holds (168 x 384 or 128 x 512)
+    static constexpr int kRegCtl = kQuant ? 48 : 56, kRegStream = kQuant ? 184 : 224, kRegConv = 96;
+    static_assert(kQuant ? kRegCtl + 2 * kRegStream + kRegConv <= 512 : kRegCtl + 2 * kRegStream <= 504,
+                  "register split");
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffKv = kOffQ + 2 * kTileRows * D * 2;
+    static constexpr int kOffSc = kOffKv + kSlots * kSlotB;
+    static constexpr int kOffBar = kOffSc + kScSlots * kScB;
+    // barriers: FULL, EMPTY, RAW [kSlots]; QF, SF, PF, OD [2]; TD
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarQf = 3 * kSlots,
+                         kBarSf = kBarQf + 2, kBarPf = kBarSf + 2, kBarOd = kBarPf + 2,
+                         kBarTd = kBarOd + 2, kNumBars = kBarTd + 1;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kSmem = kOffMisc + 16 + (kThreads / 32 + 4) * 8;
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+    // a partial result: both streams' rows, O as float4 columns of 128 rows, then maximum and sum
+    static constexpr int kPartStream = kTileRows * D + 2 * kTileRows;
+    static constexpr int kPart = 2 * kPartStream;
+};
+constexpr int kPartSlots = 3;  // per CTA: a unit begun before, a unit ended after, a unit of its own
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// (a0, a1) = (a0, a1) * (b0, b1) and (a0 * s + b, a1 * s + b) in one instruction each
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n"
+        " mov.b64 {%0, %1}, a;\n}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s, float b) {
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 c, {%3, %3};\n"
+        " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(s), "f"(b));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
+        " mov.b64 {%0, %1}, a;\n}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fence_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A pair of consecutive E4M3 codes (bytes i, i + 1 of w, i even) as two bf16: each code to the
+// top byte of a half word, its sign in place, its other bits four down: 2^-120 times the
+// value, restored by one exact product.
+__device__ __forceinline__ uint32_t e4m3_two(uint32_t w, int i) {
+    const uint32_t x = __byte_perm(w, 0, i ? 0x3424 : 0x1404);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;"
+        : "=r"(r)
+        : "r"((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u)), "r"(0x7B807B80u));
+    return r;
+}
+// Nibbles 2i and 2i + 1 of w (two's complement) as two bf16: 128 + (n + 8) by its bits, less 136.
+__device__ __forceinline__ uint32_t int4_two(uint32_t w, int i) {
+    const uint32_t b = w >> (8 * i);
+    uint32_t t, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t) : "r"((b & 0xFu) | (b << 12)), "r"(0x000F000Fu), "r"(0x43084308u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(t), "r"(0x3F803F80u), "r"(0xC308C308u));
+    return r;
+}
+
+// One CTA's stretch of a unit: which key tiles each stream takes.
+struct Stretch {
+    int t0, t1;        // tiles of the unit, relative to u.tile0
+    int lo[2], hi[2];  // of them, those with keys for the stream's rows
+    bool split;        // even and odd tiles of one row tile instead of two row tiles
+    __device__ __forceinline__ bool act(int x, int i) const {
+        if (split && ((i - t0) & 1) != x) return false;
+        return i >= lo[x] && i < hi[x];
+    }
+};
+
+__device__ __forceinline__ Stretch stretch(const AttnParams& p, const Unit& u, int tile, int64_t left) {
+    Stretch s;
+    s.t0 = tile;
+    s.t1 = (int)min((int64_t)u.tiles, tile + left);
+    const int half = p.c.tq / 2, i0 = u.rt * p.c.tq, have = min(p.c.tq, u.n - i0);
+    s.split = have <= half;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        // the stream's tokens [a, b) of the sequence, their keys [k0, k1)
+        const int a = i0 + (s.split ? 0 : x * half), b = min(u.n, s.split ? i0 + have : a + half);
+        const int k1 = max(0, u.len - u.n + b);
+        const int k0 = p.a.d.window ? max(0, u.len - u.n + a - p.a.d.window + 1) : 0;
+        s.lo[x] = max(s.t0, k0 / kTk - u.tile0);
+        s.hi[x] = k1 > k0 ? min(s.t1, (k1 + kTk - 1) / kTk - u.tile0) : s.lo[x];
+    }
+    return s;
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(TilesShape<FMT, D>::kThreads, 1)
+attn_tiles_kernel(const __grid_constant__ AttnParams p) {
+    using S = TilesShape<FMT, D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+    auto bar = [&](int i) { return smem_u32(bars + i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
+    volatile int* last_flag = abort_flag + 1;
+    WsHeader* hdr = p.a.hdr;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(bar(S::kBarFull + s), S::kQuant ? 4 : 1);
+            mbar_init(bar(S::kBarEmpty + s), 1);
+            mbar_init(bar(S::kBarRaw + s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(S::kBarQf + x), 4);
+            mbar_init(bar(S::kBarSf + x), 1);
+            mbar_init(bar(S::kBarPf + x), 4);
+            mbar_init(bar(S::kBarOd + x), 1);
+        }
+        mbar_init(bar(S::kBarTd), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const Share sh = deal<S::kThreads>(p, reinterpret_cast<int64_t*>(smem + S::kOffMisc + 16));
+    if (sh.w0 >= sh.w1) return;
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Unit u = sh.u;
+    int64_t w = sh.w0;
+    int tile = (int)(w - sh.unit0);
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegCtl));
+        if (warp == 0) {
+            // ------------------------------------------------------------ copies
+            const int page = 1 << p.c.page_log2;
+            const int box_rows = page < kTk ? page : kTk;
+            const int boxes = kTk / box_rows;
+            uint32_t it = 0;   // slots filled
+            uint32_t tiles = 0;
+            bool ok = true;
+            while (w < sh.w1 && ok) {
+                const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
+                const int hk = u.hs;
+                const int32_t* row = p.a.pages + (int64_t)u.b * p.a.d.max_pages;
+                const int pg0 = u.key0 >> p.c.page_log2;
+                const int pg1 = (int)(((int64_t)u.key1 + page - 1) >> p.c.page_log2);
+                auto fetch = [&](int at) {
+                    const int i = at + lane;
+                    return i >= pg0 && i < pg1 ? __ldg(row + i) : 0;
+                };
+                int ids = 0, ids_next = 0, ids_at = -1;  // 32 page ids from page ids_at on
+                for (; tile < end && ok; ++tile, ++w, ++tiles) {
+                    const int key = (u.tile0 + tile) * kTk;
+                    const int pg = key >> p.c.page_log2;
+                    if (ids_at < 0 || pg >= ids_at + 32) {
+                        const int at = pg & ~31;
+                        ids = ids_at >= 0 && at == ids_at + 32 ? ids_next : fetch(at);
+                        ids_at = at;
+                        ids_next = fetch(at + 32);
+                    }
+                    int id = __shfl_sync(0xFFFFFFFFu, ids, (pg + lane) & 31);
+                    const bool live = lane < boxes && pg + lane >= pg0 && pg + lane < pg1 &&
+                                      key + lane * box_rows < u.key1;
+                    if (live && (id < 0 || id >= p.a.d.n_pages)) {
+                        record_error(hdr, kErrBadPage);
+                        id = 0;
+                    }
+                    const uint32_t n_live = __popc(__ballot_sync(0xFFFFFFFFu, live));
+                    const int at = key & (page - 1);
+#pragma unroll
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                        const int s = it % kSlots;
+                        if (!mbar_wait(bar(S::kBarEmpty + s), ((it / kSlots) & 1) ^ 1, abort_flag, hdr)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t done = bar((S::kQuant ? S::kBarRaw : S::kBarFull) + s);
+                        const uint32_t sc_bytes = S::kQuant ? box_rows * 4 : 0;
+                        if (lane == 0) mbar_expect_tx(done, n_live * (box_rows * S::kRowB + sc_bytes));
+                        __syncwarp();
+                        if (live) {
+                            const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
+                            const uint32_t d = sbase + S::kOffKv + s * S::kSlotB +
+                                               (S::kQuant ? S::kRawOff : 0) + lane * box_rows * S::kBoxB;
+#pragma unroll
+                            for (int h = 0; h < S::kRowB / S::kBoxB; ++h)
+                                tma_load_4d(d + h * kTk * S::kBoxB, tm, h * S::kBoxB / (S::kQuant ? 1 : 2), at, hk, id, done);
+                            if (S::kQuant)
+                                bulk_load(sbase + S::kOffSc + (tiles % S::kScSlots) * S::kScB + kv * kTk * 4 + lane * box_rows * 4,
+                                          (kv ? p.a.cache.vs : p.a.cache.ks) + ((int64_t)id * p.a.d.H_kv + hk) * page + at,
+                                          sc_bytes, done);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (w < sh.w1 && ok) {
+                    next_unit(p, u);
+                    tile = 0;
+                }
+            }
+            if (!ok)  // no copy may be in flight when the CTA ends
+                for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k)
+                    mbar_drain(bar((S::kQuant ? S::kBarRaw : S::kBarFull) + k % kSlots), (k / kSlots) & 1, hdr);
+        } else if (warp == 1 && lane == 0) {
+            // ---------------------------------------------------------- products
+            const uint32_t id_qk = idesc_bf16(128, kTk), id_pv = idesc_bf16_bmn(128, D);
+            uint32_t it0 = 0;    // slot index of the unit stretch's first key tile
+            uint32_t n_pf[2] = {0, 0}, n_q = 0;
+            bool ok = true;
+            bool fresh[2];
+            auto wait = [&](int b, uint32_t par) {
+                if (ok) ok = mbar_wait(bar(b), par & 1, abort_flag, hdr);
+                tc_fence_after();
+                return ok;
+            };
+            // the tile's slots: K of relative tile i is the 2 i-th after it0, V the next
+            auto kslot = [&](const Stretch& s, int i) { return it0 + 2 * (uint32_t)(i - s.t0); };
+            auto full = [&](uint32_t k) { return wait(S::kBarFull + k % kSlots, k / kSlots); };
+            auto release = [&](uint32_t k) { mma_commit(bar(S::kBarEmpty + k % kSlots)); };
+            auto qk = [&](int x, uint32_t k) {
+                const uint32_t qa = sbase + S::kOffQ + x * kTileRows * D * 2;
+                const uint32_t ka = sbase + S::kOffKv + (k % kSlots) * S::kSlotB;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t o = (ks / 4) * (128 * 128) + (ks % 4) * 32;
+                    mma_ss_bf16(tmem + x * 128, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), id_qk, ks > 0);
+                }
+                mma_commit(bar(S::kBarSf + x));
+            };
+            auto pv = [&](int x, uint32_t k) {
+                const uint32_t va = sbase + S::kOffKv + (k % kSlots) * S::kSlotB;
+#pragma unroll
+                for (int ks = 0; ks < kTk / 16; ++ks)
+                    mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8,
+                           smem_desc_sw128_mn(va + ks * 16 * 128, kTk * 128), id_pv, !(fresh[x] && ks == 0));
+                fresh[x] = false;
+            };
+            while (w < sh.w1 && ok) {
+                const Stretch s = stretch(p, u, tile, sh.w1 - w);
+                fresh[0] = fresh[1] = true;
+                // first products; a stream whose first tile comes later starts in the loop
+                full(kslot(s, s.t0));
+                for (int x = 0; x < 2 && ok; ++x) {
+                    wait(S::kBarQf + x, n_q);
+                    if (ok && s.act(x, s.t0)) qk(x, kslot(s, s.t0));
+                }
+                ++n_q;
+                if (!ok) break;
+                release(kslot(s, s.t0));
+                if (s.split && s.t0 + 1 < s.t1) {
+                    if (!full(kslot(s, s.t0 + 1))) break;
+                    if (s.act(1, s.t0 + 1)) qk(1, kslot(s, s.t0 + 1));
+                    release(kslot(s, s.t0 + 1));
+                }
+                for (int i = s.t0; i < s.t1 && ok; ++i) {
+                    full(kslot(s, i) + 1);
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (s.act(x, i)) {
+                            if (!wait(S::kBarPf + x, n_pf[x]++)) break;
+                            pv(x, kslot(s, i) + 1);
+                        }
+                        if (!s.split && s.act(x, i + 1)) {
+                            if (!full(kslot(s, i + 1))) break;
+                            qk(x, kslot(s, i + 1));
+                        }
+                    }
+                    if (!ok) break;
+                    release(kslot(s, i) + 1);
+                    if (!s.split && i + 1 < s.t1) {
+                        if (!full(kslot(s, i + 1))) break;
+                        release(kslot(s, i + 1));
+                    } else if (s.split && i + 2 < s.t1) {
+                        if (!full(kslot(s, i + 2))) break;
+                        const int x = (i - s.t0) & 1;
+                        if (s.act(x, i + 2)) qk(x, kslot(s, i + 2));
+                        release(kslot(s, i + 2));
+                    }
+                }
+                if (!ok) break;
+                mma_commit(bar(S::kBarOd));
+                mma_commit(bar(S::kBarOd + 1));
+                it0 = kslot(s, s.t1);
+                w += s.t1 - s.t0;
+                if (w < sh.w1) {
+                    next_unit(p, u);
+                    tile = 0;
+                }
+            }
+            if (!ok) {  // products in flight end before TMEM is given back
+                mma_commit(bar(S::kBarTd));
+                mbar_drain(bar(S::kBarTd), 0, hdr);
+            }
+        }
+    } else if (warp < 12) {
+        // ----------------------------------------------------------------- streams
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegStream));
+        const int x = warp >= 8, r = threadIdx.x - (x ? 256 : 128);
+        const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
+        const uint32_t ts = trow + x * 128, to = trow + 256 + x * 128;
+        // a negative scale's sign goes into the queries; never 0, so that a masked -inf stays one
+        const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
+        const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
+        uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
+        bool ok = true;
+        int64_t unit0 = sh.unit0;
+        auto wait = [&](int b, uint32_t par) {  // once a wait gave up the streams run on, in step
+            if (ok) ok = mbar_wait(bar(b), par & 1, abort_flag, hdr);
+        };
+        int64_t orow;       // this thread's row of out and lse: token * H + head, -1: none
+        int pos, first;     // keys it sees: first .. pos
+        auto load_q = [&](const Unit& v, bool split) {
+            const int tok = v.rt * p.c.tq + (split ? 0 : x * half) + r / G, hd = v.hs * G + r % G;
+            const bool live = r < half * G && tok < v.n;
+            orow = live ? (int64_t)(v.tok0 + tok) * p.a.d.H + hd : -1;
+            pos = live ? v.len - v.n + tok : -1;
+            first = p.a.d.window ? max(0, pos - p.a.d.window + 1) : 0;
+            const uint16_t* q = p.a.q + (int64_t)(v.tok0 + tok) * p.a.ldq + hd * D;
+            uint8_t* d = smem + S::kOffQ + x * kTileRows * D * 2 + r * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 e = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
+                e.x ^= flip, e.y ^= flip, e.z ^= flip, e.w ^= flip;
+                *reinterpret_cast<uint4*>(d + (c / 8) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4)) = e;
+            }
+            fence_async();
+            __syncwarp();
+        };
+        Stretch s = stretch(p, u, tile, sh.w1 - w);
+        load_q(u, s.split);
+        if (lane == 0) mbar_arrive(bar(S::kBarQf + x));
+        while (true) {
+            const bool whole = s.t0 == 0 && s.t1 == u.tiles;
+            float m = kNoMax, l = 0.0f;
+            bool any = false;
+            // keys that all of the stream's rows see need no mask
+            const int i0 = u.rt * p.c.tq + (s.split ? 0 : x * half);
+            const int inner1 = u.len - u.n + i0 + 1;
+            const int inner0 = p.a.d.window ? u.len - u.n + min(u.n, i0 + half) - p.a.d.window : 0;
+            for (int i = s.t0; i < s.t1; ++i) {
+                if (!s.act(x, i)) continue;
+                const uint32_t vk = 2 * (tiles0 + (uint32_t)(i - s.t0)) + 1;  // the value tile's slot index
+                const int key = (u.tile0 + i) * kTk;
+                wait(S::kBarSf + x, n_sf++);
+                tc_fence_after();
+                float v[128];
+                uint32_t* vr = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, vr + 32 * c);
+                if (!S::kQuant && !(s.split == false && x == 1 && s.act(0, i)) &&
+                    (key < u.key0 || key + kTk > u.key1)) {
+                    // keys outside [key0, key1) are nobody's: their slots may hold anything, so the
+                    // values are cleared (by the first stream that takes the tile), not just weighted with 0
+                    wait(S::kBarFull + vk % kSlots, vk / kSlots);
+                    if (key + r < u.key0 || key + r >= u.key1) {
+                        uint8_t* z = smem + S::kOffKv + (vk % kSlots) * S::kSlotB + r * 128;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            *reinterpret_cast<uint4*>(z + (c / 8) * (128 * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async();
+                }
+                const float4* ksc = nullptr;
+                if (S::kQuant) {
+                    wait(S::kBarFull + vk % kSlots, vk / kSlots);
+                    ksc = reinterpret_cast<const float4*>(smem + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB);
+                }
+                tmem_wait_ld();
+                if (S::kQuant) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float4 f = ksc[c];
+                        mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
+                        mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
+                    }
+                }
+                if (!(key >= inner0 && key + kTk <= inner1)) {
+                    const int hi = pos - key, lo = first - key;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > hi || c < lo) v[c] = -INFINITY;
+                }
+                float mx = v[0];
+#pragma unroll
+                for (int c = 1; c < 128; ++c) mx = fmaxf(mx, v[c]);
+                mx *= sc;
+                if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
+                    const float mn = fmaxf(m, mx), a = ex2(m - mn);
+                    m = mn;
+                    l *= a;
+                    if (any) {  // P V of the tile before is done: S of this one came after it
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            tmem_st_x32(to + c, o);
+                        }
+                    }
+                }
+                any = true;
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float a = v[32 * h + 2 * c], b = v[32 * h + 2 * c + 1];
+                        fma2(a, b, sc, -m);
+                        a = ex2(a);
+                        b = ex2(b);
+                        add2(l0, l1, a, b);
+                        if (S::kQuant) {
+                            const float2 f = reinterpret_cast<const float2*>(ksc + 32)[16 * h + c];
+                            mul2(a, b, f.x, f.y);
+                        }
+                        pk[c] = bf16x2_of(a, b);
+                    }
+                    tmem_st_x16(ts + 16 * h, pk);
+                }
+                l += l0 + l1;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::kBarPf + x));
+            }
+            tiles0 += s.t1 - s.t0;
+            w += s.t1 - s.t0;
+            const int dtiles = u.tiles;
+            const bool dsplit = s.split;
+            const int64_t drow = orow, dunit0 = unit0;
+            const bool more = w < sh.w1;
+            // The next unit's queries go to shared memory while the last products run (the scores
+            // that read the old ones are done), and are handed over once they are.
+            if (!any) wait(S::kBarOd + x, n_od);
+            if (more) {
+                unit0 += u.tiles;
+                next_unit(p, u);
+                s = stretch(p, u, 0, sh.w1 - w);
+                load_q(u, s.split);
+            }
+            if (any) wait(S::kBarOd + x, n_od);
+            ++n_od;
+            if (more && lane == 0) mbar_arrive(bar(S::kBarQf + x));
+            tc_fence_after();
+            if (whole && !dsplit) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint16_t* out = p.a.out + drow * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_ld_x32(to + c, o);
+                        tmem_wait_ld();
+                    }
+                    if (drow >= 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint4 e = make_uint4(0, 0, 0, 0);
+                            if (any) {
+                                const float* f = reinterpret_cast<const float*>(o) + 8 * k;
+                                e = make_uint4(bf16x2_of(f[0] * inv, f[1] * inv), bf16x2_of(f[2] * inv, f[3] * inv),
+                                               bf16x2_of(f[4] * inv, f[5] * inv), bf16x2_of(f[6] * inv, f[7] * inv));
+                            }
+                            *reinterpret_cast<uint4*>(out + c + 8 * k) = e;
+                        }
+                    }
+                }
+                if (drow >= 0 && p.a.lse) p.a.lse[drow] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                // a partial result of each stream; the CTA that completes the unit joins them
+                const int c = blockIdx.x;
+                const int c0 = whole ? c : share_owner(sh.W, sh.R, dunit0);
+                const int c1 = whole ? c : share_owner(sh.W, sh.R, dunit0 + dtiles - 1);
+                auto part = [&](int k, int y) {
+                    const int slot = whole ? 2 : k == c0;
+                    return p.part + ((int64_t)kPartSlots * k + slot) * S::kPart + y * S::kPartStream;
+                };
+                float4* po = reinterpret_cast<float4*>(part(c, x));
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_ld_x32(to + k, o);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    const float* f = reinterpret_cast<const float*>(o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        __stcg(po + (k / 4 + e) * kTileRows + r, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
+                }
+                __stcg(reinterpret_cast<float2*>(part(c, x) + kTileRows * D) + r, make_float2(m, l));
+                __threadfence();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (threadIdx.x == 128) {
+                    const bool last = whole || atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+                    if (last && !whole) p.counters[c0] = 0;
+                    *last_flag = last;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (*last_flag) {
+                    __threadfence();
+                    // two row tiles: each stream joins its own rows; one: each takes half of the columns
+                    const int y0 = dsplit ? 0 : x, y1 = dsplit ? 1 : x;
+                    float M = kNoMax, L = 0.0f;
+                    for (int k = c0; k <= c1; ++k)
+                        for (int y = y0; y <= y1; ++y)
+                            M = fmaxf(M, __ldcg(&(reinterpret_cast<const float2*>(part(k, y) + kTileRows * D) + r)->x));
+                    for (int k = c0; k <= c1; ++k)
+                        for (int y = y0; y <= y1; ++y) {
+                            const float2 e = __ldcg(reinterpret_cast<const float2*>(part(k, y) + kTileRows * D) + r);
+                            L += e.y * ex2(e.x - M);
+                        }
+                    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                    const int cb = dsplit ? x * (D / 2) : 0, ce = dsplit ? cb + D / 2 : D;
+#pragma unroll 1
+                    for (int k0 = cb; k0 < ce; k0 += 32) {
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = 0.0f;
+#pragma unroll 1
+                        for (int k = c0; k <= c1; ++k)
+                            for (int y = y0; y <= y1; ++y) {
+                                const float* q = part(k, y);
+                                const float a = ex2(__ldcg(&(reinterpret_cast<const float2*>(q + kTileRows * D) + r)->x) - M);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 g = __ldcg(reinterpret_cast<const float4*>(q) + (k0 / 4 + e) * kTileRows + r);
+                                    f[4 * e] += g.x * a;
+                                    f[4 * e + 1] += g.y * a;
+                                    f[4 * e + 2] += g.z * a;
+                                    f[4 * e + 3] += g.w * a;
+                                }
+                            }
+                        if (drow >= 0)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint4*>(p.a.out + drow * D + k0 + 8 * e) = make_uint4(
+                                    bf16x2_of(f[8 * e] * inv, f[8 * e + 1] * inv), bf16x2_of(f[8 * e + 2] * inv, f[8 * e + 3] * inv),
+                                    bf16x2_of(f[8 * e + 4] * inv, f[8 * e + 5] * inv), bf16x2_of(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
+                    }
+                    if (drow >= 0 && p.a.lse && (!dsplit || x == 0))
+                        p.a.lse[drow] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+                }
+                // the flag and the CTA's own slot are free for the next unit
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            // the next P V may overwrite O only after every thread of the warp has read it: P of
+            // the next unit is handed over by the warp as a whole, after this point
+            tc_fence_before();
+            if (!more) break;
+        }
+    } else {
+        // -------------------------------------------------------------- conversion
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
+        if constexpr (S::kQuant) {
+            const int r = threadIdx.x - 384;  // row (key) of the tile
+            uint32_t it = 0, tiles = 0;
+            bool ok = true;
+            while (w < sh.w1) {
+                const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
+                for (; tile < end; ++tile, ++w, ++tiles) {
+                    const int key = (u.tile0 + tile) * kTk + r;
+                    const bool seen = key >= u.key0 && key < u.key1;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const int sl = it % kSlots;
+                        if (ok) ok = mbar_wait(bar(S::kBarRaw + sl), (it / kSlots) & 1, abort_flag, hdr);
+                        uint8_t* slot = smem + S::kOffKv + sl * S::kSlotB;
+                        constexpr int kIn = S::kRowB / 16;  // 16-byte chunks of a row's codes
+                        uint4 raw[kIn];
+                        const int sw = S::kBoxB == 128 ? r & 7 : S::kBoxB == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+#pragma unroll
+                        for (int c = 0; c < kIn; ++c)
+                            raw[c] = *reinterpret_cast<const uint4*>(slot + S::kRawOff + r * S::kRowB + ((c ^ sw) << 4));
+                        if (!seen) {  // nobody's key: its slot may hold anything
+#pragma unroll
+                            for (int c = 0; c < kIn; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+                            if (kv) reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB)[kTk + r] = 0.0f;
+                        }
+                        if (S::kSyncInPlace) asm volatile("bar.sync 2, 128;" ::: "memory");
+                        constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;  // output chunks of an input chunk
+#pragma unroll
+                        for (int c = 0; c < kIn; ++c) {
+                            const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                            for (int k = 0; k < kPer; ++k) {
+                                uint4 o;
+                                if constexpr (FMT == kKvE4m3)
+                                    o = make_uint4(e4m3_two(in[2 * k], 0), e4m3_two(in[2 * k], 2),
+                                                   e4m3_two(in[2 * k + 1], 0), e4m3_two(in[2 * k + 1], 2));
+                                else
+                                    o = make_uint4(int4_two(in[k], 0), int4_two(in[k], 1), int4_two(in[k], 2), int4_two(in[k], 3));
+                                const int oc = c * kPer + k;
+                                *reinterpret_cast<uint4*>(slot + (oc / 8) * (128 * 128) + r * 128 + (((oc & 7) ^ (r & 7)) << 4)) = o;
+                            }
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(S::kBarFull + sl));
+                    }
+                }
+                if (w < sh.w1) {
+                    next_unit(p, u);
+                    tile = 0;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int FMT, int D>
+cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+                   unsigned* counters, cudaStream_t st) {
+    using S = TilesShape<FMT, D>;
+    AttnParams p;
+    p.a = a;
+    const int G = a.d.H / a.d.H_kv;
+    p.c.hg = G;
+    p.c.tq = 2 * (kTileRows / G);
+    p.c.subs = 1;
+    p.c.hs = a.d.H_kv;
+    p.c.tk_log2 = 7;
+    p.c.page_log2 = __builtin_ctz(a.d.page);
+    p.c.min_tiles = 1;
+    p.c.rows_lo = rows_lo;
+    p.c.rows_hi = rows_hi;
+    p.part = part;
+    p.counters = counters;
+    p.scale_log2 = a.scale * kLog2e;
+    if (!make_kv_map(&p.tm_k, a.cache.k, a, S::kBoxB, std::min(a.d.page, kTk)) ||
+        !make_kv_map(&p.tm_v, a.cache.v, a, S::kBoxB, std::min(a.d.page, kTk)))
+        return cudaErrorInvalidValue;
+    const void* kern = reinterpret_cast<const void*>(&attn_tiles_kernel<FMT, D>);
+    cudaError_t e = ensure_dynamic_smem(kern, S::kSmem);
+    if (e != cudaSuccess) return e;
+    // the streams' register share is drawn from what the launch holds: check it once
+    static std::atomic<int> regs{0};
+    if (!regs.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes at{};
+        if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+        regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    const int need = S::kRegCtl + 2 * S::kRegStream + (S::kQuant ? S::kRegConv : 0);
+    if (need * 128 > regs.load(std::memory_order_relaxed) * S::kThreads) return cudaErrorInvalidConfiguration;
+    attn_tiles_kernel<FMT, D><<<sm_count(), S::kThreads, S::kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_tiles_part_bytes(const moe_kv_dims_t& d) {
+    return (size_t)kPartSlots * sm_count() * 2 * (kTileRows * d.D + 2 * kTileRows) * sizeof(float);
+}
+
+cudaError_t launch_attn_tiles(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+                              unsigned* counters, cudaStream_t st) {
+    const bool wide = a.d.D == 128;
+    switch (a.d.format) {
+        case kKvBf16:
+            return wide ? launch<kKvBf16, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch<kKvBf16, 64>(a, rows_lo, rows_hi, part, counters, st);
+        case kKvE4m3:
+            return wide ? launch<kKvE4m3, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch<kKvE4m3, 64>(a, rows_lo, rows_hi, part, counters, st);
+        case kKvInt4:
+            return wide ? launch<kKvInt4, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch<kKvInt4, 64>(a, rows_lo, rows_hi, part, counters, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace moe

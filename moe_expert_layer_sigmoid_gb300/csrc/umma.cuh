@@ -27,6 +27,14 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
     return d;
 }
 
+// The same for an MN-major operand (rows of 64 consecutive M or N elements, 128
+// bytes, one row per K index): 8-row groups along K are 1024 B apart (SBO), the
+// next 64 elements along M or N `lbo` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t lbo) {
+    uint64_t d = smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 16);
+    return d | (uint64_t)(lbo >> 4) << 16;
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, both K-major.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
     return (1u << 4)                        // D format: f32
@@ -35,6 +43,9 @@ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N) {
            | ((uint32_t)(N >> 3) << 17)     // N / 8
            | ((uint32_t)(M >> 4) << 24);    // M / 16
 }
+
+// The same with B MN-major.
+__device__ __forceinline__ uint32_t idesc_bf16_bmn(int M, int N) { return idesc_bf16(M, N) | (1u << 16); }
 
 // Instruction descriptor, kind::f8f6f4: E4M3 A and B (format code 0), fp32 D,
 // both K-major.
@@ -81,6 +92,13 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // TMEM copies of 32 consecutive columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
     asm volatile(
@@ -95,6 +113,15 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* v) {
         : "memory");
 }
 
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
     asm volatile(

@@ -40,6 +40,7 @@ struct AttnCut {
 
 struct AttnParams {
     CUtensorMap tm_k, tm_v;
+    CUtensorMap tm_q;     // the tcgen05 kernel's
     AttnArgs a;
     AttnCut c;
     float* part;          // partial results, two slots for each CTA

@@ -51,24 +51,25 @@ struct TilesShape {
     // where the codes land in a slot: in the place of the second column block (E4M3, D = 128: row
     // r's codes under row r's values), over the tile (int4, D = 128), behind it (D = 64)
     static constexpr bool kInPlace = kQuant && D == 128;
-    static constexpr bool kSyncInPlace = kInPlace && FMT == kKvInt4;
     static constexpr int kRawOff = FMT == kKvE4m3 && D == 128 ? kTileB / 2 : kInPlace ? 0 : kTileB;
     static constexpr int kSlotB = kTileB + (kQuant && !kInPlace ? kTk * kRowB : 0);
     static constexpr int kScB = kQuant ? 2 * kTk * 4 : 0;     // key and value scales of a tile
     static constexpr int kScSlots = 4;
     // registers per thread: control, streams, conversion; in 128-thread groups they add up to
     // what the launch holds (168 x 384 or 128 x 512)
-    static constexpr int kRegCtl = kQuant ? 48 : 56, kRegStream = kQuant ? 184 : 224, kRegConv = 96;
+    static constexpr int kRegCtl = 72, kRegStream = kQuant ? 176 : 216, kRegConv = 88;
     static_assert(kQuant ? kRegCtl + 2 * kRegStream + kRegConv <= 512 : kRegCtl + 2 * kRegStream <= 504,
                   "register split");
     static constexpr int kOffQ = 0;
     static constexpr int kOffKv = kOffQ + 2 * kTileRows * D * 2;
     static constexpr int kOffSc = kOffKv + kSlots * kSlotB;
-    static constexpr int kOffBar = kOffSc + kScSlots * kScB;
-    // barriers: FULL, EMPTY, RAW [kSlots]; QF, SF, PF, OD [2]; TD
-    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarQf = 3 * kSlots,
-                         kBarSf = kBarQf + 2, kBarPf = kBarSf + 2, kBarOd = kBarPf + 2,
-                         kBarTd = kBarOd + 2, kNumBars = kBarTd + 1;
+    // output rows on their way from registers to coalesced stores: 32 rows x 64 bytes per warp
+    static constexpr int kOffStage = kOffSc + kScSlots * kScB;
+    static constexpr int kOffBar = kOffStage + 8 * 2048;
+    // barriers: FULL, EMPTY, RAW [kSlots]; SF, PF, OD [2]; QF, QE, TD
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarSf = 3 * kSlots,
+                         kBarPf = kBarSf + 2, kBarOd = kBarPf + 2, kBarQf = kBarOd + 2,
+                         kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmem = kOffMisc + 16 + (kThreads / 32 + 4) * 8;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -175,11 +176,12 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             mbar_init(bar(S::kBarRaw + s), 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(S::kBarQf + x), 4);
             mbar_init(bar(S::kBarSf + x), 1);
             mbar_init(bar(S::kBarPf + x), 4);
             mbar_init(bar(S::kBarOd + x), 1);
         }
+        mbar_init(bar(S::kBarQf), 1);
+        mbar_init(bar(S::kBarQe), 1);
         mbar_init(bar(S::kBarTd), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -208,11 +210,29 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             const int box_rows = page < kTk ? page : kTk;
             const int boxes = kTk / box_rows;
             uint32_t it = 0;   // slots filled
-            uint32_t tiles = 0;
+            uint32_t tiles = 0, n_q = 0;
             bool ok = true;
+            const int half = p.c.tq / 2;
             while (w < sh.w1 && ok) {
                 const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
                 const int hk = u.hs;
+                // the queries, {64 columns, heads, tokens} boxes: row r of a stream is token r / heads,
+                // head r % heads.  Rows of other sequences' tokens may come along: rows do not mix.
+                if (!mbar_wait(bar(S::kBarQe), (n_q & 1) ^ 1, abort_flag, hdr)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const int tok = u.tok0 + u.rt * p.c.tq, tok1 = tok + (u.n - u.rt * p.c.tq > half ? half : 0);
+                    mbar_expect_tx(bar(S::kBarQf), 2 * (D / 64) * half * p.c.hg * 128);
+                    for (int h = 0; h < 2 * (D / 64); ++h) {
+                        const int x = h / (D / 64), c = h % (D / 64);
+                        tma_load_3d(sbase + S::kOffQ + x * kTileRows * D * 2 + c * (128 * 128), &p.tm_q, c * 64,
+                                    hk * p.c.hg, x ? tok1 : tok, bar(S::kBarQf));
+                    }
+                }
+                ++n_q;
+                __syncwarp();
                 const int32_t* row = p.a.pages + (int64_t)u.b * p.a.d.max_pages;
                 const int pg0 = u.key0 >> p.c.page_log2;
                 const int pg1 = (int)(((int64_t)u.key1 + page - 1) >> p.c.page_log2);
@@ -270,88 +290,112 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     tile = 0;
                 }
             }
+            if (!ok && n_q) mbar_drain(bar(S::kBarQf), (n_q - 1) & 1, hdr);
             if (!ok)  // no copy may be in flight when the CTA ends
                 for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k)
                     mbar_drain(bar((S::kQuant ? S::kBarRaw : S::kBarFull) + k % kSlots), (k / kSlots) & 1, hdr);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ---------------------------------------------------------- products
+            // The whole warp follows the loop, so that its values are uniform; one thread issues.
             const uint32_t id_qk = idesc_bf16(128, kTk), id_pv = idesc_bf16_bmn(128, D);
-            uint32_t it0 = 0;    // slot index of the unit stretch's first key tile
+            const uint32_t q_lo = desc_lo_sw128(sbase + S::kOffQ), k_lo = desc_lo_sw128(sbase + S::kOffKv);
+            const uint32_t v_lo = desc_lo_sw128_mn(sbase + S::kOffKv, kTk * 128);
+            uint32_t it0 = 0;    // slot index of the stretch's first key tile
             uint32_t n_pf[2] = {0, 0}, n_q = 0;
             bool ok = true;
-            bool fresh[2];
+            bool fresh[2];       // no product in the stream's O yet
             auto wait = [&](int b, uint32_t par) {
-                if (ok) ok = mbar_wait(bar(b), par & 1, abort_flag, hdr);
+                if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), par & 1, abort_flag, hdr));
                 tc_fence_after();
                 return ok;
             };
-            // the tile's slots: K of relative tile i is the 2 i-th after it0, V the next
-            auto kslot = [&](const Stretch& s, int i) { return it0 + 2 * (uint32_t)(i - s.t0); };
+            // K of relative tile i is the slot 2 i after it0, V the next
             auto full = [&](uint32_t k) { return wait(S::kBarFull + k % kSlots, k / kSlots); };
-            auto release = [&](uint32_t k) { mma_commit(bar(S::kBarEmpty + k % kSlots)); };
+            auto release = [&](uint32_t k) {
+                if (elect_one()) mma_commit(bar(S::kBarEmpty + k % kSlots));
+                __syncwarp();
+            };
             auto qk = [&](int x, uint32_t k) {
-                const uint32_t qa = sbase + S::kOffQ + x * kTileRows * D * 2;
-                const uint32_t ka = sbase + S::kOffKv + (k % kSlots) * S::kSlotB;
+                const uint32_t a = q_lo + x * (kTileRows * D * 2 / 16), b = k_lo + (k % kSlots) * (S::kSlotB / 16);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t o = (ks / 4) * (128 * 128) + (ks % 4) * 32;
-                    mma_ss_bf16(tmem + x * 128, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), id_qk, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t o = ((ks / 4) * (128 * 128) + (ks % 4) * 32) / 16;
+                        mma_ss_lo(tmem + x * 128, a + o, b + o, id_qk, ks > 0);
+                    }
+                    mma_commit(bar(S::kBarSf + x));
                 }
-                mma_commit(bar(S::kBarSf + x));
+                __syncwarp();
             };
             auto pv = [&](int x, uint32_t k) {
-                const uint32_t va = sbase + S::kOffKv + (k % kSlots) * S::kSlotB;
+                const uint32_t b = v_lo + (k % kSlots) * (S::kSlotB / 16);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kTk / 16; ++ks)
-                    mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8,
-                           smem_desc_sw128_mn(va + ks * 16 * 128, kTk * 128), id_pv, !(fresh[x] && ks == 0));
+                    for (int ks = 0; ks < kTk / 16; ++ks)
+                        mma_ts_lo(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, b + ks * (16 * 128 / 16), id_pv,
+                                  ks > 0 || !fresh[x]);
+                }
+                __syncwarp();
                 fresh[x] = false;
             };
             while (w < sh.w1 && ok) {
                 const Stretch s = stretch(p, u, tile, sh.w1 - w);
+                auto kslot = [&](int i) { return it0 + 2 * (uint32_t)(i - s.t0); };
                 fresh[0] = fresh[1] = true;
                 // first products; a stream whose first tile comes later starts in the loop
-                full(kslot(s, s.t0));
-                for (int x = 0; x < 2 && ok; ++x) {
-                    wait(S::kBarQf + x, n_q);
-                    if (ok && s.act(x, s.t0)) qk(x, kslot(s, s.t0));
-                }
-                ++n_q;
-                if (!ok) break;
-                release(kslot(s, s.t0));
+                if (!wait(S::kBarQf, n_q++) || !full(kslot(s.t0))) break;
+                if (s.act(0, s.t0)) qk(0, kslot(s.t0));
+                if (s.act(1, s.t0)) qk(1, kslot(s.t0));
+                release(kslot(s.t0));
                 if (s.split && s.t0 + 1 < s.t1) {
-                    if (!full(kslot(s, s.t0 + 1))) break;
-                    if (s.act(1, s.t0 + 1)) qk(1, kslot(s, s.t0 + 1));
-                    release(kslot(s, s.t0 + 1));
+                    if (!full(kslot(s.t0 + 1))) break;
+                    if (s.act(1, s.t0 + 1)) qk(1, kslot(s.t0 + 1));
+                    release(kslot(s.t0 + 1));
                 }
-                for (int i = s.t0; i < s.t1 && ok; ++i) {
-                    full(kslot(s, i) + 1);
-                    for (int x = 0; x < 2 && ok; ++x) {
+                // behind the unit's last scores the place of its queries is free
+                const int stride = s.split ? 2 : 1;
+                auto queries_done = [&] {
+                    if (elect_one()) mma_commit(bar(S::kBarQe));
+                    __syncwarp();
+                };
+                if (s.t1 - s.t0 <= stride) queries_done();
+                for (int i = s.t0; i < s.t1; ++i) {
+                    if (!full(kslot(i) + 1)) break;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
                         if (s.act(x, i)) {
                             if (!wait(S::kBarPf + x, n_pf[x]++)) break;
-                            pv(x, kslot(s, i) + 1);
+                            pv(x, kslot(i) + 1);
                         }
                         if (!s.split && s.act(x, i + 1)) {
-                            if (!full(kslot(s, i + 1))) break;
-                            qk(x, kslot(s, i + 1));
+                            if (!full(kslot(i + 1))) break;
+                            qk(x, kslot(i + 1));
                         }
                     }
                     if (!ok) break;
-                    release(kslot(s, i) + 1);
+                    release(kslot(i) + 1);
                     if (!s.split && i + 1 < s.t1) {
-                        if (!full(kslot(s, i + 1))) break;
-                        release(kslot(s, i + 1));
+                        if (!full(kslot(i + 1))) break;
+                        release(kslot(i + 1));
                     } else if (s.split && i + 2 < s.t1) {
-                        if (!full(kslot(s, i + 2))) break;
+                        if (!full(kslot(i + 2))) break;
                         const int x = (i - s.t0) & 1;
-                        if (s.act(x, i + 2)) qk(x, kslot(s, i + 2));
-                        release(kslot(s, i + 2));
+                        if (s.act(x, i + 2)) {
+                            if (x) qk(1, kslot(i + 2));
+                            else qk(0, kslot(i + 2));
+                        }
+                        release(kslot(i + 2));
                     }
+                    if (i + stride == s.t1 - 1) queries_done();
                 }
                 if (!ok) break;
-                mma_commit(bar(S::kBarOd));
-                mma_commit(bar(S::kBarOd + 1));
-                it0 = kslot(s, s.t1);
+                // (only for a stream that had a tile: its warps wait for no other)
+                if (elect_one()) {
+                    if (!fresh[0]) mma_commit(bar(S::kBarOd));
+                    if (!fresh[1]) mma_commit(bar(S::kBarOd + 1));
+                }
+                __syncwarp();
+                it0 = kslot(s.t1);
                 w += s.t1 - s.t0;
                 if (w < sh.w1) {
                     next_unit(p, u);
@@ -359,7 +403,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
             if (!ok) {  // products in flight end before TMEM is given back
-                mma_commit(bar(S::kBarTd));
+                if (elect_one()) mma_commit(bar(S::kBarTd));
+                __syncwarp();
                 mbar_drain(bar(S::kBarTd), 0, hdr);
             }
         }
@@ -369,10 +414,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         const int x = warp >= 8, r = threadIdx.x - (x ? 256 : 128);
         const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
         const uint32_t ts = trow + x * 128, to = trow + 256 + x * 128;
-        // a negative scale's sign goes into the queries; never 0, so that a masked -inf stays one
+        // never 0, so that a masked -inf stays one; a negative scale turns the scores' sign
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
-        const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const bool neg = p.scale_log2 < 0.0f;
         const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
+        uint8_t* stage = smem + S::kOffStage + (warp - 4) * 2048;
         uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
         bool ok = true;
         int64_t unit0 = sh.unit0;
@@ -381,26 +427,32 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         };
         int64_t orow;       // this thread's row of out and lse: token * H + head, -1: none
         int pos, first;     // keys it sees: first .. pos
-        auto load_q = [&](const Unit& v, bool split) {
+        auto rows_of = [&](const Unit& v, bool split) {
             const int tok = v.rt * p.c.tq + (split ? 0 : x * half) + r / G, hd = v.hs * G + r % G;
             const bool live = r < half * G && tok < v.n;
             orow = live ? (int64_t)(v.tok0 + tok) * p.a.d.H + hd : -1;
             pos = live ? v.len - v.n + tok : -1;
             first = p.a.d.window ? max(0, pos - p.a.d.window + 1) : 0;
-            const uint16_t* q = p.a.q + (int64_t)(v.tok0 + tok) * p.a.ldq + hd * D;
-            uint8_t* d = smem + S::kOffQ + x * kTileRows * D * 2 + r * 128;
+        };
+        // 32 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory: each four
+        // lanes store 64 bytes of a row
+        auto put = [&](const uint32_t* e, int64_t row, int col) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 e = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0, 0, 0, 0);
-                e.x ^= flip, e.y ^= flip, e.z ^= flip, e.w ^= flip;
-                *reinterpret_cast<uint4*>(d + (c / 8) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4)) = e;
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int rr = 8 * k + (lane >> 2), c = lane & 3;
+                const int64_t to_row = __shfl_sync(0xFFFFFFFFu, row, rr);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+                if (to_row >= 0) *reinterpret_cast<uint4*>(p.a.out + to_row * D + col + 8 * c) = v;
             }
-            fence_async();
             __syncwarp();
         };
         Stretch s = stretch(p, u, tile, sh.w1 - w);
-        load_q(u, s.split);
-        if (lane == 0) mbar_arrive(bar(S::kBarQf + x));
+        rows_of(u, s.split);
         while (true) {
             const bool whole = s.t0 == 0 && s.t1 == u.tiles;
             float m = kNoMax, l = 0.0f;
@@ -445,6 +497,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
                         mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
                     }
+                }
+                if (neg) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
                 }
                 if (!(key >= inner0 && key + kTk <= inner1)) {
                     const int hi = pos - key, lo = first - key;
@@ -503,23 +559,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             const int dtiles = u.tiles;
             const bool dsplit = s.split;
             const int64_t drow = orow, dunit0 = unit0;
-            const bool more = w < sh.w1;
-            // The next unit's queries go to shared memory while the last products run (the scores
-            // that read the old ones are done), and are handed over once they are.
-            if (!any) wait(S::kBarOd + x, n_od);
-            if (more) {
-                unit0 += u.tiles;
-                next_unit(p, u);
-                s = stretch(p, u, 0, sh.w1 - w);
-                load_q(u, s.split);
-            }
-            if (any) wait(S::kBarOd + x, n_od);
-            ++n_od;
-            if (more && lane == 0) mbar_arrive(bar(S::kBarQf + x));
+            if (any) wait(S::kBarOd + x, n_od++);
             tc_fence_after();
             if (whole && !dsplit) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint16_t* out = p.a.out + drow * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -527,18 +570,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         tmem_ld_x32(to + c, o);
                         tmem_wait_ld();
                     }
-                    if (drow >= 0) {
+                    uint32_t e[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint4 e = make_uint4(0, 0, 0, 0);
-                            if (any) {
-                                const float* f = reinterpret_cast<const float*>(o) + 8 * k;
-                                e = make_uint4(bf16x2_of(f[0] * inv, f[1] * inv), bf16x2_of(f[2] * inv, f[3] * inv),
-                                               bf16x2_of(f[4] * inv, f[5] * inv), bf16x2_of(f[6] * inv, f[7] * inv));
-                            }
-                            *reinterpret_cast<uint4*>(out + c + 8 * k) = e;
-                        }
-                    }
+                    for (int k = 0; k < 16; ++k)
+                        e[k] = any ? bf16x2_of(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv) : 0u;
+                    put(e, drow, c);
                 }
                 if (drow >= 0 && p.a.lse) p.a.lse[drow] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
             } else {
@@ -609,12 +645,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                                     f[4 * e + 3] += g.w * a;
                                 }
                             }
-                        if (drow >= 0)
+                        uint32_t e[16];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4*>(p.a.out + drow * D + k0 + 8 * e) = make_uint4(
-                                    bf16x2_of(f[8 * e] * inv, f[8 * e + 1] * inv), bf16x2_of(f[8 * e + 2] * inv, f[8 * e + 3] * inv),
-                                    bf16x2_of(f[8 * e + 4] * inv, f[8 * e + 5] * inv), bf16x2_of(f[8 * e + 6] * inv, f[8 * e + 7] * inv));
+                        for (int j = 0; j < 16; ++j) e[j] = bf16x2_of(f[2 * j] * inv, f[2 * j + 1] * inv);
+                        put(e, drow, k0);
                     }
                     if (drow >= 0 && p.a.lse && (!dsplit || x == 0))
                         p.a.lse[drow] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
@@ -625,7 +659,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             // the next P V may overwrite O only after every thread of the warp has read it: P of
             // the next unit is handed over by the warp as a whole, after this point
             tc_fence_before();
-            if (!more) break;
+            if (w >= sh.w1) break;
+            unit0 += u.tiles;
+            next_unit(p, u);
+            s = stretch(p, u, 0, sh.w1 - w);
+            rows_of(u, s.split);
         }
     } else {
         // -------------------------------------------------------------- conversion
@@ -655,7 +693,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                             for (int c = 0; c < kIn; ++c) raw[c] = make_uint4(0, 0, 0, 0);
                             if (kv) reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB)[kTk + r] = 0.0f;
                         }
-                        if (S::kSyncInPlace) asm volatile("bar.sync 2, 128;" ::: "memory");
+                        if (S::kInPlace && FMT == kKvInt4) asm volatile("bar.sync 2, 128;" ::: "memory");
                         constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;  // output chunks of an input chunk
 #pragma unroll
                         for (int c = 0; c < kIn; ++c) {
@@ -714,6 +752,16 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     if (!make_kv_map(&p.tm_k, a.cache.k, a, S::kBoxB, std::min(a.d.page, kTk)) ||
         !make_kv_map(&p.tm_v, a.cache.v, a, S::kBoxB, std::min(a.d.page, kTk)))
         return cudaErrorInvalidValue;
+    {
+        // queries {D, H, T}; one token needs no token stride
+        const int64_t ld = a.d.T > 1 ? a.ldq : (int64_t)a.d.H * D;
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.d.H, (cuuint64_t)a.d.T};
+        const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTileRows / G)};
+        if (!make_map_nd(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
     const void* kern = reinterpret_cast<const void*>(&attn_tiles_kernel<FMT, D>);
     cudaError_t e = ensure_dynamic_smem(kern, S::kSmem);
     if (e != cudaSuccess) return e;

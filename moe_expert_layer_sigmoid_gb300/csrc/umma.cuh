@@ -27,12 +27,22 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
     return d;
 }
 
-// The same for an MN-major operand (rows of 64 consecutive M or N elements, 128
-// bytes, one row per K index): 8-row groups along K are 1024 B apart (SBO), the
-// next 64 elements along M or N `lbo` bytes on.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t d = smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 16);
-    return d | (uint64_t)(lbo >> 4) << 16;
+// An MN-major operand (rows of 64 consecutive M or N elements, 128 bytes, one row per K
+// index) has its 8-row groups along K 1024 B apart (SBO) and the next 64 elements along M or N
+// `lbo` bytes on.  Here come both halves, for issue loops that step through a tile by adding to the low
+// word (addresses below 256 KB never carry out of its 14 address bits): the low word for an
+// address, and the high word, the same for all.
+__device__ __forceinline__ uint32_t desc_lo_sw128(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_sw128_mn(uint32_t addr, uint32_t lbo) {
+    return (addr >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// One thread of the (converged) warp, the same each time; the compiler knows it for one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, both K-major.
@@ -72,6 +82,24 @@ __device__ __forceinline__ void mma_ss_bf16(uint32_t d_tmem, uint64_t a_desc, ui
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The bf16 forms with descriptors by their low words.
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n"
+        " mov.b64 b, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
         : "memory");
 }
 

@@ -30,6 +30,7 @@
 // Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-7 stream A, 8-11 stream B,
 // 12-15 conversion.
 #include <atomic>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "umma.cuh"
@@ -84,24 +85,34 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// (a0, a1) = (a0, a1) * (b0, b1) and (a0 * s + b, a1 * s + b) in one instruction each
+// (a0, a1) = (a0, a1) * (b0, b1), (a0 * s0 + b, a1 * s1 + b) and (a0 + b0, a1 + b1), one instruction each
 __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
     asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n"
         " mov.b64 {%0, %1}, a;\n}"
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
 }
-__device__ __forceinline__ void fma2(float& a0, float& a1, float s, float b) {
-    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 c, {%3, %3};\n"
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float b) {
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 c, {%4, %4};\n"
         " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
         : "+f"(a0), "+f"(a1)
-        : "f"(s), "f"(b));
+        : "f"(s0), "f"(s1), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
     asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
         " mov.b64 {%0, %1}, a;\n}"
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 f;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
+    return f;
 }
 __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -414,9 +425,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         const int x = warp >= 8, r = threadIdx.x - (x ? 256 : 128);
         const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
         const uint32_t ts = trow + x * 128, to = trow + 256 + x * 128;
-        // never 0, so that a masked -inf stays one; a negative scale turns the scores' sign
-        const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
+        // never 0, so that a masked score stays infinite
         const bool neg = p.scale_log2 < 0.0f;
+        const float sc = neg ? fminf(p.scale_log2, -1e-37f) : fmaxf(p.scale_log2, 1e-37f);
         const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
         uint8_t* stage = smem + S::kOffStage + (warp - 4) * 2048;
         uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
@@ -467,10 +478,6 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 const int key = (u.tile0 + i) * kTk;
                 wait(S::kBarSf + x, n_sf++);
                 tc_fence_after();
-                float v[128];
-                uint32_t* vr = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + 32 * c, vr + 32 * c);
                 if (!S::kQuant && !(s.split == false && x == 1 && s.act(0, i)) &&
                     (key < u.key0 || key + kTk > u.key1)) {
                     // keys outside [key0, key1) are nobody's: their slots may hold anything, so the
@@ -484,36 +491,46 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     }
                     fence_async();
                 }
-                const float4* ksc = nullptr;
-                if (S::kQuant) {
-                    wait(S::kBarFull + vk % kSlots, vk / kSlots);
-                    ksc = reinterpret_cast<const float4*>(smem + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB);
-                }
-                tmem_wait_ld();
-                if (S::kQuant) {
+                // the keys' scales (times sc), then the values'
+                const uint32_t ksc = sbase + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB;
+                if (S::kQuant) wait(S::kBarFull + vk % kSlots, vk / kSlots);
+                const bool inner = key >= inner0 && key + kTk <= inner1;
+                const int hi = pos - key, lo = first - key;
+                // columns 32 c .. of the scores, masked; f: their factors into the exponent's domain
+                auto scores = [&](float* v, int c, auto masked) {
+                    if constexpr (masked) {
+                        const int h = hi - 32 * c, l_ = lo - 32 * c;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float4 f = ksc[c];
-                        mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
-                        mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
+                        for (int k = 0; k < 32; ++k)
+                            if (k > h || k < l_) v[k] = neg ? INFINITY : -INFINITY;
                     }
-                }
-                if (neg) {
+                };
+                auto factor = [&](int c, int k) {  // of columns 32 c + 4 k ..
+                    return S::kQuant ? lds4(ksc + 128 * c + 16 * k) : make_float4(sc, sc, sc, sc);
+                };
+                auto row_max = [&](auto masked) {
+                    float mx = kNoMax;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t vr[32];
+                        tmem_ld_x32(ts + 32 * c, vr);
+                        tmem_wait_ld32(vr);
+                        float* v = reinterpret_cast<float*>(vr);
+                        scores(v, c, masked);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
-                }
-                if (!(key >= inner0 && key + kTk <= inner1)) {
-                    const int hi = pos - key, lo = first - key;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > hi || c < lo) v[c] = -INFINITY;
-                }
-                float mx = v[0];
-#pragma unroll
-                for (int c = 1; c < 128; ++c) mx = fmaxf(mx, v[c]);
-                mx *= sc;
-                if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
-                    const float mn = fmaxf(m, mx), a = ex2(m - mn);
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = factor(c, k);
+                            mx = max3(mx, v[4 * k] * f.x, v[4 * k + 1] * f.y);
+                            mx = max3(mx, v[4 * k + 2] * f.z, v[4 * k + 3] * f.w);
+                        }
+                    }
+                    return mx;
+                };
+                auto raise = [&] {
+                    // (a little above the largest score, so that no rounding of a product lets the exact
+                    // one in the pass come out above it)
+                    const float mx = inner ? row_max(std::false_type{}) : row_max(std::true_type{}),
+                                mn = mx > m ? mx + fabsf(mx) * 1.2e-7f : m, a = ex2(m - mn);
                     m = mn;
                     l *= a;
                     if (any) {  // P V of the tile before is done: S of this one came after it
@@ -521,33 +538,61 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32];
                             tmem_ld_x32(to + c, o);
-                            tmem_wait_ld();
+                            tmem_wait_ld32(o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
                             tmem_st_x32(to + c, o);
                         }
                     }
+                };
+                // One pass with the maximum as it stands; where a score exceeds it by 2^8 (S is still
+                // whole) the maximum is raised and the pass done once more.
+                if (!any) raise();
+                uint32_t pk[64];
+                float l0, l1;
+                auto pass = [&](auto masked) {  // the largest exponent
+                    float t0 = kNoMax, t1 = kNoMax;
+                    l0 = l1 = 0.0f;
+                    uint32_t vr[2][32];
+                    tmem_ld_x32(ts, vr[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld32(vr[c & 1]);
+                        if (c < 3) tmem_ld_x32(ts + 32 * (c + 1), vr[(c + 1) & 1]);
+                        float* v = reinterpret_cast<float*>(vr[c & 1]);
+                        scores(v, c, masked);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = factor(c, k);
+                            float* e = v + 4 * k;
+                            fma2(e[0], e[1], f.x, f.y, -m);
+                            fma2(e[2], e[3], f.z, f.w, -m);
+                            t0 = max3(t0, e[0], e[1]);
+                            t1 = max3(t1, e[2], e[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) e[j] = ex2(e[j]);
+                            add2(l0, l1, e[0], e[1]);
+                            add2(l0, l1, e[2], e[3]);
+                            if (S::kQuant) {
+                                const float4 g = lds4(ksc + 512 + 128 * c + 16 * k);
+                                mul2(e[0], e[1], g.x, g.y);
+                                mul2(e[2], e[3], g.z, g.w);
+                            }
+                            pk[16 * c + 2 * k] = bf16x2_of(e[0], e[1]);
+                            pk[16 * c + 2 * k + 1] = bf16x2_of(e[2], e[3]);
+                        }
+                    }
+                    return fmaxf(t0, t1);
+                };
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    const float t = inner ? pass(std::false_type{}) : pass(std::true_type{});
+                    if (k == 1 || !__any_sync(0xFFFFFFFFu, t > 8.0f)) break;
+                    raise();
                 }
                 any = true;
-                float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float a = v[32 * h + 2 * c], b = v[32 * h + 2 * c + 1];
-                        fma2(a, b, sc, -m);
-                        a = ex2(a);
-                        b = ex2(b);
-                        add2(l0, l1, a, b);
-                        if (S::kQuant) {
-                            const float2 f = reinterpret_cast<const float2*>(ksc + 32)[16 * h + c];
-                            mul2(a, b, f.x, f.y);
-                        }
-                        pk[c] = bf16x2_of(a, b);
-                    }
-                    tmem_st_x16(ts + 16 * h, pk);
-                }
+                tmem_st_x32(ts, pk);
+                tmem_st_x32(ts + 32, pk + 32);
                 l += l0 + l1;
                 tmem_wait_st();
                 tc_fence_before();
@@ -568,7 +613,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     uint32_t o[32];
                     if (any) {
                         tmem_ld_x32(to + c, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(o);
                     }
                     uint32_t e[16];
 #pragma unroll
@@ -592,7 +637,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     uint32_t o[32];
                     if (any) {
                         tmem_ld_x32(to + k, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(o);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0;
@@ -670,6 +715,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
         if constexpr (S::kQuant) {
             const int r = threadIdx.x - 384;  // row (key) of the tile
+            const float sc = p.scale_log2 < 0.0f ? fminf(p.scale_log2, -1e-37f) : fmaxf(p.scale_log2, 1e-37f);
+            auto key_scale = [&](float s) {  // of the scale's sign, and never 0
+                s *= sc;
+                return sc < 0.0f ? fminf(s, -1e-37f) : fmaxf(s, 1e-37f);
+            };
             uint32_t it = 0, tiles = 0;
             bool ok = true;
             while (w < sh.w1) {
@@ -688,10 +738,14 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                         for (int c = 0; c < kIn; ++c)
                             raw[c] = *reinterpret_cast<const uint4*>(slot + S::kRawOff + r * S::kRowB + ((c ^ sw) << 4));
-                        if (!seen) {  // nobody's key: its slot may hold anything
+                        // the keys' scales take the call's along (not 0: see the streams); nobody's key
+                        // may have anything in its slot
+                        float* scale = reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB) + kv * kTk + r;
+                        if (!kv) *scale = seen ? key_scale(*scale) : sc;
+                        else if (!seen) *scale = 0.0f;
+                        if (!seen) {
 #pragma unroll
                             for (int c = 0; c < kIn; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-                            if (kv) reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB)[kTk + r] = 0.0f;
                         }
                         if (S::kInPlace && FMT == kKvInt4) asm volatile("bar.sync 2, 128;" ::: "memory");
                         constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;  // output chunks of an input chunk

@@ -5,15 +5,17 @@
 // consecutive new tokens of the sequence, a head slot the query heads of one
 // key/value head that share a tile (row r of the tile is token r / hg, head
 // r % hg of the slot).  A unit walks the tiles of `tk` keys that its rows see.
-// The units' tiles, in the order sequence, row tile, head slot, key tile, form
-// one line of W tiles; CTA c of R takes tiles [c W / R, (c + 1) W / R).  So every
-// CTA gets the same share of keys whatever the lengths are, and a unit cut by
-// a border is joined from its CTAs' partial results (running maximum, sum and
-// unnormalised output).  A CTA leaves at most two partials: of the unit it
-// starts in the middle of, and of the unit it ends in the middle of, so the
-// workspace does not grow with the batch.  The CTA that arrives last at a unit
-// joins it, in CTA order, so the result does not depend on who is last.
-// Lengths are read on the device only: a captured call follows them.
+// The units, in the order sequence, row tile, head slot, form one line of
+// length W: each takes `unit_cost` places (what a unit costs besides its
+// tiles, in tiles) and then one place for each key tile; CTA c of R takes the
+// places [c W / R, (c + 1) W / R).  So every CTA gets the same share whatever
+// the lengths are, and a unit cut by a border is joined from its CTAs' partial
+// results (running maximum, sum and unnormalised output).  A CTA leaves at most
+// two partials: of the unit it starts in the middle of, and of the unit it ends
+// in the middle of, so the workspace does not grow with the batch.  The CTA
+// that arrives last at a unit joins it, in CTA order, so the result does not
+// depend on who is last.  Lengths are read on the device only: a captured call
+// follows them.
 #pragma once
 
 #include "kv.cuh"
@@ -33,7 +35,8 @@ struct AttnCut {
     int hs;        // head slots: H_kv * subs
     int tk_log2;   // keys per tile
     int page_log2;
-    int min_tiles;  // fewest tiles that a CTA is worth starting for
+    int unit_cost;  // places of a unit besides its tiles
+    int min_share;  // fewest places that a CTA is worth starting for
     // sequences with rows_lo < n * (H / H_kv) <= rows_hi are this launch's
     int64_t rows_lo, rows_hi;
 };
@@ -83,114 +86,160 @@ __device__ __forceinline__ int row_tiles(const AttnParams& p, int n) {
     return (n + p.c.tq - 1) / p.c.tq;
 }
 
-// Tiles of one sequence, over its row tiles and one head slot.
-__device__ __forceinline__ int64_t seq_tiles(const AttnParams& p, int n, int len) {
-    int64_t s = 0;
-    Unit u;
-    u.n = n;
-    u.len = len;
-    const int rts = row_tiles(p, n);
-    for (u.rt = 0; u.rt < rts; ++u.rt) {
-        unit_keys(p, u);
-        s += u.tiles;
-    }
-    return s;
-}
-
 // A CTA's share and its first unit.
 struct Share {
-    int64_t W;        // tiles of the launch
+    int64_t W;        // places of the launch
     int64_t w0, w1;   // this CTA's
-    int64_t unit0;    // index of the first unit's first tile
+    int64_t unit0;    // the first unit's first place
     int R;            // CTAs that take part
     Unit u;           // the first unit
 };
 
-__device__ __forceinline__ int64_t share_start(int64_t W, int R, int c) { return (W * c) / R; }
-// The CTA that holds tile w.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int64_t c) {
+    const int64_t n = a * b;
+    return n >> 32 == 0 && c >> 32 == 0 ? (uint32_t)n / (uint32_t)c : n / c;
+}
+// The CTA that holds place w.
 __device__ __forceinline__ int share_owner(int64_t W, int R, int64_t w) {
-    return (int)(((w + 1) * R - 1) / W);
+    const int64_t n = (w + 1) * R - 1;
+    return (int)(n >> 32 == 0 && W >> 32 == 0 ? (uint32_t)n / (uint32_t)W : n / W);
 }
 
-// Every thread of the CTA calls this; `sm` is scratch of (threads / 32 + 4) int64.
-// Sums the sequences' tiles in order (each thread a run of sequences), deals
-// the line and finds the unit that holds this CTA's first tile.
-template <int THREADS>
-__device__ Share deal(const AttnParams& p, int64_t* sm) {
-    constexpr int kWarps = THREADS / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = p.a.d.B, per = (B + THREADS - 1) / THREADS;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int tok0, n, len;
-        load_seq(p, b, tok0, n, len);
-        mine += n ? seq_tiles(p, n, len) * p.c.hs : 0;
-    }
-    int64_t incl = mine;
+// Inclusive scan over the CTA; `sm` holds a value for each warp.
+template <int THREADS, class T>
+__device__ __forceinline__ T cta_scan(T x, T* sm, T& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
+        const T v = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += v;
     }
-    if (lane == 31) sm[warp] = incl;
+    if (lane == 31) sm[warp] = x;
     __syncthreads();
-    int64_t before = 0, W = 0;
+    total = 0;
+    T before = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         if (i < warp) before += sm[i];
-        W += sm[i];
+        total += sm[i];
     }
-    before += incl - mine;
+    return before + x;
+}
+
+// Every thread of the CTA calls this; `sm` is 8-aligned scratch of deal_bytes(THREADS) that
+// nothing else uses until the CTA's next __syncthreads.  Counts the row tiles of
+// the sequences (each thread a run of sequences), then the places of the row
+// tiles (each thread a run of row tiles), deals the line and finds the unit that
+// holds this CTA's first place.
+constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 4) + 4 * threads; }
+template <int THREADS>
+__device__ Share deal(const AttnParams& p, void* scratch) {
+    constexpr int kWarps = THREADS / 32;
+    int64_t* sm = static_cast<int64_t*>(scratch);  // [warps] sums, [warps] row tiles (int), the first unit
+    int* smr = reinterpret_cast<int*>(sm + kWarps);
+    int64_t* found = sm + 2 * kWarps;
+    int* first = reinterpret_cast<int*>(found + 4);  // [threads]: row tiles before each thread's sequences
+    const int tid = threadIdx.x, B = p.a.d.B, per = (B + THREADS - 1) / THREADS;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int rts = 0;
+    Unit u;
+    for (u.b = b0; u.b < b1; ++u.b) {
+        load_seq(p, u.b, u.tok0, u.n, u.len);
+        rts += row_tiles(p, u.n);
+    }
+    int n_rt;
+    first[tid] = cta_scan<THREADS>(rts, smr, n_rt) - rts;
+    __syncthreads();
+    // this thread's row tiles [e0, e1): their sequences lie in the run of thread k and later
+    const int pe = (n_rt + THREADS - 1) / THREADS, e0 = min(n_rt, tid * pe), e1 = min(n_rt, e0 + pe);
+    int k = 0;
+#pragma unroll
+    for (int step = THREADS >= 512 ? 256 : THREADS >= 256 ? 256 : 128; step; step >>= 1)
+        if (k + step < THREADS && first[k + step] <= e0) k += step;
+    auto seek = [&] {  // u to row tile e0
+        u.b = k * per;
+        u.rt = e0 - first[k];
+        load_seq(p, u.b, u.tok0, u.n, u.len);
+        for (int r; u.rt >= (r = row_tiles(p, u.n));) {
+            u.rt -= r;
+            load_seq(p, ++u.b, u.tok0, u.n, u.len);
+        }
+    };
+    auto step = [&] {
+        if (++u.rt < row_tiles(p, u.n)) return;
+        u.rt = 0;
+        do {
+            if (++u.b >= B) return;
+            load_seq(p, u.b, u.tok0, u.n, u.len);
+        } while (u.n == 0);
+    };
+    auto places = [&] {
+        unit_keys(p, u);
+        return (int64_t)(u.tiles + p.c.unit_cost) * p.c.hs;
+    };
+    int64_t mine = 0, W;
+    if (e0 < e1) {
+        seek();
+        for (int e = e0;;) {
+            mine += places();
+            if (++e == e1) break;
+            step();
+        }
+    }
+    int64_t before = cta_scan<THREADS>(mine, sm, W) - mine;
     Share s;
     s.W = W;
-    s.R = (int)min((int64_t)gridDim.x, max((int64_t)1, W / p.c.min_tiles));
+    s.R = (int)min((int64_t)gridDim.x, max((int64_t)1, W / p.c.min_share));
     const bool idle = (int)blockIdx.x >= s.R || W == 0;
-    s.w0 = idle ? 0 : share_start(W, s.R, blockIdx.x);
-    s.w1 = idle ? 0 : share_start(W, s.R, blockIdx.x + 1);
+    s.w0 = idle ? 0 : mul_div(W, blockIdx.x, s.R);
+    s.w1 = idle ? 0 : mul_div(W, blockIdx.x + 1, s.R);
     if (!idle && s.w0 >= before && s.w0 < before + mine) {
-        for (int b = b0; b < b1; ++b) {
-            int tok0, n, len;
-            load_seq(p, b, tok0, n, len);
-            const int64_t t = n ? seq_tiles(p, n, len) * p.c.hs : 0;
-            if (s.w0 < before + t) {
-                sm[kWarps] = b;
-                sm[kWarps + 1] = before;
-                break;
-            }
+        seek();
+        for (int64_t t; s.w0 >= before + (t = places());) {
             before += t;
+            step();
         }
+        found[0] = u.b;
+        found[1] = u.rt;
+        found[2] = before;
     }
     __syncthreads();
     if (!idle) {
-        Unit& u = s.u;
-        u.b = (int)sm[kWarps];
-        int64_t at = sm[kWarps + 1];
-        load_seq(p, u.b, u.tok0, u.n, u.len);
-        for (u.rt = 0;; ++u.rt) {
-            unit_keys(p, u);
-            const int64_t t = (int64_t)u.tiles * p.c.hs;
-            if (s.w0 < at + t || u.rt + 1 >= row_tiles(p, u.n)) break;
-            at += t;
-        }
-        u.hs = (int)((s.w0 - at) / u.tiles);
-        s.unit0 = at + (int64_t)u.hs * u.tiles;
+        s.u.b = (int)found[0];
+        s.u.rt = (int)found[1];
+        load_seq(p, s.u.b, s.u.tok0, s.u.n, s.u.len);
+        unit_keys(p, s.u);
+        const int each = s.u.tiles + p.c.unit_cost;
+        const int64_t off = s.w0 - found[2];
+        s.u.hs = (int)(off >> 31 == 0 ? (uint32_t)off / (uint32_t)each : off / each);
+        s.unit0 = found[2] + (int64_t)s.u.hs * each;
     }
     return s;
 }
 
-// The unit after u (which is not the launch's last).
-__device__ __forceinline__ void next_unit(const AttnParams& p, Unit& u) {
-    if (++u.hs < p.c.hs) return;
+// The tiles [t0, t1) of unit u (whose first place is unit0) that are in this CTA's share.
+__device__ __forceinline__ void unit_share(const AttnParams& p, const Share& s, const Unit& u,
+                                           int64_t unit0, int& t0, int& t1) {
+    const int64_t at = unit0 + p.c.unit_cost;
+    t0 = (int)max((int64_t)0, s.w0 - at);
+    t1 = (int)max((int64_t)0, min((int64_t)u.tiles, s.w1 - at));
+}
+
+// Moves u and unit0 on; false if no tile of the next unit is in the share.
+__device__ __forceinline__ bool next_unit(const AttnParams& p, const Share& s, Unit& u, int64_t& unit0) {
+    unit0 += u.tiles + p.c.unit_cost;
+    if (unit0 + p.c.unit_cost >= s.w1) return false;
+    if (++u.hs < p.c.hs) return true;
     u.hs = 0;
     if (++u.rt >= row_tiles(p, u.n)) {
         u.rt = 0;
         do {
-            if (++u.b >= p.a.d.B) return;
+            if (++u.b >= p.a.d.B) return false;
             load_seq(p, u.b, u.tok0, u.n, u.len);
         } while (u.n == 0);
     }
     unit_keys(p, u);
+    return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -102,7 +102,7 @@ struct RowsShape {
     static constexpr int kOffMl = kOffJoin + kRows * D * 4;
     static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
-    static constexpr int kSmem = kOffMisc + 128;
+    static constexpr int kSmem = kOffMisc + 16;
     static_assert(kSmem <= 115712, "two CTAs share an SM's shared memory");
 };
 
@@ -142,8 +142,9 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const Share sh = deal<kRowsThreads>(p, reinterpret_cast<int64_t*>(smem + S::kOffMisc + 16));
+    const Share sh = deal<kRowsThreads>(p, smem);
     if (sh.w0 >= sh.w1) return;
+    __syncthreads();
     WsHeader* hdr = p.a.hdr;
 
     if (warp == 4) {
@@ -152,13 +153,13 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         const int box_rows = page < S::kTk ? page : S::kTk;
         const int boxes = S::kTk / box_rows;     // boxes of a tile: one per page, or one
         Unit u = sh.u;
-        int64_t w = sh.w0;
-        int tile = (int)(w - sh.unit0);
+        int64_t unit0 = sh.unit0;
         uint32_t it = 0;
         bool ok = true;
         int ids = 0, ids_next = 0, ids_at = -1;  // 32 page ids from page ids_at on
-        while (w < sh.w1 && ok) {
-            const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
+        do {
+            int tile, end;
+            unit_share(p, sh, u, unit0, tile, end);
             const int hk = u.hs / p.c.subs;
             const int32_t* row = p.a.pages + (int64_t)u.b * p.a.d.max_pages;
             const int pg0 = u.key0 >> p.c.page_log2;
@@ -168,7 +169,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 return i >= pg0 && i < pg1 ? __ldg(row + i) : 0;
             };
             ids_at = -1;
-            for (; tile < end; ++tile, ++w, ++it) {
+            for (; tile < end; ++tile, ++it) {
                 const int s = it % S::kStages;
                 const int key = (u.tile0 + tile) * S::kTk;
                 const int pg = key >> p.c.page_log2;  // first page of the tile
@@ -214,11 +215,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 }
                 __syncwarp();
             }
-            if (w < sh.w1 && ok) {
-                next_unit(p, u);
-                tile = 0;
-            }
-        }
+        } while (ok && next_unit(p, sh, u, unit0));
         // after an abort: no copy may be in flight when the CTA ends
         if (!ok)
             for (uint32_t k = it > S::kStages ? it - S::kStages : 0; k < it; ++k)
@@ -231,15 +228,16 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kSteps = D / 16;              // k16 steps of a score
     constexpr int kNk = S::kKw / 8;             // key tiles of a warp
     Unit u = sh.u;
-    int64_t w = sh.w0, unit0 = sh.unit0;
-    int tile = (int)(w - unit0);
+    int64_t unit0 = sh.unit0;
     uint32_t it = 0;
     bool ok = true;
     const float sc = p.scale_log2;
     float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
     float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);  // [warp][row]: maximum, sum
-    while (w < sh.w1) {
-        const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
+    do {
+        int tile, end;
+        unit_share(p, sh, u, unit0, tile, end);
+        if (tile >= end) continue;
         const bool whole = tile == 0 && end == u.tiles;
         // the lane's two rows
         RowInfo ri;
@@ -289,7 +287,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         const int inner0 = p.a.d.window ? max(0, u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - p.a.d.window) : 0;
         const int inner1 = u.len - u.n + u.rt * p.c.tq + 1;  // [inner0, inner1)
 
-        for (; tile < end; ++tile, ++w, ++it) {
+        for (; tile < end; ++tile, ++it) {
             const int s = it % S::kStages;
             // once a wait gave up the flag is set; the warps then run on without waiting, in step
             // with each other, to the end
@@ -503,8 +501,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         bool write = whole;
         if (!whole) {
             // a partial result: slot 0 of a CTA for a unit that an earlier CTA began, else slot 1
-            const int c = blockIdx.x, c0 = share_owner(sh.W, sh.R, unit0);
-            const int c1 = share_owner(sh.W, sh.R, unit0 + u.tiles - 1);
+            const int c = blockIdx.x, c0 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost);
+            const int c1 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost + u.tiles - 1);
             constexpr int kPart = kRows * D + 2 * kRows;
             if (warp == 0) {
                 float* part = p.part + (int64_t)(2 * c + (c == c0)) * kPart;
@@ -585,12 +583,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                     p.a.lse[ri.q[i]] = L[i] > 0.0f ? (M[i] + log2f(L[i])) * kLn2 : -INFINITY;
             }
         }
-        if (w < sh.w1) {
-            unit0 += u.tiles;
-            next_unit(p, u);
-            tile = 0;
-        }
-    }
+    } while (next_unit(p, sh, u, unit0));
 }
 
 template <int FMT, int D>
@@ -606,7 +599,8 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     p.c.hs = a.d.H_kv * p.c.subs;
     p.c.tk_log2 = S::kTk == 128 ? 7 : 6;
     p.c.page_log2 = __builtin_ctz(a.d.page);
-    p.c.min_tiles = 1;
+    p.c.unit_cost = 1;
+    p.c.min_share = 2;
     p.c.rows_lo = rows_lo;
     p.c.rows_hi = rows_hi;
     p.part = part;

@@ -66,19 +66,20 @@ struct TilesShape {
     static constexpr int kOffSc = kOffKv + kSlots * kSlotB;
     // output rows on their way from registers to coalesced stores: 32 rows x 64 bytes per warp
     static constexpr int kOffStage = kOffSc + kScSlots * kScB;
-    static constexpr int kOffBar = kOffStage + 8 * 2048;
+    static constexpr int kOffMl = kOffStage + 8 * 2048;  // the streams' maxima and sums, for their join
+    static constexpr int kOffBar = kOffMl + 2 * kTileRows * 8;
     // barriers: FULL, EMPTY, RAW [kSlots]; SF, PF, OD [2]; QF, QE, TD
     static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarSf = 3 * kSlots,
                          kBarPf = kBarSf + 2, kBarOd = kBarPf + 2, kBarQf = kBarOd + 2,
                          kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kSmem = kOffMisc + 16 + (kThreads / 32 + 4) * 8;
+    static constexpr int kSmem = kOffMisc + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
     // a partial result: both streams' rows, O as float4 columns of 128 rows, then maximum and sum
     static constexpr int kPartStream = kTileRows * D + 2 * kTileRows;
     static constexpr int kPart = 2 * kPartStream;
 };
-constexpr int kPartSlots = 3;  // per CTA: a unit begun before, a unit ended after, a unit of its own
+constexpr int kPartSlots = 2;  // per CTA: a unit begun before, a unit ended after
 
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     uint32_t r;
@@ -149,10 +150,9 @@ struct Stretch {
     }
 };
 
-__device__ __forceinline__ Stretch stretch(const AttnParams& p, const Unit& u, int tile, int64_t left) {
+__device__ __forceinline__ Stretch stretch(const AttnParams& p, const Share& sh, const Unit& u, int64_t unit0) {
     Stretch s;
-    s.t0 = tile;
-    s.t1 = (int)min((int64_t)u.tiles, tile + left);
+    unit_share(p, sh, u, unit0, s.t0, s.t1);
     const int half = p.c.tq / 2, i0 = u.rt * p.c.tq, have = min(p.c.tq, u.n - i0);
     s.split = have <= half;
 #pragma unroll
@@ -197,7 +197,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const Share sh = deal<S::kThreads>(p, reinterpret_cast<int64_t*>(smem + S::kOffMisc + 16));
+    const Share sh = deal<S::kThreads>(p, smem);
     if (sh.w0 >= sh.w1) return;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -210,8 +210,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     Unit u = sh.u;
-    int64_t w = sh.w0;
-    int tile = (int)(w - sh.unit0);
+    int64_t unit0 = sh.unit0;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegCtl));
@@ -224,8 +223,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             uint32_t tiles = 0, n_q = 0;
             bool ok = true;
             const int half = p.c.tq / 2;
-            while (w < sh.w1 && ok) {
-                const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
+            do {
+                int tile, end;
+                unit_share(p, sh, u, unit0, tile, end);
+                if (tile >= end) continue;
                 const int hk = u.hs;
                 // the queries, {64 columns, heads, tokens} boxes: row r of a stream is token r / heads,
                 // head r % heads.  Rows of other sequences' tokens may come along: rows do not mix.
@@ -252,7 +253,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     return i >= pg0 && i < pg1 ? __ldg(row + i) : 0;
                 };
                 int ids = 0, ids_next = 0, ids_at = -1;  // 32 page ids from page ids_at on
-                for (; tile < end && ok; ++tile, ++w, ++tiles) {
+                for (; tile < end && ok; ++tile, ++tiles) {
                     const int key = (u.tile0 + tile) * kTk;
                     const int pg = key >> p.c.page_log2;
                     if (ids_at < 0 || pg >= ids_at + 32) {
@@ -296,11 +297,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         __syncwarp();
                     }
                 }
-                if (w < sh.w1 && ok) {
-                    next_unit(p, u);
-                    tile = 0;
-                }
-            }
+            } while (ok && next_unit(p, sh, u, unit0));
             if (!ok && n_q) mbar_drain(bar(S::kBarQf), (n_q - 1) & 1, hdr);
             if (!ok)  // no copy may be in flight when the CTA ends
                 for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k)
@@ -349,8 +346,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
                 fresh[x] = false;
             };
-            while (w < sh.w1 && ok) {
-                const Stretch s = stretch(p, u, tile, sh.w1 - w);
+            do {
+                const Stretch s = stretch(p, sh, u, unit0);
+                if (s.t0 >= s.t1) continue;
                 auto kslot = [&](int i) { return it0 + 2 * (uint32_t)(i - s.t0); };
                 fresh[0] = fresh[1] = true;
                 // first products; a stream whose first tile comes later starts in the loop
@@ -377,6 +375,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         if (s.act(x, i)) {
                             if (!wait(S::kBarPf + x, n_pf[x]++)) break;
                             pv(x, kslot(i) + 1);
+                            if (!s.act(x, i + stride)) {  // the stream's output of the unit is whole
+                                if (elect_one()) mma_commit(bar(S::kBarOd + x));
+                                __syncwarp();
+                            }
                         }
                         if (!s.split && s.act(x, i + 1)) {
                             if (!full(kslot(i + 1))) break;
@@ -400,19 +402,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     if (i + stride == s.t1 - 1) queries_done();
                 }
                 if (!ok) break;
-                // (only for a stream that had a tile: its warps wait for no other)
-                if (elect_one()) {
-                    if (!fresh[0]) mma_commit(bar(S::kBarOd));
-                    if (!fresh[1]) mma_commit(bar(S::kBarOd + 1));
-                }
-                __syncwarp();
                 it0 = kslot(s.t1);
-                w += s.t1 - s.t0;
-                if (w < sh.w1) {
-                    next_unit(p, u);
-                    tile = 0;
-                }
-            }
+            } while (next_unit(p, sh, u, unit0));
             if (!ok) {  // products in flight end before TMEM is given back
                 if (elect_one()) mma_commit(bar(S::kBarTd));
                 __syncwarp();
@@ -430,9 +421,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         const float sc = neg ? fminf(p.scale_log2, -1e-37f) : fmaxf(p.scale_log2, 1e-37f);
         const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
         uint8_t* stage = smem + S::kOffStage + (warp - 4) * 2048;
+        float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
         uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
         bool ok = true;
-        int64_t unit0 = sh.unit0;
         auto wait = [&](int b, uint32_t par) {  // once a wait gave up the streams run on, in step
             if (ok) ok = mbar_wait(bar(b), par & 1, abort_flag, hdr);
         };
@@ -462,9 +453,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             }
             __syncwarp();
         };
-        Stretch s = stretch(p, u, tile, sh.w1 - w);
-        rows_of(u, s.split);
-        while (true) {
+        do {
+            const Stretch s = stretch(p, sh, u, unit0);
+            if (s.t0 >= s.t1) continue;
+            rows_of(u, s.split);
             const bool whole = s.t0 == 0 && s.t1 == u.tiles;
             float m = kNoMax, l = 0.0f;
             bool any = false;
@@ -499,10 +491,13 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 // columns 32 c .. of the scores, masked; f: their factors into the exponent's domain
                 auto scores = [&](float* v, int c, auto masked) {
                     if constexpr (masked) {
-                        const int h = hi - 32 * c, l_ = lo - 32 * c;
+                        // bit k: column 32 c + k is seen
+                        const int h = hi - 32 * c, g = lo - 32 * c;
+                        const uint32_t see = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1) &
+                                             (g <= 0 ? ~0u : g > 31 ? 0u : ~0u << g);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (k > h || k < l_) v[k] = neg ? INFINITY : -INFINITY;
+                            if (!(see >> k & 1)) v[k] = neg ? INFINITY : -INFINITY;
                     }
                 };
                 auto factor = [&](int c, int k) {  // of columns 32 c + 4 k ..
@@ -600,116 +595,149 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 if (lane == 0) mbar_arrive(bar(S::kBarPf + x));
             }
             tiles0 += s.t1 - s.t0;
-            w += s.t1 - s.t0;
-            const int dtiles = u.tiles;
-            const bool dsplit = s.split;
-            const int64_t drow = orow, dunit0 = unit0;
             if (any) wait(S::kBarOd + x, n_od++);
             tc_fence_after();
-            if (whole && !dsplit) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    if (any) {
-                        tmem_ld_x32(to + c, o);
-                        tmem_wait_ld32(o);
-                    }
-                    uint32_t e[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        e[k] = any ? bf16x2_of(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv) : 0u;
-                    put(e, drow, c);
-                }
-                if (drow >= 0 && p.a.lse) p.a.lse[drow] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-            } else {
-                // a partial result of each stream; the CTA that completes the unit joins them
-                const int c = blockIdx.x;
-                const int c0 = whole ? c : share_owner(sh.W, sh.R, dunit0);
-                const int c1 = whole ? c : share_owner(sh.W, sh.R, dunit0 + dtiles - 1);
-                auto part = [&](int k, int y) {
-                    const int slot = whole ? 2 : k == c0;
-                    return p.part + ((int64_t)kPartSlots * k + slot) * S::kPart + y * S::kPartStream;
-                };
-                float4* po = reinterpret_cast<float4*>(part(c, x));
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    uint32_t o[32];
-                    if (any) {
-                        tmem_ld_x32(to + k, o);
-                        tmem_wait_ld32(o);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0;
-                    }
-                    const float* f = reinterpret_cast<const float*>(o);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        __stcg(po + (k / 4 + e) * kTileRows + r, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
-                }
-                __stcg(reinterpret_cast<float2*>(part(c, x) + kTileRows * D) + r, make_float2(m, l));
-                __threadfence();
+            // The CTA's own result of the stretch: the stream's, or (one row tile) both streams', of
+            // which each warpgroup takes half of the columns.
+            constexpr int kCw = D / 2;  // columns at a time
+            const int cb = s.split ? x * kCw : 0, ce = s.split ? cb + kCw : D;
+            float M = m, L = l, a0 = 1.0f, a1 = 0.0f;
+            bool use0 = any, use1 = false;
+            uint32_t o0 = to, o1 = to;
+            if (s.split) {
+                ml[x * kTileRows + r] = make_float2(m, l);
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (threadIdx.x == 128) {
-                    const bool last = whole || atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-                    if (last && !whole) p.counters[c0] = 0;
-                    *last_flag = last;
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (*last_flag) {
-                    __threadfence();
-                    // two row tiles: each stream joins its own rows; one: each takes half of the columns
-                    const int y0 = dsplit ? 0 : x, y1 = dsplit ? 1 : x;
-                    float M = kNoMax, L = 0.0f;
-                    for (int k = c0; k <= c1; ++k)
-                        for (int y = y0; y <= y1; ++y)
-                            M = fmaxf(M, __ldcg(&(reinterpret_cast<const float2*>(part(k, y) + kTileRows * D) + r)->x));
-                    for (int k = c0; k <= c1; ++k)
-                        for (int y = y0; y <= y1; ++y) {
-                            const float2 e = __ldcg(reinterpret_cast<const float2*>(part(k, y) + kTileRows * D) + r);
-                            L += e.y * ex2(e.x - M);
-                        }
-                    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                    const int cb = dsplit ? x * (D / 2) : 0, ce = dsplit ? cb + D / 2 : D;
-#pragma unroll 1
-                    for (int k0 = cb; k0 < ce; k0 += 32) {
-                        float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = 0.0f;
-#pragma unroll 1
-                        for (int k = c0; k <= c1; ++k)
-                            for (int y = y0; y <= y1; ++y) {
-                                const float* q = part(k, y);
-                                const float a = ex2(__ldcg(&(reinterpret_cast<const float2*>(q + kTileRows * D) + r)->x) - M);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float4 g = __ldcg(reinterpret_cast<const float4*>(q) + (k0 / 4 + e) * kTileRows + r);
-                                    f[4 * e] += g.x * a;
-                                    f[4 * e + 1] += g.y * a;
-                                    f[4 * e + 2] += g.z * a;
-                                    f[4 * e + 3] += g.w * a;
-                                }
-                            }
-                        uint32_t e[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) e[j] = bf16x2_of(f[2 * j] * inv, f[2 * j + 1] * inv);
-                        put(e, drow, k0);
-                    }
-                    if (drow >= 0 && p.a.lse && (!dsplit || x == 0))
-                        p.a.lse[drow] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
-                }
-                // the flag and the CTA's own slot are free for the next unit
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                tc_fence_after();
+                const float2 e0 = ml[r], e1 = ml[kTileRows + r];
+                M = fmaxf(e0.x, e1.x);
+                a0 = ex2(e0.x - M);
+                a1 = ex2(e1.x - M);
+                L = e0.y * a0 + e1.y * a1;
+                use0 = s.act(0, s.t0);
+                use1 = s.act(1, s.t0 + 1);
+                o0 = trow + 256;
+                o1 = trow + 384;
             }
-            // the next P V may overwrite O only after every thread of the warp has read it: P of
-            // the next unit is handed over by the warp as a whole, after this point
+            auto own = [&](int col, float* f) {  // columns col .. col + 31, unnormalised
+                uint32_t o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = 0.0f;
+                if (use0) {  // (the same for the whole warp: it goes by the stretch, not by a row's values)
+                    tmem_ld_x32(o0 + col, o);
+                    tmem_wait_ld32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * a0;
+                }
+                if (use1) {
+                    tmem_ld_x32(o1 + col, o);
+                    tmem_wait_ld32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * a1;
+                }
+            };
+            auto finish = [&](const float* f, int col, float inv) {
+                uint32_t e[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) e[k] = bf16x2_of(f[2 * k] * inv, f[2 * k + 1] * inv);
+                put(e, orow, col);
+            };
+            bool join = false;
+            const int c = blockIdx.x;
+            int c0 = c, c1 = c;
+            if (!whole) {
+                // A partial result; the CTA that comes last to the unit joins them.  If the others
+                // have all come its own need not go through memory.
+                c0 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost);
+                c1 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost + u.tiles - 1);
+                const unsigned others = c1 - c0;
+                unsigned* arrived = p.counters + c0;
+                if (threadIdx.x == 128) {
+                    unsigned n;
+                    asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
+                    *last_flag = n == others;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                join = *last_flag;
+                if (!join) {
+                    float* part = p.part + ((int64_t)kPartSlots * c + (c == c0)) * S::kPart + (s.split ? 0 : x) * S::kPartStream;
+                    float4* po = reinterpret_cast<float4*>(part);
+#pragma unroll 1
+                    for (int col = cb; col < ce; col += 32) {
+                        float f[32];
+                        own(col, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(po + (col / 4 + e) * kTileRows + r, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
+                    }
+                    if (!s.split || x == 0) __stcg(reinterpret_cast<float2*>(part + kTileRows * D) + r, make_float2(M, L));
+                    __threadfence();
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    if (threadIdx.x == 128) *last_flag = atomicAdd(arrived, 1u) == others;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    join = *last_flag;
+                }
+                if (join) {
+                    __threadfence();
+                    if (threadIdx.x == 128) *arrived = 0;
+                }
+            }
+            if (whole) {
+                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+                for (int col = cb; col < ce; col += 32) {
+                    float f[32];
+                    own(col, f);
+                    finish(f, col, inv);
+                }
+            } else if (join) {
+                auto part = [&](int k) {
+                    return p.part + ((int64_t)kPartSlots * k + (k == c0)) * S::kPart + (s.split ? 0 : x) * S::kPartStream;
+                };
+                auto stat = [&](int k) {  // maximum and sum of part k
+                    return k == c ? make_float2(M, L) : __ldcg(reinterpret_cast<const float2*>(part(k) + kTileRows * D) + r);
+                };
+                float Mj = kNoMax, Lj = 0.0f;
+#pragma unroll 4
+                for (int k = c0; k <= c1; ++k) Mj = fmaxf(Mj, stat(k).x);
+#pragma unroll 4
+                for (int k = c0; k <= c1; ++k) {
+                    const float2 e = stat(k);
+                    Lj += e.y * ex2(e.x - Mj);
+                }
+                const float inv = Lj > 0.0f ? 1.0f / Lj : 0.0f;
+#pragma unroll 1
+                for (int col = cb; col < ce; col += 32) {
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = 0.0f;
+#pragma unroll 1
+                    for (int k = c0; k <= c1; ++k) {
+                        const float a = ex2(stat(k).x - Mj);
+                        float g[32];
+                        if (k == c) own(col, g);
+                        else {
+                            const float4* q = reinterpret_cast<const float4*>(part(k)) + (col / 4) * kTileRows + r;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = __ldcg(q + e * kTileRows);
+                                g[4 * e] = v.x, g[4 * e + 1] = v.y, g[4 * e + 2] = v.z, g[4 * e + 3] = v.w;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] += g[e] * a;
+                    }
+                    finish(f, col, inv);
+                }
+                M = Mj;
+                L = Lj;
+            }
+            if ((whole || join) && orow >= 0 && p.a.lse && (!s.split || x == 0))
+                p.a.lse[orow] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            // Both streams may have read both outputs, and the flags: the next unit's products (which
+            // wait for P of its first tiles) and flags come after this point.
             tc_fence_before();
-            if (w >= sh.w1) break;
-            unit0 += u.tiles;
-            next_unit(p, u);
-            s = stretch(p, u, 0, sh.w1 - w);
-            rows_of(u, s.split);
-        }
+            if (s.split || !whole) asm volatile("bar.sync 1, 256;" ::: "memory");
+        } while (next_unit(p, sh, u, unit0));
     } else {
         // -------------------------------------------------------------- conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
@@ -722,9 +750,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             };
             uint32_t it = 0, tiles = 0;
             bool ok = true;
-            while (w < sh.w1) {
-                const int end = (int)min((int64_t)u.tiles, tile + (sh.w1 - w));
-                for (; tile < end; ++tile, ++w, ++tiles) {
+            do {
+                int tile, end;
+                unit_share(p, sh, u, unit0, tile, end);
+                for (; tile < end; ++tile, ++tiles) {
                     const int key = (u.tile0 + tile) * kTk + r;
                     const bool seen = key >= u.key0 && key < u.key1;
 #pragma unroll 1
@@ -769,11 +798,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         if (lane == 0) mbar_arrive(bar(S::kBarFull + sl));
                     }
                 }
-                if (w < sh.w1) {
-                    next_unit(p, u);
-                    tile = 0;
-                }
-            }
+            } while (next_unit(p, sh, u, unit0));
         }
     }
     __syncwarp();
@@ -797,7 +822,8 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     p.c.hs = a.d.H_kv;
     p.c.tk_log2 = 7;
     p.c.page_log2 = __builtin_ctz(a.d.page);
-    p.c.min_tiles = 1;
+    p.c.unit_cost = 2;
+    p.c.min_share = 3;
     p.c.rows_lo = rows_lo;
     p.c.rows_hi = rows_hi;
     p.part = part;

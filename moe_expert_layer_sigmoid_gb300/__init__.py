@@ -167,7 +167,8 @@ def _ptr(t):
 
 
 # 16-bit float patterns may travel as int16 or as the matching torch dtype
-_ALIASES = {torch.int16: (torch.int16, torch.bfloat16, torch.float16)}
+_BITS16 = (torch.int16, torch.bfloat16, torch.float16)
+_ALIASES = {torch.int16: _BITS16}
 
 
 def _dev(t: torch.Tensor, dtype, name: str):
@@ -181,8 +182,11 @@ def _dev(t: torch.Tensor, dtype, name: str):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The raw stream: the current device's current one, or that of a torch stream.  (Read without
+    building a torch.cuda.Stream, which takes 3 us on the GB300's host cores, against 0.3 us.)"""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def w4(q: torch.Tensor, s: torch.Tensor) -> W4:
@@ -467,19 +471,22 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor | None = None,
 
 
 def _kv_check(dims: KvDims, cache: Kv):
-    if cache.shape is not None and (
-            cache.shape != (dims.n_pages, dims.H_kv, dims.page, _kv_row(dims.format, dims.D)) or
-            cache.dtype not in _KV_DTYPES.get(dims.format, (cache.dtype,))):
+    if cache.shape is None:  # made from raw pointers
+        return
+    fmt = dims.format
+    if (cache.shape != (dims.n_pages, dims.H_kv, dims.page, _kv_row(fmt, dims.D)) or
+            (fmt in _KV_DTYPES and cache.dtype not in _KV_DTYPES[fmt])):
         raise ValueError("the cache's shape or type is not that of dims")
 
 
 def _rows(t: torch.Tensor, T: int, H: int, D: int, name: str):
     """Pointer and token stride of bf16 [T][H][D] whose tokens may lie apart."""
-    if not t.is_cuda or t.dtype not in _ALIASES[torch.int16]:
+    if not t.is_cuda or t.dtype not in _BITS16:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    ld, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.shape != (T, H, D) or one != 1 or (head != D and H > 1):
         raise ValueError(f"{name} must be [T][H][D] with contiguous tokens, got {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), ld if T > 1 else H * D
 
 
 def _ints(t: torch.Tensor, n: int, name: str):

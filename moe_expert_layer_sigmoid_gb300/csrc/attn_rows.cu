@@ -1,31 +1,35 @@
-// Attention of few rows: decode steps and short drafts, 16 rows (tokens x query
-// heads of one key/value head) per unit.
+// Attention of few rows: decode steps and short drafts, 8 or 16 rows (tokens x
+// query heads of one key/value head) per unit.
 //
-// Each cached byte is used for 16 rows only, so the kernel is bound by the
-// cache's bytes from HBM: the design keeps copies in flight and the work per byte small.
-// A CTA is four warps of compute and one that issues TMA copies into a ring of
-// stages, two CTAs per SM.  Every warp takes its own quarter of a stage's
-// keys through scores, softmax and values with no exchange with the others;
-// the warps' (maximum, sum, output) are joined once per unit.
+// Each cached byte is used for few rows only, so the floor is the cache's bytes
+// from HBM; what stands in the way is the work per byte in the SM, so the design keeps
+// copies in flight and that work small.  A CTA is four warps of compute and one that issues
+// TMA copies into a ring of stages, three CTAs per SM (two with 16 rows).  Every
+// warp takes its own quarter of a stage's keys through scores, softmax and values
+// with no exchange with the others; the warps' (maximum, sum, output) are joined once
+// per unit.
 //
-// Products run on the warp-level tensor cores, m16n8k16 with bf16 operands:
-//   S[16 x 8 keys]  += Q[16 x 16 of D] K^T     K from shared memory by ldmatrix
-//   O[16 x 8 of D]  += P[16 x 16 keys] V       P straight from S's registers,
-//                                             V by ldmatrix.trans
-// Codes are turned into bf16 in registers.  A contraction may run in any
-// order, so the k index is permuted to whatever order the unpacking leaves:
-// ldmatrix hands lane (g, t) four bytes of key g, which for E4M3 are elements
-// 4t .. 4t+3 (bytes 0, 2 and 1, 3 become the two register pairs of a k16
-// step), for int4 elements 8t .. 8t+7 (nibble i with nibble i + 4); the query
-// fragments are loaded in that order.  For values the transposed load gives
-// each lane the same bytes of keys 2t and 2t+1, the pairing the B operand
-// needs, and the permutation falls on the output columns.
-// The key scales multiply the scores and the value scales the weights, so the
-// codes enter the products exactly.
+// Products run on the warp-level tensor cores, m16n8k16, keys (and output columns) along
+// the 16 and the few rows along the 8, so that no product is spent on rows that are not there:
+//   S^T[16 keys x 8 rows] += K[16 keys x 16 of D] Q^T      K by ldmatrix
+//   O^T[16 of D x 8 rows] += V^T[16 of D x 16 keys] P^T    V by ldmatrix.trans, P^T from S^T's
+//                                                          registers by movmatrix
+// The key scales multiply the scores and the value scales the weights, so codes enter the
+// products exactly.  They are turned into operands in registers; a contraction may run in
+// any order, so the k index (and for values the order of the output columns) is
+// permuted to whatever the unpacking leaves:
+//   E4M3 keys: f16 by the conversion of two codes; the query row is scaled by the power of two
+//     that puts its largest element at 2^14, where f16 holds every bf16 down to 2^-28 of it.
+//   int4 keys: the nibble n + 8 alone is the f16 subnormal (n + 8) 2^-24 (2^-20 four bits up):
+//     one mask each, the queries take the other scale and the accumulators start at -8 sum q.
+//   E4M3 values: sign and the seven other bits, moved four down, are the bf16 of 2^-120 times the
+//     value; the weights take 2^112 along, less a power of two above the largest value scale so far
+//     (raised like the maximum), so that they stay in range.  Weights need bf16's range.
+//   int4 values: 128 + (n + 8) by its bits, less 136.
 //
-// The running maximum is only raised when some score exceeds it by 2^8: a
-// warp vote decides, and most tiles need neither the shuffles nor the rescaling
-// of the output.  Weights stay below 2^8 and the sums are fp32, so nothing is lost.
+// The running maximum is only raised when some score exceeds it by 2^8: a warp vote decides, and
+// most tiles need neither the shuffles nor the rescaling of the output.  Weights stay below 2^8
+// and the sums are fp32, so nothing is lost.
 #include "attn.cuh"
 
 namespace moe {
@@ -33,14 +37,21 @@ namespace {
 
 constexpr int kRowsWarps = 5;              // four of compute, one of copies
 constexpr int kRowsThreads = kRowsWarps * 32;
-constexpr int kRows = 16;                  // rows of a unit
 
-__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool F16>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -56,16 +67,22 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
 }
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// E4M3 codes in bytes 0 and 2 (odd = false) or 1 and 3 of w as two bf16.  The
-// code's sign goes to the top and its seven other bits to the exponent's low
-// bits and the fraction's top: a bf16 of 2^-120 times the value (subnormals
-// included), which one exact product restores.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, bool odd) {
-    const uint32_t mag = odd ? (w >> 4) & 0x07F007F0u : (w << 4) & 0x07F007F0u;
-    const uint32_t sgn = odd ? w & 0x80008000u : (w << 8) & 0x80008000u;
+// An 8 x 8 matrix of 16-bit elements across the warp (lane (g, t): row g, columns 2t, 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(mag | sgn), "r"(0x7B807B80u));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+// Two E4M3 codes to two f16.
+__device__ __forceinline__ uint32_t e4m3_f16(uint16_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
+    return r;
+}
+// E4M3 codes in bytes 0 and 2 (odd = false) or 1 and 3 of w as two bf16, 2^-120 times the values.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, bool odd) {
+    const uint32_t x = odd ? w : __byte_perm(w, 0, 0x2404);  // the codes to bytes 1 and 3
+    return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
 }
 // Nibbles i and i + 4 of w (two's complement) as two bf16: 128 + (n + 8) by its
 // bits, then less 136.
@@ -80,30 +97,40 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
 
-// Shapes of one instantiation.
-template <int FMT, int D>
+// Shapes of one instantiation; R8: blocks of eight rows.
+template <int FMT, int D, int R8>
 struct RowsShape {
+    static constexpr int kRows = 8 * R8;
+    static constexpr int kCtas = R8 == 1 ? 3 : 2;               // per SM
     static constexpr int kRowB = kv_row_bytes(FMT, D);          // bytes of a cache row
     static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;     // of a box's row: the swizzle span
     static constexpr int kHalves = kRowB / kBoxB;
-    // keys of a stage: 32 KB of keys and values, 128 keys at most
-    static constexpr int kTk = 2 * kRowB * 128 <= 32768 ? 128 : 64;
-    static constexpr int kKw = kTk / 4;                         // keys of a warp
+    static constexpr int kTk = FMT == kKvBf16 ? 64 : 128;       // keys of a stage
+    static constexpr int kKm = kTk / 64;                        // blocks of 16 keys of a warp
     static constexpr int kTileB = kTk * kRowB;                  // bytes of a stage's keys
     static constexpr int kScB = FMT == kKvBf16 ? 0 : kTk * 4;   // and of their scales
-    static constexpr int kStages = 98304 / (2 * kTileB) < 8 ? 98304 / (2 * kTileB) : 8;
+    static constexpr int kRing = R8 == 1 ? 65536 : 98304;
+    static constexpr int kStages = kRing / (2 * kTileB) < 8 ? kRing / (2 * kTileB) : 8;
     static constexpr int kChunks = kRowB / 16;                  // 16-byte chunks of a row
-    static constexpr int kEl = D / kChunks;                     // elements of a chunk: 8, 16, 32
-    static constexpr int kNt = D / 8;                           // output column tiles
+    static constexpr int kDm = D / 16;                          // blocks of 16 output columns
+    static constexpr int kLd = D + 4;                           // row stride of the join's buffer
     // shared memory: tiles, scales, the join's buffer, barriers
     static constexpr int kOffSc = kStages * 2 * kTileB;
     static constexpr int kOffJoin = kOffSc + kStages * 2 * kScB;
-    static constexpr int kOffMl = kOffJoin + kRows * D * 4;
+    static constexpr int kOffMl = kOffJoin + kRows * kLd * 4;
     static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
     static constexpr int kSmem = kOffMisc + 16;
-    static_assert(kSmem <= 115712, "two CTAs share an SM's shared memory");
+    static_assert(kSmem <= (R8 == 1 ? 76800 : 115712), "the CTAs of an SM share its shared memory");
+    static_assert(kSmem >= deal_bytes(kRowsThreads), "scratch");
+    static constexpr int kPart = kRows * D + 2 * kRows;         // floats of a partial result
 };
 
 // Byte offset of a 16-byte chunk of a row inside a tile as TMA leaves it.
@@ -115,17 +142,19 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return half * (TK * BOXB) + row * BOXB + ((c ^ x) << 4);
 }
 
-// A unit's rows as one lane sees them (rows g and g + 8).
-struct RowInfo {
-    int64_t q[2];     // row of out / lse: token * H + head, -1 where there is none
-    int pos[2];       // last key it sees
-    int first[2];     // first key it sees
-};
+// The output column of a lane's accumulators (block m, upper half or not).
+template <int FMT>
+__device__ __forceinline__ int out_col(int m, int half, int g) {
+    if (FMT == kKvBf16) return 16 * m + 8 * half + g;
+    if (FMT == kKvE4m3) return 16 * m + 2 * g + half;
+    return 32 * (m / 2) + 4 * g + 2 * (m & 1) + half;
+}
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+template <int FMT, int D, int R8>
+__global__ void __launch_bounds__(kRowsThreads, RowsShape<FMT, D, R8>::kCtas)
 attn_rows_kernel(const __grid_constant__ AttnParams p) {
-    using S = RowsShape<FMT, D>;
+    using S = RowsShape<FMT, D, R8>;
+    constexpr int kRows = S::kRows;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,9 +253,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
     }
 
     // -------------------------------------------------------------------- compute
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, tid = threadIdx.x;
     constexpr int kSteps = D / 16;              // k16 steps of a score
-    constexpr int kNk = S::kKw / 8;             // key tiles of a warp
+    constexpr int kDm = S::kDm, kKm = S::kKm;
+    constexpr bool kRef = FMT == kKvE4m3;       // weights relative to a value scale
     Unit u = sh.u;
     int64_t unit0 = sh.unit0;
     uint32_t it = 0;
@@ -234,55 +264,118 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
     const float sc = p.scale_log2;
     float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
     float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);  // [warp][row]: maximum, sum
+    const int G = p.a.d.H / p.a.d.H_kv;
     do {
         int tile, end;
         unit_share(p, sh, u, unit0, tile, end);
         if (tile >= end) continue;
         const bool whole = tile == 0 && end == u.tiles;
-        // the lane's two rows
-        RowInfo ri;
         const int hk = u.hs / p.c.subs, sub = u.hs % p.c.subs;
-        const int G = p.a.d.H / p.a.d.H_kv;
+        // row r of the unit: its token in the sequence and its query head, -1 where there is none
+        auto token_of = [&](int r) {
+            const int tok = u.rt * p.c.tq + r / p.c.hg;
+            return r < p.c.tq * p.c.hg && tok < u.n && sub * p.c.hg + r % p.c.hg < G ? tok : -1;
+        };
+        auto head_of = [&](int r) { return hk * G + sub * p.c.hg + r % p.c.hg; };
+        // query fragments (row g of each block), in the order that the codes unpack to
+        uint32_t qf[kSteps][R8][2];
+        float rs[R8][2], off[R8][2];  // of rows 2t, 2t + 1 of a block: factor and start of the scores
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i, tok = u.rt * p.c.tq + r / p.c.hg, hd = sub * p.c.hg + r % p.c.hg;
-            const bool live = r < p.c.tq * p.c.hg && tok < u.n && hd < G;
-            ri.q[i] = live ? (int64_t)(u.tok0 + tok) * p.a.d.H + hk * G + hd : -1;
-            ri.pos[i] = live ? u.len - u.n + tok : -1;
-            ri.first[i] = p.a.d.window ? max(0, ri.pos[i] - p.a.d.window + 1) : 0;
-        }
-        // query fragments, in the order that the codes unpack to
-        uint32_t qf[kSteps][4];
+        for (int n = 0; n < R8; ++n) {
+            const int tok = token_of(8 * n + g);
+            const bool live = tok >= 0;
+            const uint16_t* q = p.a.q + (int64_t)(u.tok0 + max(tok, 0)) * p.a.ldq + head_of(8 * n + g) * D;
+            rs[n][0] = rs[n][1] = sc;
+            off[n][0] = off[n][1] = 0.0f;
+            if constexpr (FMT == kKvBf16) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t tok = ri.q[i] >= 0 ? ri.q[i] / p.a.d.H : 0, hd = ri.q[i] >= 0 ? ri.q[i] % p.a.d.H : 0;
-            const uint16_t* q = p.a.q + tok * p.a.ldq + hd * D;
-            const bool live = ri.q[i] >= 0;
+                for (int c = 0; c < S::kChunks; ++c)
+                    qf[c / 2][n][c & 1] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + 8 * c + 2 * t)) : 0;
+            } else {
+                // elements kPer t .. of each chunk of 4 kPer
+                constexpr int kPer = FMT == kKvE4m3 ? 4 : 8;
+                uint32_t x[S::kChunks][kPer / 2];
 #pragma unroll
-            for (int c = 0; c < S::kChunks; ++c) {
-                if constexpr (FMT == kKvBf16) {
-                    // chunk c: k pair (2t, 2t + 1) of half c & 1 of step c / 2
-                    qf[c / 2][2 * (c & 1) + i] =
-                        live ? __ldg(reinterpret_cast<const uint32_t*>(q + 8 * c + 2 * t)) : 0;
-                } else if constexpr (FMT == kKvE4m3) {
-                    const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(q + 16 * c + 4 * t))
-                                         : make_uint2(0, 0);
-                    qf[c][i] = __byte_perm(x.x, x.y, 0x5410);      // elements 0, 2
-                    qf[c][2 + i] = __byte_perm(x.x, x.y, 0x7632);  // elements 1, 3
-                } else {
-                    const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q + 32 * c + 8 * t))
-                                         : make_uint4(0, 0, 0, 0);
-                    qf[2 * c][i] = __byte_perm(x.x, x.z, 0x5410);          // 0, 4
-                    qf[2 * c][2 + i] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
-                    qf[2 * c + 1][i] = __byte_perm(x.y, x.w, 0x5410);      // 2, 6
-                    qf[2 * c + 1][2 + i] = __byte_perm(x.y, x.w, 0x7632);  // 3, 7
+                for (int c = 0; c < S::kChunks; ++c) {
+                    if constexpr (FMT == kKvE4m3) {
+                        const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(q + 16 * c + 4 * t)) : make_uint2(0, 0);
+                        x[c][0] = v.x, x[c][1] = v.y;
+                    } else {
+                        const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q + 32 * c + 8 * t)) : make_uint4(0, 0, 0, 0);
+                        x[c][0] = v.x, x[c][1] = v.y, x[c][2] = v.z, x[c][3] = v.w;
+                    }
+                }
+                uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+                for (int c = 0; c < S::kChunks; ++c)
+#pragma unroll
+                    for (int k = 0; k < kPer / 2; ++k)
+                        top = max(top, max(x[c][k] & 0x7FFFu, (x[c][k] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int e = min(126, 14 - ((int)(top >> 7) - 127));  // the largest comes to [2^14, 2^15)
+                const float up = pow2(e);
+                float sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < S::kChunks; ++c) {
+                    if constexpr (FMT == kKvE4m3) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            qf[c][n][k] = f16_pair(bf16_lo(x[c][k]) * up, bf16_hi(x[c][k]) * up);
+                    } else {
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            f[2 * k] = bf16_lo(x[c][k]) * up;
+                            f[2 * k + 1] = bf16_hi(x[c][k]) * up;
+                        }
+                        // nibbles 0, 4 and 2, 6 are read in bits 0-3 of their words, 1, 5 and 3, 7 in bits
+                        // 4-7, where they count 16 times as much
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float d = k & 1 ? 0.0625f : 1.0f;
+                            const uint32_t h = f16_pair(f[k] * d, f[k + 4] * d);
+                            qf[2 * c + k / 2][n][k & 1] = h;
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            sum += (b.x + b.y) / d;
+                        }
+                    }
+                }
+                if constexpr (FMT == kKvInt4) {
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                }
+                const float down = sc * pow2(max(-126, -e));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    rs[n][i] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * t + i)) * (FMT == kKvInt4 ? 16777216.0f : 1.0f);
+                    if constexpr (FMT == kKvInt4)
+                        off[n][i] = __shfl_sync(0xFFFFFFFFu, sum, 4 * (2 * t + i)) * (-8.0f / 16777216.0f);
                 }
             }
         }
-        float o[S::kNt][4];
+        // rows 2t, 2t + 1 of each block: the keys they see
+        int pos[R8][2], first[R8][2];
 #pragma unroll
-        for (int j = 0; j < S::kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
+        for (int n = 0; n < R8; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tok = token_of(8 * n + 2 * t + i);
+                pos[n][i] = tok >= 0 ? u.len - u.n + tok : -1;
+                first[n][i] = p.a.d.window ? max(0, pos[n][i] - p.a.d.window + 1) : 0;
+            }
+        float o[kDm][R8][4];
+#pragma unroll
+        for (int j = 0; j < kDm; ++j)
+#pragma unroll
+            for (int n = 0; n < R8; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+        float m[R8][2], l[R8][2];
+#pragma unroll
+        for (int n = 0; n < R8; ++n) {
+            m[n][0] = m[n][1] = kNoMax;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+        float vlim = 0.0f, vf = 1.0f, vout = 1.0f;  // kRef: largest value scale in range, its factor, the output's
         // keys that every row of the unit sees need no mask
         const int inner0 = p.a.d.window ? max(0, u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - p.a.d.window) : 0;
         const int inner1 = u.len - u.n + u.rt * p.c.tq + 1;  // [inner0, inner1)
@@ -292,312 +385,326 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             // once a wait gave up the flag is set; the warps then run on without waiting, in step
             // with each other, to the end
             if (ok) ok = mbar_wait(full(s), (it / S::kStages) & 1, abort_flag, hdr);
-            const int kw0 = warp * S::kKw;                       // the warp's first key in the tile
+            const int kw0 = warp * 16 * kKm;                       // the warp's first key in the tile
             const int key = (u.tile0 + tile) * S::kTk + kw0;
-            if (key < u.key1 && key + S::kKw > u.key0) {
+            if (key < u.key1 && key + 16 * kKm > u.key0) {
                 const uint32_t kt = sbase + s * 2 * S::kTileB, vt = kt + S::kTileB;
-                float sv[kNk][4];
+                float sv[kKm][R8][4];
 #pragma unroll
-                for (int j = 0; j < kNk; ++j) sv[j][0] = sv[j][1] = sv[j][2] = sv[j][3] = 0.0f;
-                // scores: chunks of 16 bytes, four per ldmatrix
-                if constexpr (FMT == kKvBf16) {
+                for (int km = 0; km < kKm; ++km)
 #pragma unroll
-                    for (int j = 0; j < kNk; ++j)
+                    for (int n = 0; n < R8; ++n) {
+                        sv[km][n][0] = sv[km][n][2] = off[n][0];
+                        sv[km][n][1] = sv[km][n][3] = off[n][1];
+                    }
 #pragma unroll
-                        for (int c = 0; c < S::kChunks; c += 4) {
-                            uint32_t r[4];
-                            ldsm4(r, kt + chunk_at<S::kBoxB, S::kTk>(kw0 + 8 * j + (lane & 7), c + (lane >> 3)));
-                            mma16816(sv[j], qf[c / 2], r[0], r[1]);
-                            mma16816(sv[j], qf[c / 2 + 1], r[2], r[3]);
-                        }
-                } else if constexpr (S::kChunks >= 4) {
+                for (int km = 0; km < kKm; ++km)
 #pragma unroll
-                    for (int j = 0; j < kNk; ++j)
+                    for (int c = 0; c < S::kChunks; c += 2) {
+                        // r: keys 0-7 and 8-15 of chunk c, then of chunk c + 1
+                        uint32_t r[4];
+                        ldsm4(r, kt + chunk_at<S::kBoxB, S::kTk>(kw0 + 16 * km + (lane & 15), c + (lane >> 4)));
+                        if constexpr (FMT == kKvBf16) {
 #pragma unroll
-                        for (int c = 0; c < S::kChunks; c += 4) {
-                            uint32_t r[4];
-                            ldsm4(r, kt + chunk_at<S::kBoxB, S::kTk>(kw0 + 8 * j + (lane & 7), c + (lane >> 3)));
+                            for (int n = 0; n < R8; ++n) mma16816<false>(sv[km][n], r, qf[c / 2][n]);
+                        } else if constexpr (FMT == kKvE4m3) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if constexpr (FMT == kKvE4m3) {
-                                    mma16816(sv[j], qf[c + i], e4m3_pair(r[i], false), e4m3_pair(r[i], true));
-                                } else {
-                                    mma16816(sv[j], qf[2 * (c + i)], int4_pair(r[i], 0), int4_pair(r[i], 1));
-                                    mma16816(sv[j], qf[2 * (c + i) + 1], int4_pair(r[i], 2), int4_pair(r[i], 3));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x = r[2 * i], y = r[2 * i + 1];
+                                const uint32_t a[4] = {e4m3_f16((uint16_t)x), e4m3_f16((uint16_t)y),
+                                                       e4m3_f16((uint16_t)(x >> 16)), e4m3_f16((uint16_t)(y >> 16))};
+#pragma unroll
+                                for (int n = 0; n < R8; ++n) mma16816<true>(sv[km][n], a, qf[c + i][n]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x = r[2 * i] ^ 0x88888888u, y = r[2 * i + 1] ^ 0x88888888u;
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t xs = x >> (8 * h), ys = y >> (8 * h);
+                                    const uint32_t a[4] = {xs & 0x000F000Fu, ys & 0x000F000Fu, xs & 0x00F000F0u,
+                                                           ys & 0x00F000F0u};
+#pragma unroll
+                                    for (int n = 0; n < R8; ++n) mma16816<true>(sv[km][n], a, qf[2 * (c + i) + h][n]);
                                 }
                             }
                         }
-                } else {  // two chunks (int4, D = 64): two key tiles per ldmatrix
-#pragma unroll
-                    for (int j = 0; j < kNk; j += 2) {
-                        uint32_t r[4];
-                        ldsm4(r, kt + chunk_at<S::kBoxB, S::kTk>(kw0 + 8 * (j + (lane >> 4)) + (lane & 7), (lane >> 3) & 1));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = i & 1;
-                            mma16816(sv[j + i / 2], qf[2 * c], int4_pair(r[i], 0), int4_pair(r[i], 1));
-                            mma16816(sv[j + i / 2], qf[2 * c + 1], int4_pair(r[i], 2), int4_pair(r[i], 3));
-                        }
                     }
-                }
                 // to the exponent's domain: scale * log2(e), the keys' scales, the masks
-                const float* ks = reinterpret_cast<const float*>(smem + S::kOffSc + s * 2 * S::kScB) + kw0;
-                const bool inner = key >= inner0 && key + S::kKw <= inner1;
-                float mx[2] = {kNoMax, kNoMax};
+                const float* ks = reinterpret_cast<const float*>(smem + S::kOffSc + s * 2 * S::kScB) + kw0 + g;
+                const bool inner = key >= inner0 && key + 16 * kKm <= inner1;
+                const bool edge = key < u.key0 || key + 16 * kKm > u.key1;
+                float mx[R8][2], vw[kKm][2], vtop = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kNk; ++j) {
-                    float2 f = make_float2(sc, sc);
-                    if (FMT != kKvBf16) {
-                        f = *reinterpret_cast<const float2*>(ks + 8 * j + 2 * t);
-                        f.x *= sc;
-                        f.y *= sc;
+                for (int n = 0; n < R8; ++n) mx[n][0] = mx[n][1] = kNoMax;
+#pragma unroll
+                for (int km = 0; km < kKm; ++km)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // keys g and g + 8 of the block
+                        const int k = key + 16 * km + 8 * h + g;
+                        if constexpr (FMT != kKvBf16) {
+                            // keys outside [key0, key1) are nobody's: their scales may be anything
+                            vw[km][h] = edge && (k < u.key0 || k >= u.key1) ? 0.0f : ks[S::kTk + 16 * km + 8 * h];
+                            vtop = fmaxf(vtop, vw[km][h]);
+                        }
+                        const float f = FMT != kKvBf16 ? ks[16 * km + 8 * h] : 1.0f;
+#pragma unroll
+                        for (int n = 0; n < R8; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float& x = sv[km][n][2 * h + i];
+                                x *= FMT != kKvBf16 ? rs[n][i] * f : sc;
+                                if (!inner && (k > pos[n][i] || k < first[n][i])) x = -INFINITY;
+                                mx[n][i] = fmaxf(mx[n][i], x);
+                            }
                     }
-                    sv[j][0] *= f.x;
-                    sv[j][1] *= f.y;
-                    sv[j][2] *= f.x;
-                    sv[j][3] *= f.y;
-                    if (!inner) {
-                        const int k0 = key + 8 * j + 2 * t;
+                bool raise = kRef && vtop > vlim;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int k = k0 + (e & 1), i = e >> 1;
-                            if (k > ri.pos[i] || k < ri.first[i]) sv[j][e] = -INFINITY;
+                for (int n = 0; n < R8; ++n) raise |= mx[n][0] > m[n][0] + 8.0f || mx[n][1] > m[n][1] + 8.0f;
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    float va = 1.0f;
+                    if (kRef) {
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
+                        if (vtop > vlim) {
+                            // scales up to 64 times this one's power of two keep p * scale * vf below 2^127
+                            const int e = min(max(((__float_as_int(vtop) >> 23) & 255) - 126, -14), 113);
+                            const float was = vout;
+                            vlim = pow2(e) * 64.0f;
+                            vf = pow2(112 - e);
+                            vout = pow2(e + 8);
+                            va = was / vout;
                         }
                     }
-                    mx[0] = fmaxf(mx[0], fmaxf(sv[j][0], sv[j][1]));
-                    mx[1] = fmaxf(mx[1], fmaxf(sv[j][2], sv[j][3]));
-                }
-                if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
-                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
-                        const float mn = fmaxf(m[i], mx[i]), a = ex2(m[i] - mn);
-                        m[i] = mn;
-                        l[i] *= a;
-#pragma unroll
-                        for (int j = 0; j < S::kNt; ++j) {
-                            o[j][2 * i] *= a;
-                            o[j][2 * i + 1] *= a;
-                        }
-                    }
-                }
-                // weights; their sum takes them unrounded and without the values' scales
-                const float* vs = ks + S::kTk;
-                uint32_t pf[kNk / 2][4];
-#pragma unroll
-                for (int j = 0; j < kNk; ++j) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float p0 = ex2(sv[j][2 * i] - m[i]), p1 = ex2(sv[j][2 * i + 1] - m[i]);
-                        l[i] += p0 + p1;
-                        if (FMT != kKvBf16) {
-                            const float2 f = *reinterpret_cast<const float2*>(vs + 8 * j + 2 * t);
-                            p0 *= f.x;
-                            p1 *= f.y;
-                        }
-                        pf[j / 2][2 * (j & 1) + i] = bf16_pair(p0, p1);
-                    }
-                }
-                // keys outside [key0, key1) are nobody's: their slots may hold anything, so the
-                // values (and their scales) are cleared, not just weighted with 0
-                const bool edge = key < u.key0 || key + S::kKw > u.key1;
-                uint32_t vmask[kNk];
-                if (edge) {
-#pragma unroll
-                    for (int j = 0; j < kNk; ++j) {
-                        const int k0 = key + 8 * j + 2 * t;
-                        vmask[j] = (k0 >= u.key0 && k0 < u.key1 ? 0x0000FFFFu : 0u) |
-                                   (k0 + 1 >= u.key0 && k0 + 1 < u.key1 ? 0xFFFF0000u : 0u);
-                        if (FMT != kKvBf16) {
-                            pf[j / 2][2 * (j & 1)] &= vmask[j];
-                            pf[j / 2][2 * (j & 1) + 1] &= vmask[j];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int kk = 0; kk < kNk / 2; ++kk)
-#pragma unroll
-                    for (int c = 0; c < S::kChunks; c += 2) {
-                        // chunks c and c + 1 of keys 16 kk .. + 7 and + 8 .. + 15
-                        uint32_t r[4];
-                        ldsm4t(r, vt + chunk_at<S::kBoxB, S::kTk>(kw0 + 16 * kk + (lane & 15), c + (lane >> 4)));
-                        if (edge) {
-                            r[0] &= vmask[2 * kk];
-                            r[1] &= vmask[2 * kk + 1];
-                            r[2] &= vmask[2 * kk];
-                            r[3] &= vmask[2 * kk + 1];
-                        }
+                    for (int n = 0; n < R8; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t lo = r[2 * i], hi = r[2 * i + 1];
-                            if constexpr (FMT == kKvBf16) {
-                                mma16816(o[c + i], pf[kk], lo, hi);
-                            } else if constexpr (FMT == kKvE4m3) {
-                                const int j = 2 * (c + i);
-                                mma16816(o[j], pf[kk], e4m3_pair(lo, false), e4m3_pair(hi, false));
-                                mma16816(o[j + 1], pf[kk], e4m3_pair(lo, true), e4m3_pair(hi, true));
-                            } else {
+                            float x = mx[n][i];
 #pragma unroll
-                                for (int n = 0; n < 4; ++n)
-                                    mma16816(o[4 * (c + i) + n], pf[kk], int4_pair(lo, n), int4_pair(hi, n));
+                            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+                            const float mn = fmaxf(m[n][i], x), a = ex2(m[n][i] - mn);
+                            m[n][i] = mn;
+                            l[n][i] *= a;
+#pragma unroll
+                            for (int j = 0; j < kDm; ++j) {
+                                o[j][n][i] *= a * va;
+                                o[j][n][2 + i] *= a * va;
+                            }
+                        }
+                }
+                // weights; their sum takes them unrounded and without the values' scales
+                uint32_t pb[kKm][R8][2];
+#pragma unroll
+                for (int km = 0; km < kKm; ++km)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < R8; ++n) {
+                            float p0 = ex2(sv[km][n][2 * h] - m[n][0]), p1 = ex2(sv[km][n][2 * h + 1] - m[n][1]);
+                            l[n][0] += p0;
+                            l[n][1] += p1;
+                            if constexpr (FMT != kKvBf16) {
+                                const float f = kRef ? vw[km][h] * vf : vw[km][h];
+                                p0 *= f;
+                                p1 *= f;
+                            }
+                            pb[km][n][h] = transposed(bf16_pair(p0, p1));
+                        }
+#pragma unroll
+                for (int km = 0; km < kKm; ++km) {
+                    // bf16: what nobody's slots hold is cleared, not just weighted with 0 (codes are
+                    // finite whatever they are)
+                    uint32_t vm[2] = {~0u, ~0u};
+                    if (FMT == kKvBf16 && edge) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int k = key + 16 * km + 8 * h + 2 * t;
+                            vm[h] = (k >= u.key0 && k < u.key1 ? 0x0000FFFFu : 0u) |
+                                    (k + 1 >= u.key0 && k + 1 < u.key1 ? 0xFFFF0000u : 0u);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < S::kChunks; c += 2) {
+                        uint32_t r[4];
+                        ldsm4t(r, vt + chunk_at<S::kBoxB, S::kTk>(kw0 + 16 * km + (lane & 15), c + (lane >> 4)));
+                        if constexpr (FMT == kKvBf16) {
+                            if (edge) {
+                                r[0] &= vm[0], r[2] &= vm[0];
+                                r[1] &= vm[1], r[3] &= vm[1];
+                            }
+                            const uint32_t a[4] = {r[0], r[2], r[1], r[3]};
+#pragma unroll
+                            for (int n = 0; n < R8; ++n) mma16816<false>(o[c / 2][n], a, pb[km][n]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x = r[2 * i], y = r[2 * i + 1];
+                                if constexpr (FMT == kKvE4m3) {
+                                    const uint32_t a[4] = {e4m3_pair(x, false), e4m3_pair(x, true), e4m3_pair(y, false),
+                                                           e4m3_pair(y, true)};
+#pragma unroll
+                                    for (int n = 0; n < R8; ++n) mma16816<false>(o[c + i][n], a, pb[km][n]);
+                                } else {
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const uint32_t a[4] = {int4_pair(x, 2 * h), int4_pair(x, 2 * h + 1),
+                                                               int4_pair(y, 2 * h), int4_pair(y, 2 * h + 1)};
+#pragma unroll
+                                        for (int n = 0; n < R8; ++n) mma16816<false>(o[2 * (c + i) + h][n], a, pb[km][n]);
+                                    }
+                                }
                             }
                         }
                     }
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(s));
         }
 
         // ------------------------------------------------------ join the four warps
-        // (row g: registers 0, 1; row g + 8: 2, 3; the same lanes hold them in every warp)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-            if (t == 0) ml[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
-        }
-        compute_sync();
-        float M[2], L[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            M[i] = kNoMax;
-            L[i] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) M[i] = fmaxf(M[i], ml[k * kRows + g + 8 * i].x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 x = ml[k * kRows + g + 8 * i];
-                L[i] += x.y * ex2(x.x - M[i]);
-            }
-            const float a = ex2(m[i] - M[i]);
-#pragma unroll
-            for (int j = 0; j < S::kNt; ++j) {
-                o[j][2 * i] *= a;
-                o[j][2 * i + 1] *= a;
-            }
-        }
-        float4* jb = reinterpret_cast<float4*>(join);
-        // 1 -> 0, 3 -> 2, then 2 -> 0: a fixed order
-#pragma unroll
-        for (int round = 0; round < 3; ++round) {
-            const int from = round == 0 ? 1 : round == 1 ? 3 : 2, to = round == 1 ? 2 : 0;
-            if (warp == from)
-#pragma unroll
-                for (int j = 0; j < S::kNt; ++j)
-                    jb[j * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-            compute_sync();
-            if (warp == to)
-#pragma unroll
-                for (int j = 0; j < S::kNt; ++j) {
-                    const float4 x = jb[j * 32 + lane];
-                    o[j][0] += x.x;
-                    o[j][1] += x.y;
-                    o[j][2] += x.z;
-                    o[j][3] += x.w;
-                }
-            compute_sync();
-        }
-        bool write = whole;
-        if (!whole) {
-            // a partial result: slot 0 of a CTA for a unit that an earlier CTA began, else slot 1
-            const int c = blockIdx.x, c0 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost);
-            const int c1 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost + u.tiles - 1);
-            constexpr int kPart = kRows * D + 2 * kRows;
-            if (warp == 0) {
-                float* part = p.part + (int64_t)(2 * c + (c == c0)) * kPart;
-                float4* po = reinterpret_cast<float4*>(part);
-#pragma unroll
-                for (int j = 0; j < S::kNt; ++j)
-                    __stcg(po + j * 32 + lane, make_float4(o[j][0], o[j][1], o[j][2], o[j][3]));
-                if (t == 0) {
-                    float2* pm = reinterpret_cast<float2*>(part + kRows * D);
-                    __stcg(pm + g, make_float2(M[0], L[0]));
-                    __stcg(pm + g + 8, make_float2(M[1], L[1]));
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const unsigned seen = atomicAdd(p.counters + c0, 1u);
-                    const bool last = seen == (unsigned)(c1 - c0);
-                    if (last) p.counters[c0] = 0;
-                    *last_flag = last;
-                }
-                __syncwarp();
-                write = *last_flag != 0;
-                if (write) {
-                    __threadfence();
-                    M[0] = M[1] = kNoMax;
-                    for (int k = c0; k <= c1; ++k) {
-                        const float2* pm = reinterpret_cast<const float2*>(
-                            p.part + (int64_t)(2 * k + (k == c0)) * kPart + kRows * D);
-                        M[0] = fmaxf(M[0], __ldcg(&pm[g].x));
-                        M[1] = fmaxf(M[1], __ldcg(&pm[g + 8].x));
-                    }
-                    L[0] = L[1] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < S::kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-                    for (int k = c0; k <= c1; ++k) {
-                        const float* q = p.part + (int64_t)(2 * k + (k == c0)) * kPart;
-                        const float2* pm = reinterpret_cast<const float2*>(q + kRows * D);
-                        const float2 x0 = __ldcg(pm + g), x1 = __ldcg(pm + g + 8);
-                        const float a0 = ex2(x0.x - M[0]), a1 = ex2(x1.x - M[1]);
-                        L[0] += x0.y * a0;
-                        L[1] += x1.y * a1;
-                        const float4* po = reinterpret_cast<const float4*>(q);
-#pragma unroll
-                        for (int j = 0; j < S::kNt; ++j) {
-                            const float4 x = __ldcg(po + j * 32 + lane);
-                            o[j][0] += x.x * a0;
-                            o[j][1] += x.y * a0;
-                            o[j][2] += x.z * a1;
-                            o[j][3] += x.w * a1;
-                        }
-                    }
-                }
-            }
-        }
-        if (warp == 0 && write) {
+        for (int n = 0; n < R8; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (ri.q[i] < 0) continue;
-                const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
-                uint16_t* out = p.a.out + ri.q[i] * D;
-// of each chunk the lane holds kEl / 4 consecutive columns, over its kEl / 8 tiles
-                constexpr int kJ = S::kEl / 8;
 #pragma unroll
-                for (int c = 0; c < S::kChunks; ++c) {
-                    uint32_t x[kJ];
+                for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], d);
+                if (g == 0) ml[warp * kRows + 8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
+            }
+        compute_sync();
+        auto joined = [&](int r) {  // maximum and sum of row r over the warps
+            float M = kNoMax, L = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < kJ; ++k) {  // columns 2k, 2k + 1: tile k % kJ, register k / kJ
-                        const int k0 = 2 * k, k1 = 2 * k + 1;
-                        x[k] = bf16_pair(o[c * kJ + k0 % kJ][2 * i + k0 / kJ] * inv,
-                                         o[c * kJ + k1 % kJ][2 * i + k1 / kJ] * inv);
+            for (int k = 0; k < 4; ++k) M = fmaxf(M, ml[k * kRows + r].x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) L += ml[k * kRows + r].y * ex2(ml[k * kRows + r].x - M);
+            return make_float2(M, L);
+        };
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {  // one warp after the other: a fixed order
+            if (warp == k) {
+#pragma unroll
+                for (int n = 0; n < R8; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 8 * n + 2 * t + i;
+                        const float a = ex2(m[n][i] - joined(r).x) * vout;
+                        float* to = join + r * S::kLd;
+#pragma unroll
+                        for (int j = 0; j < kDm; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float& x = to[out_col<FMT>(j, h, g)];
+                                const float y = o[j][n][2 * h + i] * a;
+                                x = k ? x + y : y;
+                            }
                     }
-                    uint16_t* to = out + c * S::kEl + 2 * kJ * t;
-                    if constexpr (kJ == 1) *reinterpret_cast<uint32_t*>(to) = x[0];
-                    else if constexpr (kJ == 2) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
-                    else *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            compute_sync();
+        }
+        // The unit's result, or this CTA's part of it: thread by thread, eight columns of a row
+        constexpr int kPieces = kRows * D / 8;
+        auto put = [&](int piece, const float* f, float2 st) {
+            const int r = piece / (D / 8), col = piece % (D / 8) * 8, tok = token_of(r);
+            if (tok < 0) return;
+            const float inv = st.y > 0.0f ? 1.0f / st.y : 0.0f;
+            const int64_t row = (int64_t)(u.tok0 + tok) * p.a.d.H + head_of(r);
+            *reinterpret_cast<uint4*>(p.a.out + row * D + col) =
+                make_uint4(bf16_pair(f[0] * inv, f[1] * inv), bf16_pair(f[2] * inv, f[3] * inv),
+                           bf16_pair(f[4] * inv, f[5] * inv), bf16_pair(f[6] * inv, f[7] * inv));
+            if (p.a.lse && col == 0) p.a.lse[row] = st.y > 0.0f ? (st.x + log2f(st.y)) * kLn2 : -INFINITY;
+        };
+        auto mine = [&](int piece, float* f) {
+            const float4* q = reinterpret_cast<const float4*>(join + piece / (D / 8) * S::kLd + piece % (D / 8) * 8);
+            const float4 x = q[0], y = q[1];
+            f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+        };
+        if (whole) {
+            for (int i = tid; i < kPieces; i += 128) {
+                float f[8];
+                mine(i, f);
+                put(i, f, joined(i / (D / 8)));
+            }
+        } else {
+            // a partial result: slot 0 of a CTA for a unit that an earlier CTA began, else slot 1.  The CTA
+            // that comes last joins them; if the others have all come its own need not go through memory.
+            const int c = blockIdx.x, c0 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost);
+            const int c1 = share_owner(sh.W, sh.R, unit0 + p.c.unit_cost + u.tiles - 1);
+            const unsigned others = c1 - c0;
+            unsigned* arrived = p.counters + c0;
+            auto part = [&](int k) { return p.part + (int64_t)(2 * k + (k == c0)) * S::kPart; };
+            if (tid == 0) {
+                unsigned n;
+                asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
+                *last_flag = n == others;
+            }
+            compute_sync();
+            bool last = *last_flag;
+            if (!last) {
+                float* q = part(c);
+                for (int i = tid; i < kPieces; i += 128) {
+                    float f[8];
+                    mine(i, f);
+                    float4* to = reinterpret_cast<float4*>(q + i * 8);
+                    __stcg(to, make_float4(f[0], f[1], f[2], f[3]));
+                    __stcg(to + 1, make_float4(f[4], f[5], f[6], f[7]));
                 }
-                if (p.a.lse && t == 0)
-                    p.a.lse[ri.q[i]] = L[i] > 0.0f ? (M[i] + log2f(L[i])) * kLn2 : -INFINITY;
+                if (tid < kRows) __stcg(reinterpret_cast<float2*>(q + kRows * D) + tid, joined(tid));
+                __threadfence();
+                compute_sync();
+                if (tid == 0) *last_flag = atomicAdd(arrived, 1u) == others;
+                compute_sync();
+                last = *last_flag;
+            }
+            if (last) {
+                __threadfence();
+                if (tid == 0) *arrived = 0;
+                for (int i = tid; i < kPieces; i += 128) {
+                    const int r = i / (D / 8);
+                    auto stat = [&](int k) {
+                        return k == c ? joined(r) : __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D) + r);
+                    };
+                    float2 st = make_float2(kNoMax, 0.0f);
+#pragma unroll 4
+                    for (int k = c0; k <= c1; ++k) st.x = fmaxf(st.x, stat(k).x);
+                    float f[8] = {};
+#pragma unroll 4
+                    for (int k = c0; k <= c1; ++k) {
+                        const float2 e = stat(k);
+                        const float a = ex2(e.x - st.x);
+                        st.y += e.y * a;
+                        float v[8];
+                        if (k == c) mine(i, v);
+                        else {
+                            const float4* q = reinterpret_cast<const float4*>(part(k) + i * 8);
+                            const float4 x = __ldcg(q), y = __ldcg(q + 1);
+                            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] += v[j] * a;
+                    }
+                    put(i, f, st);
+                }
             }
         }
+        compute_sync();  // the buffers are free for the next unit
     } while (next_unit(p, sh, u, unit0));
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int R8>
 cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
                    unsigned* counters, cudaStream_t st) {
-    using S = RowsShape<FMT, D>;
+    using S = RowsShape<FMT, D, R8>;
     AttnParams p;
     p.a = a;
     const int G = a.d.H / a.d.H_kv;
-    p.c.hg = std::min(G, kRows);
-    p.c.tq = kRows / p.c.hg;
-    p.c.subs = (G + kRows - 1) / kRows;
+    p.c.hg = std::min(G, S::kRows);
+    p.c.tq = S::kRows / p.c.hg;
+    p.c.subs = (G + S::kRows - 1) / S::kRows;
     p.c.hs = a.d.H_kv * p.c.subs;
-    p.c.tk_log2 = S::kTk == 128 ? 7 : 6;
+    p.c.tk_log2 = __builtin_ctz(S::kTk);
     p.c.page_log2 = __builtin_ctz(a.d.page);
     p.c.unit_cost = 1;
     p.c.min_share = 2;
@@ -609,17 +716,27 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     if (!make_kv_map(&p.tm_k, a.cache.k, a, S::kBoxB, std::min(a.d.page, S::kTk)) ||
         !make_kv_map(&p.tm_v, a.cache.v, a, S::kBoxB, std::min(a.d.page, S::kTk)))
         return cudaErrorInvalidValue;
-    const void* kern = reinterpret_cast<const void*>(&attn_rows_kernel<FMT, D>);
+    const void* kern = reinterpret_cast<const void*>(&attn_rows_kernel<FMT, D, R8>);
     cudaError_t e = ensure_dynamic_smem(kern, S::kSmem);
     if (e != cudaSuccess) return e;
-    attn_rows_kernel<FMT, D><<<2 * sm_count(), kRowsThreads, S::kSmem, st>>>(p);
+    attn_rows_kernel<FMT, D, R8><<<S::kCtas * sm_count(), kRowsThreads, S::kSmem, st>>>(p);
     return cudaGetLastError();
+}
+
+template <int FMT, int D>
+cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+                       unsigned* counters, cudaStream_t st) {
+    // eight rows hold the tokens of a decode step when a group has at most eight query heads; a
+    // sequence with more rows takes more units (and reads its keys again, from L2)
+    return a.d.H / a.d.H_kv <= 8 ? launch<FMT, D, 1>(a, rows_lo, rows_hi, part, counters, st)
+                                 : launch<FMT, D, 2>(a, rows_lo, rows_hi, part, counters, st);
 }
 
 }  // namespace
 
 size_t attn_rows_part_bytes(const moe_kv_dims_t& d) {
-    return (size_t)(2 * 2 * sm_count()) * (kRows * d.D + 2 * kRows) * sizeof(float);
+    // two slots for each of three CTAs per SM with 8 rows, or two with 16
+    return (size_t)(2 * sm_count()) * std::max(3 * 8, 2 * 16) * (d.D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
@@ -627,14 +744,14 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi
     const bool wide = a.d.D == 128;
     switch (a.d.format) {
         case kKvBf16:
-            return wide ? launch<kKvBf16, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch<kKvBf16, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvBf16, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch_for<kKvBf16, 64>(a, rows_lo, rows_hi, part, counters, st);
         case kKvE4m3:
-            return wide ? launch<kKvE4m3, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch<kKvE4m3, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvE4m3, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch_for<kKvE4m3, 64>(a, rows_lo, rows_hi, part, counters, st);
         case kKvInt4:
-            return wide ? launch<kKvInt4, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch<kKvInt4, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvInt4, 128>(a, rows_lo, rows_hi, part, counters, st)
+                        : launch_for<kKvInt4, 64>(a, rows_lo, rows_hi, part, counters, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -154,7 +154,7 @@ __device__ Share deal(const AttnParams& p, void* scratch) {
     const int pe = (n_rt + THREADS - 1) / THREADS, e0 = min(n_rt, tid * pe), e1 = min(n_rt, e0 + pe);
     int k = 0;
 #pragma unroll
-    for (int step = THREADS >= 512 ? 256 : THREADS >= 256 ? 256 : 128; step; step >>= 1)
+    for (int step = THREADS > 512 ? 512 : THREADS > 256 ? 256 : 128; step; step >>= 1)
         if (k + step < THREADS && first[k + step] <= e0) k += step;
     auto seek = [&] {  // u to row tile e0
         u.b = k * per;

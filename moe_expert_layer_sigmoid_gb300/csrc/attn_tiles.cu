@@ -14,21 +14,24 @@
 //   - even and odd key tiles of one row tile, joined at the end, when it has not.
 //
 // TMEM (512 columns): S of A and B at 0 and 128, O at 256 and 384.  P (bf16, two
-// keys per column) overwrites S in place; the next S of a stream is issued after the
+// keys per column) overwrites S, each half of the keys its own half's first columns; the next S of a stream is issued after the
 // P V that reads P, and the tensor core runs one thread's products in order.
 //
-// One thread owns one row: maximum and sum need no exchange.  The running maximum
-// is raised only when a score exceeds it by 2^8, so O is rescaled (read, scaled and
-// written back in TMEM) in few tiles; when S of tile i is ready, P V of tile i - 1 is
-// too, so the row's thread may touch O without a further wait.
+// Two threads own a row, each half of a tile's keys, no shuffles.  S is read twice, in pieces of 32
+// columns, for the maximum and for the weights: that keeps registers few (shared memory leaves little
+// L1 to spill to) and the code short (a CTA runs most of it a few times only).  The running
+// maximum is raised only when a score exceeds it by 2^8: a barrier with a vote decides, and in few
+// tiles the halves exchange their maxima and O is rescaled (read, scaled and written back in TMEM);
+// when S of tile i is ready, P V of tile i - 1 is too, so the row's threads may touch O without a
+// further wait.
 //
 // Quantised caches: TMA brings the codes, a warpgroup turns them into bf16 in
 // place (the codes of a row lie where only the thread that converts it writes, or
 // the group synchronises between reading and writing).  Key scales multiply the
 // scores, value scales the weights, so codes enter the products exactly.
 //
-// Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-7 stream A, 8-11 stream B,
-// 12-15 conversion.
+// Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-11 stream A, 12-19 stream B (in each
+// four warps for the first 64 keys of a tile and four for the last), 20-23 conversion.
 #include <atomic>
 #include <type_traits>
 
@@ -45,7 +48,7 @@ constexpr int kSlots = 4;  // tiles of keys or values in shared memory
 template <int FMT, int D>
 struct TilesShape {
     static constexpr bool kQuant = FMT != kKvBf16;
-    static constexpr int kThreads = kQuant ? 512 : 384;
+    static constexpr int kThreads = kQuant ? 768 : 640;
     static constexpr int kRowB = kv_row_bytes(FMT, D);
     static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;
     static constexpr int kTileB = kTk * D * 2;                // a bf16 tile
@@ -57,17 +60,16 @@ struct TilesShape {
     static constexpr int kScB = kQuant ? 2 * kTk * 4 : 0;     // key and value scales of a tile
     static constexpr int kScSlots = 4;
     // registers per thread: control, streams, conversion; in 128-thread groups they add up to
-    // what the launch holds (168 x 384 or 128 x 512)
-    static constexpr int kRegCtl = 72, kRegStream = kQuant ? 176 : 216, kRegConv = 88;
-    static_assert(kQuant ? kRegCtl + 2 * kRegStream + kRegConv <= 512 : kRegCtl + 2 * kRegStream <= 504,
-                  "register split");
+    // what the launch holds (96 x 640 or 80 x 768)
+    static constexpr int kRegCtl = kQuant ? 64 : 96, kRegStream = kQuant ? 88 : 96, kRegConv = 64;
+    static_assert(kRegCtl + 4 * kRegStream + (kQuant ? kRegConv : 0) <= 480, "register split");
     static constexpr int kOffQ = 0;
     static constexpr int kOffKv = kOffQ + 2 * kTileRows * D * 2;
     static constexpr int kOffSc = kOffKv + kSlots * kSlotB;
-    // output rows on their way from registers to coalesced stores: 32 rows x 64 bytes per warp
+    // output rows on their way from registers to coalesced stores: 32 rows x 32 bytes per warp
     static constexpr int kOffStage = kOffSc + kScSlots * kScB;
-    static constexpr int kOffMl = kOffStage + 8 * 2048;  // the streams' maxima and sums, for their join
-    static constexpr int kOffBar = kOffMl + 2 * kTileRows * 8;
+    static constexpr int kOffMl = kOffStage + 16 * 1024;  // the streams' maxima and sums: [stream][half][row]
+    static constexpr int kOffBar = kOffMl + 4 * kTileRows * 8;
     // barriers: FULL, EMPTY, RAW [kSlots]; SF, PF, OD [2]; QF, QE, TD
     static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarSf = 3 * kSlots,
                          kBarPf = kBarSf + 2, kBarOd = kBarPf + 2, kBarQf = kBarOd + 2,
@@ -188,7 +190,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(S::kBarSf + x), 1);
-            mbar_init(bar(S::kBarPf + x), 4);
+            mbar_init(bar(S::kBarPf + x), 8);
             mbar_init(bar(S::kBarOd + x), 1);
         }
         mbar_init(bar(S::kBarQf), 1);
@@ -340,7 +342,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kTk / 16; ++ks)
-                        mma_ts_lo(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, b + ks * (16 * 128 / 16), id_pv,
+                        mma_ts_lo(tmem + 256 + x * 128, tmem + x * 128 + ks / 4 * 64 + ks % 4 * 8, b + ks * (16 * 128 / 16), id_pv,
                                   ks > 0 || !fresh[x]);
                 }
                 __syncwarp();
@@ -410,23 +412,27 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 mbar_drain(bar(S::kBarTd), 0, hdr);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 20) {
         // ----------------------------------------------------------------- streams
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegStream));
-        const int x = warp >= 8, r = threadIdx.x - (x ? 256 : 128);
+        const int x = warp >= 12, hf = (warp >> 2) & 1 ^ 1;   // stream, half of the key tile's columns
+        const int r = (warp & 3) * 32 + lane;                 // row
         const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
         const uint32_t ts = trow + x * 128, to = trow + 256 + x * 128;
-        // never 0, so that a masked score stays infinite
+        // a negative scale turns the scores' sign; not 0, so that a masked score stays infinite
         const bool neg = p.scale_log2 < 0.0f;
-        const float sc = neg ? fminf(p.scale_log2, -1e-37f) : fmaxf(p.scale_log2, 1e-37f);
+        const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
-        uint8_t* stage = smem + S::kOffStage + (warp - 4) * 2048;
+        uint8_t* stage = smem + S::kOffStage + (warp - 4) * 1024;
         float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
+        float* top = reinterpret_cast<float*>(ml + 2 * x * kTileRows) + r;  // + half * rows: halves' maxima
         uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
         bool ok = true;
         auto wait = [&](int b, uint32_t par) {  // once a wait gave up the streams run on, in step
             if (ok) ok = mbar_wait(bar(b), par & 1, abort_flag, hdr);
         };
+        auto stream_sync = [&] { asm volatile("bar.sync %0, 256;" ::"r"(2 + x) : "memory"); };
+        auto all_sync = [&] { asm volatile("bar.sync 1, 512;" ::: "memory"); };
         int64_t orow;       // this thread's row of out and lse: token * H + head, -1: none
         int pos, first;     // keys it sees: first .. pos
         auto rows_of = [&](const Unit& v, bool split) {
@@ -436,20 +442,20 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             pos = live ? v.len - v.n + tok : -1;
             first = p.a.d.window ? max(0, pos - p.a.d.window + 1) : 0;
         };
-        // 32 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory: each four
-        // lanes store 64 bytes of a row
-        auto put = [&](const uint32_t* e, int64_t row, int col) {
+        // 16 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory: each two
+        // lanes store 32 bytes of a row
+        auto put = [&](const uint32_t* e, int col) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) =
                     make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int rr = 8 * k + (lane >> 2), c = lane & 3;
-                const int64_t to_row = __shfl_sync(0xFFFFFFFFu, row, rr);
-                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-                if (to_row >= 0) *reinterpret_cast<uint4*>(p.a.out + to_row * D + col + 8 * c) = v;
+            for (int k = 0; k < 2; ++k) {
+                const int rr = 16 * k + (lane >> 1), c = lane & 1;
+                const int64_t row = __shfl_sync(0xFFFFFFFFu, orow, rr);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((c ^ ((rr >> 2) & 1)) << 4));
+                if (row >= 0) *reinterpret_cast<uint4*>(p.a.out + row * D + col + 8 * c) = v;
             }
             __syncwarp();
         };
@@ -459,191 +465,199 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             rows_of(u, s.split);
             const bool whole = s.t0 == 0 && s.t1 == u.tiles;
             float m = kNoMax, l = 0.0f;
-            bool any = false;
             // keys that all of the stream's rows see need no mask
             const int i0 = u.rt * p.c.tq + (s.split ? 0 : x * half);
             const int inner1 = u.len - u.n + i0 + 1;
             const int inner0 = p.a.d.window ? u.len - u.n + min(u.n, i0 + half) - p.a.d.window : 0;
-            for (int i = s.t0; i < s.t1; ++i) {
-                if (!s.act(x, i)) continue;
-                const uint32_t vk = 2 * (tiles0 + (uint32_t)(i - s.t0)) + 1;  // the value tile's slot index
-                const int key = (u.tile0 + i) * kTk;
+            // the stream's tiles: i0 .. (every other one with one row tile)
+            const int step = s.split ? 2 : 1;
+            const int beg = s.split ? s.t0 + x : x ? s.lo[1] : s.lo[0], end = x ? s.hi[1] : s.hi[0];
+            int key = (u.tile0 + beg) * kTk;
+            uint32_t vk = 2 * (tiles0 + (uint32_t)(beg - s.t0)) + 1;  // the value tile's slot index
+            // keys outside [key0, key1) are nobody's: their slots may hold anything.  bf16 values are cleared
+            // there, not just weighted with 0, by the first stream that takes the tile: by B where A has none.
+            const int key0 = u.key0, key1 = u.key1;
+            const int clear0 = s.split || x == 0 ? 0 : (u.tile0 + s.hi[0]) * kTk;
+#pragma unroll 1
+            for (int i = beg; i < end; i += step, key += step * kTk, vk += 2 * step) {
                 wait(S::kBarSf + x, n_sf++);
                 tc_fence_after();
-                if (!S::kQuant && !(s.split == false && x == 1 && s.act(0, i)) &&
-                    (key < u.key0 || key + kTk > u.key1)) {
-                    // keys outside [key0, key1) are nobody's: their slots may hold anything, so the
-                    // values are cleared (by the first stream that takes the tile), not just weighted with 0
+                if (!S::kQuant && (key < key0 || key + kTk > key1) && (key >= clear0 || (x == 1 && i < s.lo[0]))) {
                     wait(S::kBarFull + vk % kSlots, vk / kSlots);
-                    if (key + r < u.key0 || key + r >= u.key1) {
+                    if (key + r < key0 || key + r >= key1) {
                         uint8_t* z = smem + S::kOffKv + (vk % kSlots) * S::kSlotB + r * 128;
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
+                        for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c)
                             *reinterpret_cast<uint4*>(z + (c / 8) * (128 * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async();
                 }
-                // the keys' scales (times sc), then the values'
-                const uint32_t ksc = sbase + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB;
-                if (S::kQuant) wait(S::kBarFull + vk % kSlots, vk / kSlots);
                 const bool inner = key >= inner0 && key + kTk <= inner1;
-                const int hi = pos - key, lo = first - key;
-                // columns 32 c .. of the scores, masked; f: their factors into the exponent's domain
-                auto scores = [&](float* v, int c, auto masked) {
-                    if constexpr (masked) {
-                        // bit k: column 32 c + k is seen
-                        const int h = hi - 32 * c, g = lo - 32 * c;
+                // quantised: the half's key scales (times the call's; in place since before the products
+                // that S comes from), then its value scales
+                const uint32_t ksc = sbase + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB + 256 * hf;
+                // 32 scores of the half's 64, masked; quantised ones in the exponent's domain
+                auto scores = [&](uint32_t* vr, int c) {
+                    tmem_ld_x32(ts + 64 * hf + 32 * c, vr);
+                    tmem_wait_ld32(vr);
+                    float* v = reinterpret_cast<float*>(vr);
+                    if (S::kQuant) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = lds4(ksc + 128 * c + 16 * k);
+                            mul2(v[4 * k], v[4 * k + 1], f.x, f.y);
+                            mul2(v[4 * k + 2], v[4 * k + 3], f.z, f.w);
+                        }
+                    } else if (neg) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = -v[k];
+                    }
+                    if (!inner) {
+                        // bit k: column k is seen
+                        const int at = key + 64 * hf + 32 * c, h = pos - at, g = first - at;
                         const uint32_t see = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1) &
                                              (g <= 0 ? ~0u : g > 31 ? 0u : ~0u << g);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (!(see >> k & 1)) v[k] = neg ? INFINITY : -INFINITY;
+                            if (!(see >> k & 1)) v[k] = -INFINITY;
                     }
                 };
-                auto factor = [&](int c, int k) {  // of columns 32 c + 4 k ..
-                    return S::kQuant ? lds4(ksc + 128 * c + 16 * k) : make_float4(sc, sc, sc, sc);
-                };
-                auto row_max = [&](auto masked) {
-                    float mx = kNoMax;
+                float mx = kNoMax;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t vr[32];
-                        tmem_ld_x32(ts + 32 * c, vr);
-                        tmem_wait_ld32(vr);
-                        float* v = reinterpret_cast<float*>(vr);
-                        scores(v, c, masked);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t vr[32];
+                    scores(vr, c);
+                    const float* v = reinterpret_cast<const float*>(vr);
+                    float m0 = kNoMax, m1 = kNoMax;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = factor(c, k);
-                            mx = max3(mx, v[4 * k] * f.x, v[4 * k + 1] * f.y);
-                            mx = max3(mx, v[4 * k + 2] * f.z, v[4 * k + 3] * f.w);
-                        }
+                    for (int k = 0; k < 8; ++k) {
+                        m0 = max3(m0, v[4 * k], v[4 * k + 1]);
+                        m1 = max3(m1, v[4 * k + 2], v[4 * k + 3]);
                     }
-                    return mx;
-                };
-                auto raise = [&] {
+                    mx = max3(mx, m0, m1);
+                }
+                if (!S::kQuant) mx *= sc;
+                int raise;
+                asm volatile(
+                    "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
+                    " selp.b32 %0, 1, 0, q;\n}"
+                    : "=r"(raise)
+                    : "r"((int)(mx > m + 8.0f)), "r"(2 + x)
+                    : "memory");
+                if (raise) {
+                    top[hf * kTileRows] = mx;
+                    stream_sync();
+                    mx = fmaxf(top[0], top[kTileRows]);
                     // (a little above the largest score, so that no rounding of a product lets the exact
-                    // one in the pass come out above it)
-                    const float mx = inner ? row_max(std::false_type{}) : row_max(std::true_type{}),
-                                mn = mx > m ? mx + fabsf(mx) * 1.2e-7f : m, a = ex2(m - mn);
+                    // one in the fma come out above it)
+                    const float mn = mx > m ? mx + fabsf(mx) * 1.2e-7f : m, a = ex2(m - mn);
                     m = mn;
                     l *= a;
-                    if (any) {  // P V of the tile before is done: S of this one came after it
+                    if (i > beg) {  // P V of the tile before is done: S of this one came after it
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(to + c, o);
-                            tmem_wait_ld32(o);
+                        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_x16(to + c, o);
+                            tmem_wait_ld16(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                            tmem_st_x32(to + c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                            tmem_st_x16(to + c, o);
                         }
                     }
-                };
-                // One pass with the maximum as it stands; where a score exceeds it by 2^8 (S is still
-                // whole) the maximum is raised and the pass done once more.
-                if (!any) raise();
-                uint32_t pk[64];
-                float l0, l1;
-                auto pass = [&](auto masked) {  // the largest exponent
-                    float t0 = kNoMax, t1 = kNoMax;
-                    l0 = l1 = 0.0f;
-                    uint32_t vr[2][32];
-                    tmem_ld_x32(ts, vr[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld32(vr[c & 1]);
-                        if (c < 3) tmem_ld_x32(ts + 32 * (c + 1), vr[(c + 1) & 1]);
-                        float* v = reinterpret_cast<float*>(vr[c & 1]);
-                        scores(v, c, masked);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = factor(c, k);
-                            float* e = v + 4 * k;
-                            fma2(e[0], e[1], f.x, f.y, -m);
-                            fma2(e[2], e[3], f.z, f.w, -m);
-                            t0 = max3(t0, e[0], e[1]);
-                            t1 = max3(t1, e[2], e[3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) e[j] = ex2(e[j]);
-                            add2(l0, l1, e[0], e[1]);
-                            add2(l0, l1, e[2], e[3]);
-                            if (S::kQuant) {
-                                const float4 g = lds4(ksc + 512 + 128 * c + 16 * k);
-                                mul2(e[0], e[1], g.x, g.y);
-                                mul2(e[2], e[3], g.z, g.w);
-                            }
-                            pk[16 * c + 2 * k] = bf16x2_of(e[0], e[1]);
-                            pk[16 * c + 2 * k + 1] = bf16x2_of(e[2], e[3]);
-                        }
-                    }
-                    return fmaxf(t0, t1);
-                };
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    const float t = inner ? pass(std::false_type{}) : pass(std::true_type{});
-                    if (k == 1 || !__any_sync(0xFFFFFFFFu, t > 8.0f)) break;
-                    raise();
                 }
-                any = true;
-                tmem_st_x32(ts, pk);
-                tmem_st_x32(ts + 32, pk + 32);
-                l += l0 + l1;
+                if (S::kQuant) wait(S::kBarFull + vk % kSlots, vk / kSlots);  // for the value scales
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t vr[32], pk[16];
+                    scores(vr, c);
+                    float* v = reinterpret_cast<float*>(vr);
+                    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float* e = v + 4 * k;
+                        if (S::kQuant) {
+                            add2(e[0], e[1], -m, -m);
+                            add2(e[2], e[3], -m, -m);
+                        } else {
+                            fma2(e[0], e[1], sc, sc, -m);
+                            fma2(e[2], e[3], sc, sc, -m);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) e[j] = ex2(e[j]);
+                        add2(l0, l1, e[0], e[1]);
+                        add2(l0, l1, e[2], e[3]);
+                        if (S::kQuant) {
+                            const float4 f = lds4(ksc + 512 + 128 * c + 16 * k);
+                            mul2(e[0], e[1], f.x, f.y);
+                            mul2(e[2], e[3], f.z, f.w);
+                        }
+                        pk[2 * k] = bf16x2_of(e[0], e[1]);
+                        pk[2 * k + 1] = bf16x2_of(e[2], e[3]);
+                    }
+                    // over the first of the half's own scores, which have been read
+                    tmem_st_x16(ts + 64 * hf + 16 * c, pk);
+                    l += l0 + l1;
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::kBarPf + x));
             }
+            const bool any = beg < end;
             tiles0 += s.t1 - s.t0;
             if (any) wait(S::kBarOd + x, n_od++);
+            // maxima and sums of the halves (and, with one row tile, of both streams)
+            ml[(2 * x + hf) * kTileRows + r] = make_float2(m, l);
+            if (s.split) all_sync();
+            else stream_sync();
             tc_fence_after();
-            // The CTA's own result of the stretch: the stream's, or (one row tile) both streams', of
-            // which each warpgroup takes half of the columns.
-            constexpr int kCw = D / 2;  // columns at a time
-            const int cb = s.split ? x * kCw : 0, ce = s.split ? cb + kCw : D;
-            float M = m, L = l, a0 = 1.0f, a1 = 0.0f;
-            bool use0 = any, use1 = false;
+            // The CTA's own result of the stretch, unnormalised: a0 * (this stream's output), or with one
+            // row tile a0 * (A's) + a1 * (B's).  This thread takes the columns [cb, ce) of its row.
+            float M = m, L = ml[2 * x * kTileRows + r].y + ml[(2 * x + 1) * kTileRows + r].y, a0 = 1.0f, a1 = 0.0f;
+            bool use0 = any, use1 = false;  // (the same for the whole warp: by the stretch, not by a row's values)
             uint32_t o0 = to, o1 = to;
+            int cb = hf * (D / 2), ce = cb + D / 2;
             if (s.split) {
-                ml[x * kTileRows + r] = make_float2(m, l);
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                tc_fence_after();
-                const float2 e0 = ml[r], e1 = ml[kTileRows + r];
+                constexpr int kQ = D / 4 < 32 ? 32 : D / 4;
+                cb = min(D, (2 * x + hf) * kQ);
+                ce = min(D, cb + kQ);
+                const float2 e0 = ml[r], e1 = ml[2 * kTileRows + r];
                 M = fmaxf(e0.x, e1.x);
                 a0 = ex2(e0.x - M);
                 a1 = ex2(e1.x - M);
-                L = e0.y * a0 + e1.y * a1;
+                L = (e0.y + ml[kTileRows + r].y) * a0 + (e1.y + ml[3 * kTileRows + r].y) * a1;
                 use0 = s.act(0, s.t0);
                 use1 = s.act(1, s.t0 + 1);
                 o0 = trow + 256;
                 o1 = trow + 384;
             }
-            auto own = [&](int col, float* f) {  // columns col .. col + 31, unnormalised
-                uint32_t o[32];
+            auto own = [&](int col, float* f) {  // columns col .. col + 15
+                uint32_t o[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = 0.0f;
-                if (use0) {  // (the same for the whole warp: it goes by the stretch, not by a row's values)
-                    tmem_ld_x32(o0 + col, o);
-                    tmem_wait_ld32(o);
+                for (int e = 0; e < 16; ++e) f[e] = 0.0f;
+                if (use0) {
+                    tmem_ld_x16(o0 + col, o);
+                    tmem_wait_ld16(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * a0;
+                    for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]) * a0;
                 }
                 if (use1) {
-                    tmem_ld_x32(o1 + col, o);
-                    tmem_wait_ld32(o);
+                    tmem_ld_x16(o1 + col, o);
+                    tmem_wait_ld16(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * a1;
+                    for (int e = 0; e < 16; ++e) f[e] += __uint_as_float(o[e]) * a1;
                 }
             };
             auto finish = [&](const float* f, int col, float inv) {
-                uint32_t e[16];
+                uint32_t e[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) e[k] = bf16x2_of(f[2 * k] * inv, f[2 * k + 1] * inv);
-                put(e, orow, col);
+                for (int k = 0; k < 8; ++k) e[k] = bf16x2_of(f[2 * k] * inv, f[2 * k + 1] * inv);
+                put(e, col);
             };
             bool join = false;
             const int c = blockIdx.x;
             int c0 = c, c1 = c;
+            const bool stats = s.split ? x == 0 && hf == 0 : hf == 0;  // the thread that speaks for its row
             if (!whole) {
                 // A partial result; the CTA that comes last to the unit joins them.  If the others
                 // have all come its own need not go through memory.
@@ -656,24 +670,24 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(arrived) : "memory");
                     *last_flag = n == others;
                 }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                all_sync();
                 join = *last_flag;
                 if (!join) {
                     float* part = p.part + ((int64_t)kPartSlots * c + (c == c0)) * S::kPart + (s.split ? 0 : x) * S::kPartStream;
                     float4* po = reinterpret_cast<float4*>(part);
 #pragma unroll 1
-                    for (int col = cb; col < ce; col += 32) {
-                        float f[32];
+                    for (int col = cb; col < ce; col += 16) {
+                        float f[16];
                         own(col, f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < 4; ++e)
                             __stcg(po + (col / 4 + e) * kTileRows + r, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
                     }
-                    if (!s.split || x == 0) __stcg(reinterpret_cast<float2*>(part + kTileRows * D) + r, make_float2(M, L));
+                    if (stats) __stcg(reinterpret_cast<float2*>(part + kTileRows * D) + r, make_float2(M, L));
                     __threadfence();
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    all_sync();
                     if (threadIdx.x == 128) *last_flag = atomicAdd(arrived, 1u) == others;
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    all_sync();
                     join = *last_flag;
                 }
                 if (join) {
@@ -684,8 +698,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             if (whole) {
                 const float inv = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll 1
-                for (int col = cb; col < ce; col += 32) {
-                    float f[32];
+                for (int col = cb; col < ce; col += 16) {
+                    float f[16];
                     own(col, f);
                     finish(f, col, inv);
                 }
@@ -706,48 +720,44 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 }
                 const float inv = Lj > 0.0f ? 1.0f / Lj : 0.0f;
 #pragma unroll 1
-                for (int col = cb; col < ce; col += 32) {
-                    float f[32];
+                for (int col = cb; col < ce; col += 16) {
+                    float f[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = 0.0f;
+                    for (int e = 0; e < 16; ++e) f[e] = 0.0f;
 #pragma unroll 1
                     for (int k = c0; k <= c1; ++k) {
                         const float a = ex2(stat(k).x - Mj);
-                        float g[32];
+                        float g[16];
                         if (k == c) own(col, g);
                         else {
                             const float4* q = reinterpret_cast<const float4*>(part(k)) + (col / 4) * kTileRows + r;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
+                            for (int e = 0; e < 4; ++e) {
                                 const float4 v = __ldcg(q + e * kTileRows);
                                 g[4 * e] = v.x, g[4 * e + 1] = v.y, g[4 * e + 2] = v.z, g[4 * e + 3] = v.w;
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] += g[e] * a;
+                        for (int e = 0; e < 16; ++e) f[e] += g[e] * a;
                     }
                     finish(f, col, inv);
                 }
                 M = Mj;
                 L = Lj;
             }
-            if ((whole || join) && orow >= 0 && p.a.lse && (!s.split || x == 0))
+            if ((whole || join) && orow >= 0 && p.a.lse && stats)
                 p.a.lse[orow] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
-            // Both streams may have read both outputs, and the flags: the next unit's products (which
-            // wait for P of its first tiles) and flags come after this point.
+            // Every thread has read the outputs, sums and flags that are not its own: the next unit's products
+            // (which wait for P of its first tiles), sums and flags come after this point.
             tc_fence_before();
-            if (s.split || !whole) asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (s.split || !whole) all_sync();
+            else stream_sync();
         } while (next_unit(p, sh, u, unit0));
     } else {
         // -------------------------------------------------------------- conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
         if constexpr (S::kQuant) {
-            const int r = threadIdx.x - 384;  // row (key) of the tile
-            const float sc = p.scale_log2 < 0.0f ? fminf(p.scale_log2, -1e-37f) : fmaxf(p.scale_log2, 1e-37f);
-            auto key_scale = [&](float s) {  // of the scale's sign, and never 0
-                s *= sc;
-                return sc < 0.0f ? fminf(s, -1e-37f) : fmaxf(s, 1e-37f);
-            };
+            const int r = threadIdx.x - 640;  // row (key) of the tile
             uint32_t it = 0, tiles = 0;
             bool ok = true;
             do {
@@ -767,16 +777,15 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                         for (int c = 0; c < kIn; ++c)
                             raw[c] = *reinterpret_cast<const uint4*>(slot + S::kRawOff + r * S::kRowB + ((c ^ sw) << 4));
-                        // the keys' scales take the call's along (not 0: see the streams); nobody's key
-                        // may have anything in its slot
+                        // the keys' scales take the call's along; nobody's key may have anything in its slot
                         float* scale = reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB) + kv * kTk + r;
-                        if (!kv) *scale = seen ? key_scale(*scale) : sc;
+                        if (!kv) *scale *= p.scale_log2;
                         else if (!seen) *scale = 0.0f;
                         if (!seen) {
 #pragma unroll
                             for (int c = 0; c < kIn; ++c) raw[c] = make_uint4(0, 0, 0, 0);
                         }
-                        if (S::kInPlace && FMT == kKvInt4) asm volatile("bar.sync 2, 128;" ::: "memory");
+                        if (S::kInPlace && FMT == kKvInt4) asm volatile("bar.sync 4, 128;" ::: "memory");
                         constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;  // output chunks of an input chunk
 #pragma unroll
                         for (int c = 0; c < kIn; ++c) {
@@ -852,7 +861,7 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
         if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
         regs.store(at.numRegs, std::memory_order_relaxed);
     }
-    const int need = S::kRegCtl + 2 * S::kRegStream + (S::kQuant ? S::kRegConv : 0);
+    const int need = S::kRegCtl + 4 * S::kRegStream + (S::kQuant ? S::kRegConv : 0);
     if (need * 128 > regs.load(std::memory_order_relaxed) * S::kThreads) return cudaErrorInvalidConfiguration;
     attn_tiles_kernel<FMT, D><<<sm_count(), S::kThreads, S::kSmem, st>>>(p);
     return cudaGetLastError();

@@ -7,20 +7,21 @@ namespace {
 
 // Sequences of at most this many rows (new tokens x query heads per key/value
 // head) run on the warp-level kernel, longer ones on the tcgen05 kernel.
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 64;
 
 // Which kernels a call needs, from what the host knows of its sequences.  A
 // sequence's rows are only known on the device, so with both launched each
 // kernel takes its own; a single one takes all.
 struct Kernels {
     bool rows, tiles;
+    bool eight;  // units of eight rows on the warp-level kernel
 };
 Kernels kernels_for(const moe_kv_dims_t& d) {
     const int64_t G = d.H / d.H_kv;
     int64_t most = d.max_new > 0 ? std::min(d.max_new, d.T) : d.T;
-    if (most * G <= kFewRows) return {true, false};
-    if (d.B == 1) return {false, true};
-    return {true, true};
+    if (most * G <= kFewRows) return {true, false, most * G <= 8};
+    if (d.B == 1) return {false, true, false};
+    return {true, true, G <= 8};
 }
 
 // Workspace: the header, the arrival counters of the joins (at a place that no
@@ -64,7 +65,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
         at += align256(attn_tiles_part_bytes(a.d));
     }
     if (k.rows && e == cudaSuccess)
-        e = launch_attn_rows(a, 0, k.tiles ? kFewRows : most, reinterpret_cast<float*>(ws + at),
+        e = launch_attn_rows(a, 0, k.tiles ? kFewRows : most, k.eight, reinterpret_cast<float*>(ws + at),
                              reinterpret_cast<unsigned*>(ws + kCountersAt), st);
     return e;
 }

@@ -255,7 +255,8 @@ bool make_kv_map(CUtensorMap* m, const void* base, const AttnArgs& a, int box_by
 // Launchers.  `part` and `counters` lie in the workspace; the counters are zero
 // between calls.
 size_t attn_rows_part_bytes(const moe_kv_dims_t& d);
-cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+// `eight`: units of eight rows instead of sixteen (at most eight query heads per key/value head)
+cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
                              unsigned* counters, cudaStream_t st);
 size_t attn_tiles_part_bytes(const moe_kv_dims_t& d);
 cudaError_t launch_attn_tiles(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,

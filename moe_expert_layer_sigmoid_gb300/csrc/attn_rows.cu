@@ -724,11 +724,9 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
 }
 
 template <int FMT, int D>
-cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
                        unsigned* counters, cudaStream_t st) {
-    // eight rows hold the tokens of a decode step when a group has at most eight query heads; a
-    // sequence with more rows takes more units (and reads its keys again, from L2)
-    return a.d.H / a.d.H_kv <= 8 ? launch<FMT, D, 1>(a, rows_lo, rows_hi, part, counters, st)
+    return eight ? launch<FMT, D, 1>(a, rows_lo, rows_hi, part, counters, st)
                                  : launch<FMT, D, 2>(a, rows_lo, rows_hi, part, counters, st);
 }
 
@@ -739,19 +737,19 @@ size_t attn_rows_part_bytes(const moe_kv_dims_t& d) {
     return (size_t)(2 * sm_count()) * std::max(3 * 8, 2 * 16) * (d.D + 2) * sizeof(float);
 }
 
-cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
                              unsigned* counters, cudaStream_t st) {
     const bool wide = a.d.D == 128;
     switch (a.d.format) {
         case kKvBf16:
-            return wide ? launch_for<kKvBf16, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch_for<kKvBf16, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvBf16, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
+                        : launch_for<kKvBf16, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
         case kKvE4m3:
-            return wide ? launch_for<kKvE4m3, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch_for<kKvE4m3, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvE4m3, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
+                        : launch_for<kKvE4m3, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
         case kKvInt4:
-            return wide ? launch_for<kKvInt4, 128>(a, rows_lo, rows_hi, part, counters, st)
-                        : launch_for<kKvInt4, 64>(a, rows_lo, rows_hi, part, counters, st);
+            return wide ? launch_for<kKvInt4, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
+                        : launch_for<kKvInt4, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
         default: return cudaErrorInvalidValue;
     }
 }

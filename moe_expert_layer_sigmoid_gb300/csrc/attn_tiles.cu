@@ -17,21 +17,21 @@
 // keys per column) overwrites S, each half of the keys its own half's first columns; the next S of a stream is issued after the
 // P V that reads P, and the tensor core runs one thread's products in order.
 //
-// Two threads own a row, each half of a tile's keys, no shuffles.  S is read twice, in pieces of 32
-// columns, for the maximum and for the weights: that keeps registers few (shared memory leaves little
-// L1 to spill to) and the code short (a CTA runs most of it a few times only).  The running
-// maximum is raised only when a score exceeds it by 2^8: a barrier with a vote decides, and in few
-// tiles the halves exchange their maxima and O is rescaled (read, scaled and written back in TMEM);
-// when S of tile i is ready, P V of tile i - 1 is too, so the row's threads may touch O without a
-// further wait.
+// Two threads own a row, each half of a tile's keys, no shuffles.  A tile takes one pass over S, with the
+// running maximum as it stands; a barrier with a vote tells whether some score exceeds it by 2^8, and in
+// those few tiles (S is still whole: P is stored after the vote) the halves exchange their maxima, O is
+// rescaled (read, scaled and written back in TMEM) and the pass done again.  When S of tile i is ready,
+// P V of tile i - 1 is too, so O may be touched without a further wait.  The loop's issue slots and
+// registers are what the tensor core waits for most, so S is read 32 columns at a time and the
+// arithmetic is packed two to an instruction.
 //
-// Quantised caches: TMA brings the codes, a warpgroup turns them into bf16 in
-// place (the codes of a row lie where only the thread that converts it writes, or
-// the group synchronises between reading and writing).  Key scales multiply the
-// scores, value scales the weights, so codes enter the products exactly.
+// Quantised caches: TMA brings the codes to a ring of their own, two warpgroups (one for keys, one for
+// values) turn them into bf16 tiles.  Key scales multiply the scores, value scales the weights, so
+// codes enter the products exactly.
 //
 // Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-11 stream A, 12-19 stream B (in each
-// four warps for the first 64 keys of a tile and four for the last), 20-23 conversion.
+// four warps for the first 64 keys of a tile and four for the last), 20-23 conversion
+// of keys, 24-27 of values.
 #include <atomic>
 #include <type_traits>
 
@@ -43,37 +43,41 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kTk = 128;  // keys of a tile
-constexpr int kSlots = 4;  // tiles of keys or values in shared memory
 
 template <int FMT, int D>
 struct TilesShape {
     static constexpr bool kQuant = FMT != kKvBf16;
-    static constexpr int kThreads = kQuant ? 768 : 640;
+    static constexpr int kThreads = kQuant ? 896 : 640;
     static constexpr int kRowB = kv_row_bytes(FMT, D);
     static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;
     static constexpr int kTileB = kTk * D * 2;                // a bf16 tile
-    // where the codes land in a slot: in the place of the second column block (E4M3, D = 128: row
-    // r's codes under row r's values), over the tile (int4, D = 128), behind it (D = 64)
-    static constexpr bool kInPlace = kQuant && D == 128;
-    static constexpr int kRawOff = FMT == kKvE4m3 && D == 128 ? kTileB / 2 : kInPlace ? 0 : kTileB;
-    static constexpr int kSlotB = kTileB + (kQuant && !kInPlace ? kTk * kRowB : 0);
-    static constexpr int kScB = kQuant ? 2 * kTk * 4 : 0;     // key and value scales of a tile
+    static constexpr int kSlots = kQuant ? 3 : 4;             // bf16 tiles of keys or values
+    // Tiles of codes.  No more than bf16 slots: then a tile's codes are only there once the tile three
+    // before it is converted, so the two conversion groups cannot be a whole round of slots apart and
+    // take one phase of a slot's barrier for another.
+    static constexpr int kRaws = kQuant ? 3 : 0;
+    static_assert(kRaws <= kSlots, "phases");
+    static constexpr int kRawB = kTk * kRowB;
+    // Key and value scales of a tile.  Four slots: while V of tile i is in use (K of tile i + 2 would take its
+    // place) no codes after K of tile i + 3 are loaded.
+    static constexpr int kScB = kQuant ? 2 * kTk * 4 : 0;
     static constexpr int kScSlots = 4;
     // registers per thread: control, streams, conversion; in 128-thread groups they add up to
-    // what the launch holds (96 x 640 or 80 x 768)
-    static constexpr int kRegCtl = kQuant ? 64 : 96, kRegStream = kQuant ? 88 : 96, kRegConv = 64;
-    static_assert(kRegCtl + 4 * kRegStream + (kQuant ? kRegConv : 0) <= 480, "register split");
+    // what the launch holds (96 x 640 or 72 x 896)
+    static constexpr int kRegCtl = kQuant ? 56 : 96, kRegStream = kQuant ? 88 : 96, kRegConv = 48;
+    static_assert(kRegCtl + 4 * kRegStream + (kQuant ? 2 * kRegConv : 0) <= (kQuant ? 504 : 480), "register split");
     static constexpr int kOffQ = 0;
     static constexpr int kOffKv = kOffQ + 2 * kTileRows * D * 2;
-    static constexpr int kOffSc = kOffKv + kSlots * kSlotB;
-    // output rows on their way from registers to coalesced stores: 32 rows x 32 bytes per warp
+    static constexpr int kOffRaw = kOffKv + kSlots * kTileB;
+    static constexpr int kOffSc = kOffRaw + kRaws * kRawB;
+    // output rows on their way from registers to coalesced stores: 16 rows x 32 bytes per warp
     static constexpr int kOffStage = kOffSc + kScSlots * kScB;
-    static constexpr int kOffMl = kOffStage + 16 * 1024;  // the streams' maxima and sums: [stream][half][row]
+    static constexpr int kOffMl = kOffStage + 16 * 512;  // the streams' maxima and sums: [stream][half][row]
     static constexpr int kOffBar = kOffMl + 4 * kTileRows * 8;
-    // barriers: FULL, EMPTY, RAW [kSlots]; SF, PF, OD [2]; QF, QE, TD
-    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRaw = 2 * kSlots, kBarSf = 3 * kSlots,
-                         kBarPf = kBarSf + 2, kBarOd = kBarPf + 2, kBarQf = kBarOd + 2,
-                         kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
+    // barriers: FULL, EMPTY [kSlots]; RAWF, RAWE [kRaws]; SF, PF, OD [2]; QF, QE, TD
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRawF = 2 * kSlots, kBarRawE = kBarRawF + kRaws,
+                         kBarSf = kBarRawE + kRaws, kBarPf = kBarSf + 2, kBarOd = kBarPf + 2,
+                         kBarQf = kBarOd + 2, kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmem = kOffMisc + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -88,34 +92,39 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// (a0, a1) = (a0, a1) * (b0, b1), (a0 * s0 + b, a1 * s1 + b) and (a0 + b0, a1 + b1), one instruction each
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
-    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n"
-        " mov.b64 {%0, %1}, a;\n}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1));
+// Two floats in one 64-bit register, for the packed forms: one instruction for both.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(uint32_t lo, uint32_t hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
-__device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float b) {
-    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 c, {%4, %4};\n"
-        " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(s0), "f"(s1), "f"(b));
+__device__ __forceinline__ f2 pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void split(f2 x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
-    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
-        " mov.b64 {%0, %1}, a;\n}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-    float4 f;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
-    return f;
+__device__ __forceinline__ void lds_f2x2(uint32_t addr, f2& a, f2& b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -173,6 +182,7 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(TilesShape<FMT, D>::kThreads, 1)
 attn_tiles_kernel(const __grid_constant__ AttnParams p) {
     using S = TilesShape<FMT, D>;
+    constexpr int kSlots = S::kSlots;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -186,7 +196,10 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(bar(S::kBarFull + s), S::kQuant ? 4 : 1);
             mbar_init(bar(S::kBarEmpty + s), 1);
-            mbar_init(bar(S::kBarRaw + s), 1);
+        }
+        for (int s = 0; s < S::kRaws; ++s) {
+            mbar_init(bar(S::kBarRawF + s), 1);
+            mbar_init(bar(S::kBarRawE + s), 4);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(S::kBarSf + x), 1);
@@ -221,6 +234,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             const int page = 1 << p.c.page_log2;
             const int box_rows = page < kTk ? page : kTk;
             const int boxes = kTk / box_rows;
+            constexpr uint32_t kRing = S::kQuant ? S::kRaws : kSlots;
             uint32_t it = 0;   // slots filled
             uint32_t tiles = 0, n_q = 0;
             bool ok = true;
@@ -275,19 +289,19 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     const int at = key & (page - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-                        const int s = it % kSlots;
-                        if (!mbar_wait(bar(S::kBarEmpty + s), ((it / kSlots) & 1) ^ 1, abort_flag, hdr)) {
+                        const int s = it % kRing;
+                        if (!mbar_wait(bar((S::kQuant ? S::kBarRawE : S::kBarEmpty) + s), ((it / kRing) & 1) ^ 1, abort_flag, hdr)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t done = bar((S::kQuant ? S::kBarRaw : S::kBarFull) + s);
+                        const uint32_t done = bar((S::kQuant ? S::kBarRawF : S::kBarFull) + s);
                         const uint32_t sc_bytes = S::kQuant ? box_rows * 4 : 0;
                         if (lane == 0) mbar_expect_tx(done, n_live * (box_rows * S::kRowB + sc_bytes));
                         __syncwarp();
                         if (live) {
                             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
-                            const uint32_t d = sbase + S::kOffKv + s * S::kSlotB +
-                                               (S::kQuant ? S::kRawOff : 0) + lane * box_rows * S::kBoxB;
+                            const uint32_t d = sbase + (S::kQuant ? S::kOffRaw + s * S::kRawB : S::kOffKv + s * S::kTileB) +
+                                               lane * box_rows * S::kBoxB;
 #pragma unroll
                             for (int h = 0; h < S::kRowB / S::kBoxB; ++h)
                                 tma_load_4d(d + h * kTk * S::kBoxB, tm, h * S::kBoxB / (S::kQuant ? 1 : 2), at, hk, id, done);
@@ -302,8 +316,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             } while (ok && next_unit(p, sh, u, unit0));
             if (!ok && n_q) mbar_drain(bar(S::kBarQf), (n_q - 1) & 1, hdr);
             if (!ok)  // no copy may be in flight when the CTA ends
-                for (uint32_t k = it > kSlots ? it - kSlots : 0; k < it; ++k)
-                    mbar_drain(bar((S::kQuant ? S::kBarRaw : S::kBarFull) + k % kSlots), (k / kSlots) & 1, hdr);
+                for (uint32_t k = it > kRing ? it - kRing : 0; k < it; ++k)
+                    mbar_drain(bar((S::kQuant ? S::kBarRawF : S::kBarFull) + k % kRing), (k / kRing) & 1, hdr);
         } else if (warp == 1) {
             // ---------------------------------------------------------- products
             // The whole warp follows the loop, so that its values are uniform; one thread issues.
@@ -326,7 +340,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
             };
             auto qk = [&](int x, uint32_t k) {
-                const uint32_t a = q_lo + x * (kTileRows * D * 2 / 16), b = k_lo + (k % kSlots) * (S::kSlotB / 16);
+                const uint32_t a = q_lo + x * (kTileRows * D * 2 / 16), b = k_lo + (k % kSlots) * (S::kTileB / 16);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
@@ -338,7 +352,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
             };
             auto pv = [&](int x, uint32_t k) {
-                const uint32_t b = v_lo + (k % kSlots) * (S::kSlotB / 16);
+                const uint32_t b = v_lo + (k % kSlots) * (S::kTileB / 16);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kTk / 16; ++ks)
@@ -419,11 +433,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         const int r = (warp & 3) * 32 + lane;                 // row
         const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 lanes
         const uint32_t ts = trow + x * 128, to = trow + 256 + x * 128;
-        // a negative scale turns the scores' sign; not 0, so that a masked score stays infinite
+        // (not 0, so that a masked score stays infinite)
         const bool neg = p.scale_log2 < 0.0f;
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const int G = p.a.d.H / p.a.d.H_kv, half = p.c.tq / 2;
-        uint8_t* stage = smem + S::kOffStage + (warp - 4) * 1024;
+        uint8_t* stage = smem + S::kOffStage + (warp - 4) * 512;
         float2* ml = reinterpret_cast<float2*>(smem + S::kOffMl);
         float* top = reinterpret_cast<float*>(ml + 2 * x * kTileRows) + r;  // + half * rows: halves' maxima
         uint32_t n_sf = 0, n_od = 0, tiles0 = 0;  // tiles0: tiles of the CTA before this stretch
@@ -442,22 +456,24 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             pos = live ? v.len - v.n + tok : -1;
             first = p.a.d.window ? max(0, pos - p.a.d.window + 1) : 0;
         };
-        // 16 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory: each two
-        // lanes store 32 bytes of a row
+        // 16 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory, 16 rows at a time:
+        // each two lanes store 32 bytes of a row
         auto put = [&](const uint32_t* e, int col) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) =
-                    make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
-            __syncwarp();
+            for (int h = 0; h < 2; ++h) {
+                if (lane >> 4 == h) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int rr = 16 * k + (lane >> 1), c = lane & 1;
-                const int64_t row = __shfl_sync(0xFFFFFFFFu, orow, rr);
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(stage + (lane & 15) * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) =
+                            make_uint4(e[4 * k], e[4 * k + 1], e[4 * k + 2], e[4 * k + 3]);
+                }
+                __syncwarp();
+                const int rr = lane >> 1, c = lane & 1;
+                const int64_t row = __shfl_sync(0xFFFFFFFFu, orow, 16 * h + rr);
                 const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 32 + ((c ^ ((rr >> 2) & 1)) << 4));
                 if (row >= 0) *reinterpret_cast<uint4*>(p.a.out + row * D + col + 8 * c) = v;
+                __syncwarp();
             }
-            __syncwarp();
         };
         do {
             const Stretch s = stretch(p, sh, u, unit0);
@@ -485,7 +501,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 if (!S::kQuant && (key < key0 || key + kTk > key1) && (key >= clear0 || (x == 1 && i < s.lo[0]))) {
                     wait(S::kBarFull + vk % kSlots, vk / kSlots);
                     if (key + r < key0 || key + r >= key1) {
-                        uint8_t* z = smem + S::kOffKv + (vk % kSlots) * S::kSlotB + r * 128;
+                        uint8_t* z = smem + S::kOffKv + (vk % kSlots) * S::kTileB + r * 128;
 #pragma unroll
                         for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c)
                             *reinterpret_cast<uint4*>(z + (c / 8) * (128 * 128) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -496,19 +512,12 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 // quantised: the half's key scales (times the call's; in place since before the products
                 // that S comes from), then its value scales
                 const uint32_t ksc = sbase + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB + 256 * hf;
-                // 32 scores of the half's 64, masked; quantised ones in the exponent's domain
+                // 32 of the half's 64 scores, masked; a negative scale turns their sign
                 auto scores = [&](uint32_t* vr, int c) {
                     tmem_ld_x32(ts + 64 * hf + 32 * c, vr);
                     tmem_wait_ld32(vr);
                     float* v = reinterpret_cast<float*>(vr);
-                    if (S::kQuant) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = lds4(ksc + 128 * c + 16 * k);
-                            mul2(v[4 * k], v[4 * k + 1], f.x, f.y);
-                            mul2(v[4 * k + 2], v[4 * k + 3], f.z, f.w);
-                        }
-                    } else if (neg) {
+                    if (neg) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = -v[k];
                     }
@@ -522,81 +531,98 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                             if (!(see >> k & 1)) v[k] = -INFINITY;
                     }
                 };
-                float mx = kNoMax;
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t vr[32];
-                    scores(vr, c);
-                    const float* v = reinterpret_cast<const float*>(vr);
-                    float m0 = kNoMax, m1 = kNoMax;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        m0 = max3(m0, v[4 * k], v[4 * k + 1]);
-                        m1 = max3(m1, v[4 * k + 2], v[4 * k + 3]);
-                    }
-                    mx = max3(mx, m0, m1);
-                }
-                if (!S::kQuant) mx *= sc;
-                int raise;
-                asm volatile(
-                    "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
-                    " selp.b32 %0, 1, 0, q;\n}"
-                    : "=r"(raise)
-                    : "r"((int)(mx > m + 8.0f)), "r"(2 + x)
-                    : "memory");
-                if (raise) {
-                    top[hf * kTileRows] = mx;
-                    stream_sync();
-                    mx = fmaxf(top[0], top[kTileRows]);
-                    // (a little above the largest score, so that no rounding of a product lets the exact
-                    // one in the fma come out above it)
-                    const float mn = mx > m ? mx + fabsf(mx) * 1.2e-7f : m, a = ex2(m - mn);
-                    m = mn;
-                    l *= a;
-                    if (i > beg) {  // P V of the tile before is done: S of this one came after it
-#pragma unroll 1
-                        for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
-                            uint32_t o[16];
-                            tmem_ld_x16(to + c, o);
-                            tmem_wait_ld16(o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                            tmem_st_x16(to + c, o);
-                        }
-                    }
-                }
+                // the factors of four of them into the exponent's domain
+                auto factors = [&](int c, int k, f2& f0, f2& f1) {
+                    if (S::kQuant) lds_f2x2(ksc + 128 * c + 16 * k, f0, f1);
+                    else f0 = f1 = pair(sc, sc);
+                };
                 if (S::kQuant) wait(S::kBarFull + vk % kSlots, vk / kSlots);  // for the value scales
+                uint32_t pk[32];
+                f2 l0, l1;
+                int raise = i == beg;
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t vr[32], pk[16];
-                    scores(vr, c);
-                    float* v = reinterpret_cast<float*>(vr);
-                    float l0 = 0.0f, l1 = 0.0f;
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    if (raise) {
+                        float mx = kNoMax;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t vr[32];
+                            scores(vr, c);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float* e = v + 4 * k;
-                        if (S::kQuant) {
-                            add2(e[0], e[1], -m, -m);
-                            add2(e[2], e[3], -m, -m);
-                        } else {
-                            fma2(e[0], e[1], sc, sc, -m);
-                            fma2(e[2], e[3], sc, sc, -m);
+                            for (int k = 0; k < 8; ++k) {
+                                f2 f0, f1;
+                                float e0, e1, e2, e3;
+                                factors(c, k, f0, f1);
+                                split(mul2(pair(vr[4 * k], vr[4 * k + 1]), f0), e0, e1);
+                                split(mul2(pair(vr[4 * k + 2], vr[4 * k + 3]), f1), e2, e3);
+                                mx = max3(mx, e0, e1);
+                                mx = max3(mx, e2, e3);
+                            }
                         }
+                        top[hf * kTileRows] = mx;
+                        stream_sync();
+                        mx = fmaxf(top[0], top[kTileRows]);
+                        // (a little above the largest score, so that no rounding of a product lets the exact
+                        // one in the fma come out above it)
+                        const float mn = mx > m ? mx + fabsf(mx) * 1.2e-7f : m, a = ex2(m - mn);
+                        m = mn;
+                        l *= a;
+                        if (i > beg) {  // P V of the tile before is done: S of this one came after it
+#pragma unroll 1
+                            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_x16(to + c, o);
+                                tmem_wait_ld16(o);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) e[j] = ex2(e[j]);
-                        add2(l0, l1, e[0], e[1]);
-                        add2(l0, l1, e[2], e[3]);
-                        if (S::kQuant) {
-                            const float4 f = lds4(ksc + 512 + 128 * c + 16 * k);
-                            mul2(e[0], e[1], f.x, f.y);
-                            mul2(e[2], e[3], f.z, f.w);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+                                tmem_st_x16(to + c, o);
+                            }
                         }
-                        pk[2 * k] = bf16x2_of(e[0], e[1]);
-                        pk[2 * k + 1] = bf16x2_of(e[2], e[3]);
                     }
-                    // over the first of the half's own scores, which have been read
-                    tmem_st_x16(ts + 64 * hf + 16 * c, pk);
-                    l += l0 + l1;
+                    const f2 nm = pair(-m, -m);
+                    float t0 = kNoMax, t1 = kNoMax;
+                    l0 = l1 = pair(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t vr[32];
+                        scores(vr, c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            f2 f0, f1;
+                            float e0, e1, e2, e3;
+                            factors(c, k, f0, f1);
+                            split(fma2(pair(vr[4 * k], vr[4 * k + 1]), f0, nm), e0, e1);
+                            split(fma2(pair(vr[4 * k + 2], vr[4 * k + 3]), f1, nm), e2, e3);
+                            t0 = max3(t0, e0, e1);
+                            t1 = max3(t1, e2, e3);
+                            f2 a = pair(ex2(e0), ex2(e1)), b = pair(ex2(e2), ex2(e3));
+                            l0 = add2(l0, a);
+                            l1 = add2(l1, b);
+                            if (S::kQuant) {
+                                lds_f2x2(ksc + 512 + 128 * c + 16 * k, f0, f1);
+                                a = mul2(a, f0);
+                                b = mul2(b, f1);
+                            }
+                            split(a, e0, e1);
+                            split(b, e2, e3);
+                            pk[16 * c + 2 * k] = bf16x2_of(e0, e1);
+                            pk[16 * c + 2 * k + 1] = bf16x2_of(e2, e3);
+                        }
+                    }
+                    asm volatile(
+                        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
+                        " selp.b32 %0, 1, 0, q;\n}"
+                        : "=r"(raise)
+                        : "r"((int)(fmaxf(t0, t1) > 8.0f)), "r"(2 + x)
+                        : "memory");
+                    if (!raise) break;
+                }
+                // over the first of the half's own scores
+                tmem_st_x32(ts + 64 * hf, pk);
+                {
+                    float a0, a1;
+                    split(add2(l0, l1), a0, a1);
+                    l += a0 + a1;
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -757,39 +783,37 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         // -------------------------------------------------------------- conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
         if constexpr (S::kQuant) {
-            const int r = threadIdx.x - 640;  // row (key) of the tile
-            uint32_t it = 0, tiles = 0;
+            const int r = threadIdx.x & 127, kv = warp >= 24;  // row (key) of the tile; keys or values
+            uint32_t it = kv, tiles = 0;
             bool ok = true;
             do {
                 int tile, end;
                 unit_share(p, sh, u, unit0, tile, end);
-                for (; tile < end; ++tile, ++tiles) {
+                for (; tile < end; ++tile, ++tiles, it += 2) {
                     const int key = (u.tile0 + tile) * kTk + r;
                     const bool seen = key >= u.key0 && key < u.key1;
+                    const int sl = it % kSlots, rw = it % S::kRaws;
+                    if (ok) ok = mbar_wait(bar(S::kBarRawF + rw), (it / S::kRaws) & 1, abort_flag, hdr);
+                    if (ok) ok = mbar_wait(bar(S::kBarEmpty + sl), ((it / kSlots) & 1) ^ 1, abort_flag, hdr);
+                    const uint8_t* raw = smem + S::kOffRaw + rw * S::kRawB + r * S::kRowB;
+                    uint8_t* slot = smem + S::kOffKv + sl * S::kTileB + r * 128;
+                    const int sw = S::kBoxB == 128 ? r & 7 : S::kBoxB == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+                    // the keys' scales take the call's along (its size, and not 0: see the streams); nobody's
+                    // key may have anything in its slot
+                    float* scale = reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB) + kv * kTk + r;
+                    if (!kv) *scale = seen ? fmaxf(*scale * fabsf(p.scale_log2), 1e-37f) : 1.0f;
+                    else if (!seen) *scale = 0.0f;
+                    constexpr int kIn = S::kRowB / 16, kAt = kIn < 4 ? kIn : 4;  // 16-byte chunks of codes: of a row, at a time
+                    constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;                 // output chunks of an input chunk
 #pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++it) {
-                        const int sl = it % kSlots;
-                        if (ok) ok = mbar_wait(bar(S::kBarRaw + sl), (it / kSlots) & 1, abort_flag, hdr);
-                        uint8_t* slot = smem + S::kOffKv + sl * S::kSlotB;
-                        constexpr int kIn = S::kRowB / 16;  // 16-byte chunks of a row's codes
-                        uint4 raw[kIn];
-                        const int sw = S::kBoxB == 128 ? r & 7 : S::kBoxB == 64 ? (r >> 1) & 3 : (r >> 2) & 1;
+                    for (int c0 = 0; c0 < kIn; c0 += kAt) {
+                        uint4 in4[kAt];
 #pragma unroll
-                        for (int c = 0; c < kIn; ++c)
-                            raw[c] = *reinterpret_cast<const uint4*>(slot + S::kRawOff + r * S::kRowB + ((c ^ sw) << 4));
-                        // the keys' scales take the call's along; nobody's key may have anything in its slot
-                        float* scale = reinterpret_cast<float*>(smem + S::kOffSc + (tiles % S::kScSlots) * S::kScB) + kv * kTk + r;
-                        if (!kv) *scale *= p.scale_log2;
-                        else if (!seen) *scale = 0.0f;
-                        if (!seen) {
+                        for (int c = 0; c < kAt; ++c)
+                            in4[c] = seen ? *reinterpret_cast<const uint4*>(raw + (((c0 + c) ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                            for (int c = 0; c < kIn; ++c) raw[c] = make_uint4(0, 0, 0, 0);
-                        }
-                        if (S::kInPlace && FMT == kKvInt4) asm volatile("bar.sync 4, 128;" ::: "memory");
-                        constexpr int kPer = FMT == kKvE4m3 ? 2 : 4;  // output chunks of an input chunk
-#pragma unroll
-                        for (int c = 0; c < kIn; ++c) {
-                            const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                        for (int c = 0; c < kAt; ++c) {
+                            const uint32_t in[4] = {in4[c].x, in4[c].y, in4[c].z, in4[c].w};
 #pragma unroll
                             for (int k = 0; k < kPer; ++k) {
                                 uint4 o;
@@ -798,13 +822,16 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                                                    e4m3_two(in[2 * k + 1], 0), e4m3_two(in[2 * k + 1], 2));
                                 else
                                     o = make_uint4(int4_two(in[k], 0), int4_two(in[k], 1), int4_two(in[k], 2), int4_two(in[k], 3));
-                                const int oc = c * kPer + k;
-                                *reinterpret_cast<uint4*>(slot + (oc / 8) * (128 * 128) + r * 128 + (((oc & 7) ^ (r & 7)) << 4)) = o;
+                                const int oc = (c0 + c) * kPer + k;
+                                *reinterpret_cast<uint4*>(slot + (oc / 8) * (128 * 128) + (((oc & 7) ^ (r & 7)) << 4)) = o;
                             }
                         }
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(S::kBarFull + sl));
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(S::kBarFull + sl));
+                        mbar_arrive(bar(S::kBarRawE + rw));
                     }
                 }
             } while (next_unit(p, sh, u, unit0));
@@ -861,7 +888,7 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
         if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
         regs.store(at.numRegs, std::memory_order_relaxed);
     }
-    const int need = S::kRegCtl + 4 * S::kRegStream + (S::kQuant ? S::kRegConv : 0);
+    const int need = S::kRegCtl + 4 * S::kRegStream + (S::kQuant ? 2 * S::kRegConv : 0);
     if (need * 128 > regs.load(std::memory_order_relaxed) * S::kThreads) return cudaErrorInvalidConfiguration;
     attn_tiles_kernel<FMT, D><<<sm_count(), S::kThreads, S::kSmem, st>>>(p);
     return cudaGetLastError();

@@ -174,7 +174,7 @@ _ALIASES = {torch.int16: _BITS16}
 def _dev(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _ALIASES.get(dtype, (dtype,)):
+    if t.dtype is not dtype and t.dtype not in _ALIASES.get(dtype, (dtype,)):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -430,11 +430,6 @@ _KV_DTYPES = {MOE_KV_BF16: (torch.bfloat16, torch.int16), MOE_KV_E4M3: (torch.ui
               MOE_KV_INT4: (torch.uint8,)}
 
 
-def _kv_row(fmt: int, D: int) -> int:
-    """Elements of a cache row: D values, D codes or D/2 bytes."""
-    return D // 2 if fmt == MOE_KV_INT4 else D
-
-
 def kv_cache(k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor | None = None,
              vs: torch.Tensor | None = None) -> Kv:
     """A cache pool from its tensors: k and v [n_pages][H_kv][page][row], bf16 rows of D values
@@ -470,11 +465,11 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor | None = None,
     return c
 
 
-def _kv_check(dims: KvDims, cache: Kv):
+def _kv_check(dims: KvDims, cache: Kv, H_kv: int, D: int):
     if cache.shape is None:  # made from raw pointers
         return
     fmt = dims.format
-    if (cache.shape != (dims.n_pages, dims.H_kv, dims.page, _kv_row(fmt, dims.D)) or
+    if (cache.shape != (dims.n_pages, H_kv, dims.page, D // 2 if fmt == MOE_KV_INT4 else D) or
             (fmt in _KV_DTYPES and cache.dtype not in _KV_DTYPES[fmt])):
         raise ValueError("the cache's shape or type is not that of dims")
 
@@ -503,24 +498,30 @@ def moe_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, dims: Kv
                  stream=None):
     """New keys and values bf16 [T][H_kv][D] (tokens may lie apart) into the cache's slots
     int32 [T]; a negative slot is not written."""
-    _kv_check(dims, cache)
-    kp, ldk = _rows(k, dims.T, dims.H_kv, dims.D, "k")
-    vp, ldv = _rows(v, dims.T, dims.H_kv, dims.D, "v")
-    _check(lib().moe_kv_write(kp, ldk, vp, ldv, _ints(slots, dims.T, "slots"), ctypes.byref(dims),
-                              ctypes.byref(cache), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_kv_write")
+    T, H, D = dims.T, dims.H_kv, dims.D
+    _kv_check(dims, cache, H, D)
+    kp, ldk = _rows(k, T, H, D, "k")
+    vp, ldv = _rows(v, T, H, D, "v")
+    status = (_lib or lib()).moe_kv_write(
+        kp, ldk, vp, ldv, _ints(slots, T, "slots"), ctypes.byref(dims), ctypes.byref(cache),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_kv_write")
 
 
 def moe_kv_read(slots: torch.Tensor, dims: KvDims, cache: Kv, k: torch.Tensor, v: torch.Tensor, ws,
                 stream=None):
     """The slots int32 [T] back as bf16 rows k, v [T][H_kv][D]; a negative slot gives zeros."""
-    _kv_check(dims, cache)
-    n = dims.T * dims.H_kv * dims.D
+    T, H, D = dims.T, dims.H_kv, dims.D
+    _kv_check(dims, cache, H, D)
+    n = T * H * D
     if k.numel() != n or v.numel() != n:
         raise ValueError("k and v must be [T][H_kv][D]")
-    _check(lib().moe_kv_read(_ints(slots, dims.T, "slots"), ctypes.byref(dims), ctypes.byref(cache),
-                             _dev(k, torch.int16, "k"), _dev(v, torch.int16, "v"), _ptr(ws),
-                             ws.numel(), _stream(stream)), "moe_kv_read")
+    status = (_lib or lib()).moe_kv_read(
+        _ints(slots, T, "slots"), ctypes.byref(dims), ctypes.byref(cache), _dev(k, torch.int16, "k"),
+        _dev(v, torch.int16, "v"), ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_kv_read")
 
 
 def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor,
@@ -529,14 +530,15 @@ def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, p
     """Attention of the new tokens q bf16 [T][H][D] (tokens may lie apart) over the cache, which
     holds their keys and values: out bf16 [T][H][D], lse fp32 [T][H] or None.  q_off int32
     [B+1], kv_len int32 [B], pages int32 [B][max_pages]; see include/moe.h."""
-    _kv_check(dims, cache)
-    T, H, D = dims.T, dims.H, dims.D
+    T, B, H, D = dims.T, dims.B, dims.H, dims.D
+    _kv_check(dims, cache, dims.H_kv, D)
     qp, ldq = _rows(q, T, H, D, "q")
     if out.numel() != T * H * D or (lse is not None and lse.numel() != T * H):
         raise ValueError("out must be [T][H][D] and lse [T][H]")
-    _check(lib().moe_attn_paged(
-        qp, ldq, _ints(q_off, dims.B + 1, "q_off"), _ints(kv_len, dims.B, "kv_len"),
-        _ints(pages, dims.B * dims.max_pages, "pages"), ctypes.byref(dims), ctypes.byref(cache),
-        scale, _dev(out, torch.int16, "out"),
-        None if lse is None else _dev(lse, torch.float32, "lse"), _ptr(ws), ws.numel(),
-        _stream(stream)), "moe_attn_paged")
+    status = (_lib or lib()).moe_attn_paged(
+        qp, ldq, _ints(q_off, B + 1, "q_off"), _ints(kv_len, B, "kv_len"),
+        _ints(pages, B * dims.max_pages, "pages"), ctypes.byref(dims), ctypes.byref(cache), scale,
+        _dev(out, torch.int16, "out"), None if lse is None else _dev(lse, torch.float32, "lse"),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_attn_paged")

@@ -126,40 +126,57 @@ __device__ __forceinline__ T cta_scan(T x, T* sm, T& total) {
     return before + x;
 }
 
-// Every thread of the CTA calls this; `sm` is 8-aligned scratch of deal_bytes(THREADS) that
-// nothing else uses until the CTA's next __syncthreads.  Counts the row tiles of
-// the sequences (each thread a run of sequences), then the places of the row
-// tiles (each thread a run of row tiles), deals the line and finds the unit that
-// holds this CTA's first place.
-constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 4) + 4 * threads; }
+// Every thread of the CTA calls this; `scratch` is 8-aligned, of deal_bytes(THREADS), and nothing
+// else uses it until the CTA's next __syncthreads.  Sums the places of the sequences (each thread a run
+// of sequences; where some sequence has many row tiles, each thread a run of row tiles instead,
+// counted first), deals the line and finds the unit that holds this CTA's first place.
+constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 8) + 4 * threads; }
 template <int THREADS>
 __device__ Share deal(const AttnParams& p, void* scratch) {
     constexpr int kWarps = THREADS / 32;
+    constexpr int kFew = 4;  // row tiles per sequence that its thread may count alone
     int64_t* sm = static_cast<int64_t*>(scratch);  // [warps] sums, [warps] row tiles (int), the first unit
     int* smr = reinterpret_cast<int*>(sm + kWarps);
     int64_t* found = sm + 2 * kWarps;
-    int* first = reinterpret_cast<int*>(found + 4);  // [threads]: row tiles before each thread's sequences
+    int* first = reinterpret_cast<int*>(found + 8);  // [threads]: row tiles before each thread's sequences
     const int tid = threadIdx.x, B = p.a.d.B, per = (B + THREADS - 1) / THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int rts = 0;
     Unit u;
+    auto places = [&] {
+        unit_keys(p, u);
+        return (int64_t)(u.tiles + p.c.unit_cost) * p.c.hs;
+    };
+    int64_t mine = 0, W;
+    int rts = 0, most = 0;
     for (u.b = b0; u.b < b1; ++u.b) {
         load_seq(p, u.b, u.tok0, u.n, u.len);
-        rts += row_tiles(p, u.n);
+        const int r = row_tiles(p, u.n);
+        rts += r;
+        most = max(most, r);
+        for (u.rt = 0; u.rt < min(r, kFew); ++u.rt) mine += places();
     }
-    int n_rt;
-    first[tid] = cta_scan<THREADS>(rts, smr, n_rt) - rts;
-    __syncthreads();
-    // this thread's row tiles [e0, e1): their sequences lie in the run of thread k and later
-    const int pe = (n_rt + THREADS - 1) / THREADS, e0 = min(n_rt, tid * pe), e1 = min(n_rt, e0 + pe);
-    int k = 0;
+    // this thread's row tiles: those of its sequences, or [e0, e1) of all
+    int e0 = 0, e1 = rts, at = b0;
+    const bool many = __syncthreads_or(most > kFew);
+    if (many) {
+        int n_rt;
+        first[tid] = cta_scan<THREADS>(rts, smr, n_rt) - rts;
+        __syncthreads();
+        const int pe = (n_rt + THREADS - 1) / THREADS;
+        e0 = min(n_rt, tid * pe);
+        e1 = min(n_rt, e0 + pe);
+        int k = 0;  // the thread whose run of sequences has row tile e0
 #pragma unroll
-    for (int step = THREADS > 512 ? 512 : THREADS > 256 ? 256 : 128; step; step >>= 1)
-        if (k + step < THREADS && first[k + step] <= e0) k += step;
-    auto seek = [&] {  // u to row tile e0
-        u.b = k * per;
-        u.rt = e0 - first[k];
-        load_seq(p, u.b, u.tok0, u.n, u.len);
+        for (int step = THREADS > 512 ? 512 : THREADS > 256 ? 256 : 128; step; step >>= 1)
+            if (k + step < THREADS && first[k + step] <= e0) k += step;
+        at = k * per;
+        e1 -= first[k];
+        e0 -= first[k];
+    }
+    auto seek = [&] {  // u to row tile e0 of the sequences from `at` on
+        u.b = at;
+        u.rt = e0;
+        if (many || per > 1) load_seq(p, u.b, u.tok0, u.n, u.len);
         for (int r; u.rt >= (r = row_tiles(p, u.n));) {
             u.rt -= r;
             load_seq(p, ++u.b, u.tok0, u.n, u.len);
@@ -173,17 +190,15 @@ __device__ Share deal(const AttnParams& p, void* scratch) {
             load_seq(p, u.b, u.tok0, u.n, u.len);
         } while (u.n == 0);
     };
-    auto places = [&] {
-        unit_keys(p, u);
-        return (int64_t)(u.tiles + p.c.unit_cost) * p.c.hs;
-    };
-    int64_t mine = 0, W;
-    if (e0 < e1) {
-        seek();
-        for (int e = e0;;) {
-            mine += places();
-            if (++e == e1) break;
-            step();
+    if (many) {
+        mine = 0;
+        if (e0 < e1) {
+            seek();
+            for (int e = e0;;) {
+                mine += places();
+                if (++e == e1) break;
+                step();
+            }
         }
     }
     int64_t before = cta_scan<THREADS>(mine, sm, W) - mine;
@@ -199,20 +214,20 @@ __device__ Share deal(const AttnParams& p, void* scratch) {
             before += t;
             step();
         }
-        found[0] = u.b;
-        found[1] = u.rt;
-        found[2] = before;
+        // (places() has set the unit's keys and tiles)
+        const int each = u.tiles + p.c.unit_cost;
+        const int64_t off = s.w0 - before;
+        u.hs = (int)(off >> 31 == 0 ? (uint32_t)off / (uint32_t)each : off / each);
+        found[0] = before + (int64_t)u.hs * each;
+        int* f = reinterpret_cast<int*>(found + 1);
+        f[0] = u.b, f[1] = u.rt, f[2] = u.hs, f[3] = u.n, f[4] = u.len, f[5] = u.tok0;
     }
     __syncthreads();
     if (!idle) {
-        s.u.b = (int)found[0];
-        s.u.rt = (int)found[1];
-        load_seq(p, s.u.b, s.u.tok0, s.u.n, s.u.len);
+        const int* f = reinterpret_cast<const int*>(found + 1);
+        s.unit0 = found[0];
+        s.u.b = f[0], s.u.rt = f[1], s.u.hs = f[2], s.u.n = f[3], s.u.len = f[4], s.u.tok0 = f[5];
         unit_keys(p, s.u);
-        const int each = s.u.tiles + p.c.unit_cost;
-        const int64_t off = s.w0 - found[2];
-        s.u.hs = (int)(off >> 31 == 0 ? (uint32_t)off / (uint32_t)each : off / each);
-        s.unit0 = found[2] + (int64_t)s.u.hs * each;
     }
     return s;
 }

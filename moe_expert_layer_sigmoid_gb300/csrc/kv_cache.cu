@@ -24,13 +24,15 @@ struct KvCopyParams {
     const int32_t* slots;
     KvRows kr, vr;
     WsHeader* hdr;
-    int T, H_kv, page, n_slots;
+    int T, H_kv, page, page_log2, n_slots;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&b);
 }
+
+constexpr float kDown = 1.0f - 0x1p-21f, kUp = 1.0f + 0x1p-21f;
 
 // Quantises the row that D / 8 neighbouring lanes hold (8 values each) and
 // stores codes and scale where `put`; every lane of the warp takes part (the
@@ -57,18 +59,42 @@ __device__ __forceinline__ void store_row(uint4 x, const KvRows& r, int page, in
     if (!put) return;
     uint32_t code[2] = {0, 0};
     if (s > 0.0f) {
+        // The recipe's code is that of the fp32 quotient f / s.  f * (1 / s) is within 2^-22 of it, so where
+        // the codes of that product a little down and a little up agree, both are it; only next to
+        // a midpoint between codes is the division itself needed.  (Not for the smallest scales, whose
+        // reciprocal is out of range.)
+        const float r = 1.0f / s;
+        bool sure = s >= 1e-37f;
         if (FMT == kKvE4m3) {
+            uint32_t up = 0, down = 0, other[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t c2 = __nv_cvt_float2_to_fp8x2(
-                    make_float2(f[2 * i] / s, f[2 * i + 1] / s), __NV_SATFINITE, __NV_E4M3);
-                code[i / 2] |= c2 << (16 * (i & 1));
+                const float y0 = f[2 * i] * r, y1 = f[2 * i + 1] * r;
+                down = __nv_cvt_float2_to_fp8x2(make_float2(y0 * kDown, y1 * kDown), __NV_SATFINITE, __NV_E4M3);
+                up = __nv_cvt_float2_to_fp8x2(make_float2(y0 * kUp, y1 * kUp), __NV_SATFINITE, __NV_E4M3);
+                if (i & 1) code[i / 2] |= down << 16, other[i / 2] |= up << 16;
+                else code[i / 2] = down, other[i / 2] = up;
             }
+            sure = sure && code[0] == other[0] && code[1] == other[1];
         } else {
+            uint32_t other = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int n = (int)fminf(fmaxf(rintf(f[i] / s), -8.0f), 7.0f);
-                code[0] |= (uint32_t)(n & 15) << (4 * i);
+                const float y = f[i] * r;
+                code[0] |= (uint32_t)(__float2int_rn(y * kDown) & 15) << (4 * i);
+                other |= (uint32_t)(__float2int_rn(y * kUp) & 15) << (4 * i);
+            }
+            sure = sure && code[0] == other;
+        }
+        if (!sure) {
+            code[0] = code[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = f[i] / s;
+                if (FMT == kKvE4m3)
+                    code[i / 4] |= (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+                else
+                    code[0] |= (uint32_t)((int)fminf(fmaxf(rintf(y), -8.0f), 7.0f) & 15) << (4 * i);
             }
         }
     }
@@ -108,17 +134,17 @@ __device__ __forceinline__ uint4 load_row(const KvRows& r, int page, int h, int 
 template <int FMT, int D, bool WRITE>
 __global__ void __launch_bounds__(256) kv_copy_kernel(const KvCopyParams p) {
     constexpr int kLanes = D / 8;  // lanes of a row
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const unsigned i = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;  // row: token and head (below 2^31)
     const int sub = threadIdx.x % kLanes;
-    const bool live = i < (int64_t)p.T * p.H_kv;
-    const int t = live ? (int)(i / p.H_kv) : 0, h = live ? (int)(i % p.H_kv) : 0;
+    const bool live = i < (unsigned)p.T * (unsigned)p.H_kv;
+    const int t = live ? i / (unsigned)p.H_kv : 0, h = live ? i - t * (unsigned)p.H_kv : 0;
     int slot = live ? p.slots[t] : -1;
     if (slot >= p.n_slots) {
         if (sub == 0) record_error(p.hdr, kErrBadSlot);
         slot = -1;
     }
     const bool put = slot >= 0;
-    const int page = put ? slot / p.page : 0, at = put ? slot % p.page : 0;
+    const int page = put ? slot >> p.page_log2 : 0, at = put ? slot & (p.page - 1) : 0;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     if (WRITE) {
         if (put) {
@@ -132,15 +158,15 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const KvCopyParams p) {
             k = load_row<FMT>(p.kr, page, h, at, p.page, p.H_kv, sub);
             v = load_row<FMT>(p.vr, page, h, at, p.page, p.H_kv, sub);
         }
-        reinterpret_cast<uint4*>(p.k_out)[i * kLanes + sub] = k;
-        reinterpret_cast<uint4*>(p.v_out)[i * kLanes + sub] = v;
+        reinterpret_cast<uint4*>(p.k_out)[(int64_t)i * kLanes + sub] = k;
+        reinterpret_cast<uint4*>(p.v_out)[(int64_t)i * kLanes + sub] = v;
     }
 }
 
 template <bool WRITE>
 cudaError_t launch_copy(const KvCopyParams& p, const moe_kv_dims_t& d, cudaStream_t st) {
-    const int64_t threads = (int64_t)d.T * d.H_kv * (d.D / 8);
-    const unsigned grid = (unsigned)((threads + 255) / 256);
+    const int rows = 256 / (d.D / 8);  // of a CTA
+    const unsigned grid = (unsigned)(((int64_t)d.T * d.H_kv + rows - 1) / rows);
     const bool wide = d.D == 128;
     switch (d.format) {
         case kKvBf16:
@@ -170,6 +196,7 @@ KvCopyParams copy_params(const int32_t* slots, const moe_kv_dims_t& d, const moe
     p.T = d.T;
     p.H_kv = d.H_kv;
     p.page = d.page;
+    p.page_log2 = __builtin_ctz(d.page);
     p.n_slots = d.n_pages * d.page;
     return p;
 }

@@ -32,7 +32,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&b);
 }
 
-constexpr float kDown = 1.0f - 0x1p-21f, kUp = 1.0f + 0x1p-21f;
+// The codes of two quotients: two E4M3 bytes, or two nibbles.
+template <int FMT>
+__device__ __forceinline__ uint32_t pair_code(float a, float b) {
+    if (FMT == kKvE4m3) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    return (__float2int_rn(fminf(fmaxf(a, -8.0f), 7.0f)) & 15) | (__float2int_rn(fminf(fmaxf(b, -8.0f), 7.0f)) & 15) << 4;
+}
 
 // Quantises the row that D / 8 neighbouring lanes hold (8 values each) and
 // stores codes and scale where `put`; every lane of the warp takes part (the
@@ -59,42 +64,34 @@ __device__ __forceinline__ void store_row(uint4 x, const KvRows& r, int page, in
     if (!put) return;
     uint32_t code[2] = {0, 0};
     if (s > 0.0f) {
-        // The recipe's code is that of the fp32 quotient f / s.  f * (1 / s) is within 2^-22 of it, so where
-        // the codes of that product a little down and a little up agree, both are it; only next to
-        // a midpoint between codes is the division itself needed.  (Not for the smallest scales, whose
-        // reciprocal is out of range.)
+        // The recipe's code is that of the fp32 quotient f / s, and bf16 values over a bf16 maximum lie on
+        // midpoints between codes so often that its last bit matters.  A division for each element
+        // made the kernel issue-bound (115 us against 62 us of DRAM time at 65537 tokens of 8
+        // E4M3 heads).  With the rounded reciprocal r of the row's scale, f * r corrected by
+        // its own remainder is the rounded quotient (P. Markstein, IBM J. Res. Dev. 34, 1990); the remainder
+        // is exact while s is not tiny.
         const float r = 1.0f / s;
-        bool sure = s >= 1e-37f;
-        if (FMT == kKvE4m3) {
-            uint32_t up = 0, down = 0, other[2];
+        if (s < 0x1p-80f) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                // (by pairs from the row's words: no indexing of registers)
+                const uint32_t x2 = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+                const uint32_t d = pair_code<FMT>(bf16_lo(x2) / s, bf16_hi(x2) / s);
+                if (FMT != kKvE4m3) code[0] |= d << (8 * i);
+                else if (i < 2) code[0] |= d << (16 * i);
+                else code[1] |= d << (16 * i - 32);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = f[i] * r, q = __fmaf_rn(__fmaf_rn(-y, s, f[i]), r, y);
+                f[i] = copysignf(q, f[i]);  // (-0 stays -0)
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float y0 = f[2 * i] * r, y1 = f[2 * i + 1] * r;
-                down = __nv_cvt_float2_to_fp8x2(make_float2(y0 * kDown, y1 * kDown), __NV_SATFINITE, __NV_E4M3);
-                up = __nv_cvt_float2_to_fp8x2(make_float2(y0 * kUp, y1 * kUp), __NV_SATFINITE, __NV_E4M3);
-                if (i & 1) code[i / 2] |= down << 16, other[i / 2] |= up << 16;
-                else code[i / 2] = down, other[i / 2] = up;
-            }
-            sure = sure && code[0] == other[0] && code[1] == other[1];
-        } else {
-            uint32_t other = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = f[i] * r;
-                code[0] |= (uint32_t)(__float2int_rn(y * kDown) & 15) << (4 * i);
-                other |= (uint32_t)(__float2int_rn(y * kUp) & 15) << (4 * i);
-            }
-            sure = sure && code[0] == other;
-        }
-        if (!sure) {
-            code[0] = code[1] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = f[i] / s;
-                if (FMT == kKvE4m3)
-                    code[i / 4] |= (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
-                else
-                    code[0] |= (uint32_t)((int)fminf(fmaxf(rintf(y), -8.0f), 7.0f) & 15) << (4 * i);
+                const uint32_t d = pair_code<FMT>(f[2 * i], f[2 * i + 1]);
+                if (FMT == kKvE4m3) code[i / 2] |= d << (16 * (i & 1));
+                else code[0] |= d << (8 * i);
             }
         }
     }

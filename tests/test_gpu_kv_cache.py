@@ -98,6 +98,34 @@ def test_rows_at_the_edges_of_the_formats(fmt):
     assert torch.equal(ko, _back(k, fmt))
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int4"])
+@pytest.mark.parametrize("power", [0, 100, -60, -110, -125])
+def test_quotients_of_every_pair_of_significands(fmt, power):
+    """Each of the 128 bf16 significands under each maximum, over the codes' whole range (most
+    midpoints between codes that bf16 rows can meet are among them), at ordinary scales and at the largest
+    and smallest."""
+    D, H_kv = 128, 8
+    sig = (128 + torch.arange(128)).double()
+    rows = []
+    for top in range(128):
+        for e in range(8):      # elements a factor 2^-e (and up to 2^-1 more) below the maximum
+            x = sig * 2.0 ** -e
+            x[x > sig[top]] /= 2
+            x[::2] *= -1
+            x[0] = sig[top]
+            rows.append(x * 2.0 ** (power - 7))
+    k = torch.stack(rows).to(torch.bfloat16).view(128, H_kv, D).cuda()
+    T = k.shape[0]
+    _, _, slots, pool, sc, dims, cache, ws = _setup(T, H_kv, D, 64, fmt)
+    v = -k
+    moe.moe_kv_write(k, v, slots, dims, cache, ws)
+    p, at = slots.long() // 64, slots.long() % 64
+    for x, rows, s in ((k, pool[0], sc[0]), (v, pool[1], sc[1])):
+        codes, scales = quantise(x, fmt)
+        assert torch.equal(s[p, :, at], scales)
+        assert torch.equal(rows[p, :, at], codes)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "int4"])
 def test_slots_past_the_pool(fmt):
     """Not written, read as zeros, and recorded; the other rows are as ever."""

@@ -65,7 +65,7 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
         at += align256(attn_tiles_part_bytes(a.d));
     }
     if (k.rows && e == cudaSuccess)
-        e = launch_attn_rows(a, 0, k.tiles ? kFewRows : most, k.eight, reinterpret_cast<float*>(ws + at),
+        e = launch_attn_rows(a, 0, k.tiles ? kFewRows : most, k.eight, k.tiles, reinterpret_cast<float*>(ws + at),
                              reinterpret_cast<unsigned*>(ws + kCountersAt), st);
     return e;
 }

@@ -95,10 +95,6 @@ struct Share {
     Unit u;           // the first unit
 };
 
-__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int64_t c) {
-    const int64_t n = a * b;
-    return n >> 32 == 0 && c >> 32 == 0 ? (uint32_t)n / (uint32_t)c : n / c;
-}
 // The CTA that holds place w.
 __device__ __forceinline__ int share_owner(int64_t W, int R, int64_t w) {
     const int64_t n = (w + 1) * R - 1;
@@ -126,57 +122,56 @@ __device__ __forceinline__ T cta_scan(T x, T* sm, T& total) {
     return before + x;
 }
 
-// Every thread of the CTA calls this; `scratch` is 8-aligned, of deal_bytes(THREADS), and nothing
-// else uses it until the CTA's next __syncthreads.  Sums the places of the sequences (each thread a run
-// of sequences; where some sequence has many row tiles, each thread a run of row tiles instead,
-// counted first), deals the line and finds the unit that holds this CTA's first place.
+// Every thread of the CTA calls deal(); `scratch` is 8-aligned, of deal_bytes(THREADS), and nothing
+// else uses it until the CTA's next __syncthreads.  Sums the places of the sequences, deals the line and
+// finds the unit that holds this CTA's first place.  Everything a CTA does waits for it, and its code
+// is cold when it runs, so the common case (a sequence per thread at most, few row tiles
+// each, a line that 32 bits hold) is kept short; deal_many is for the others.
 constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 8) + 4 * threads; }
+
+// The share of the line and its first unit, from the found one's first place of its row tile.
+__device__ __forceinline__ void put_found(const AttnParams& p, int64_t* found, Unit& u, int64_t before, int64_t w0) {
+    const int each = u.tiles + p.c.unit_cost;
+    const int64_t off = w0 - before;
+    u.hs = (int)(off >> 31 == 0 ? (uint32_t)off / (uint32_t)each : off / each);
+    found[0] = before + (int64_t)u.hs * each;
+    int* f = reinterpret_cast<int*>(found + 1);
+    f[0] = u.b, f[1] = u.rt, f[2] = u.hs, f[3] = u.n, f[4] = u.len, f[5] = u.tok0;
+}
+__device__ __forceinline__ void get_found(const AttnParams& p, const int64_t* found, Share& s) {
+    const int* f = reinterpret_cast<const int*>(found + 1);
+    s.unit0 = found[0];
+    s.u.b = f[0], s.u.rt = f[1], s.u.hs = f[2], s.u.n = f[3], s.u.len = f[4], s.u.tok0 = f[5];
+    unit_keys(p, s.u);
+}
+
+// Any lengths: each thread a run of sequences to count the row tiles, then a run of row tiles to count
+// the places.
 template <int THREADS>
-__device__ Share deal(const AttnParams& p, void* scratch) {
+__device__ __noinline__ void deal_many(const AttnParams& p, int64_t* sm) {
     constexpr int kWarps = THREADS / 32;
-    constexpr int kFew = 4;  // row tiles per sequence that its thread may count alone
-    int64_t* sm = static_cast<int64_t*>(scratch);  // [warps] sums, [warps] row tiles (int), the first unit
-    int* smr = reinterpret_cast<int*>(sm + kWarps);
+    int* smr = reinterpret_cast<int*>(sm + kWarps);  // row tiles by warp
     int64_t* found = sm + 2 * kWarps;
     int* first = reinterpret_cast<int*>(found + 8);  // [threads]: row tiles before each thread's sequences
     const int tid = threadIdx.x, B = p.a.d.B, per = (B + THREADS - 1) / THREADS;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     Unit u;
-    auto places = [&] {
-        unit_keys(p, u);
-        return (int64_t)(u.tiles + p.c.unit_cost) * p.c.hs;
-    };
-    int64_t mine = 0, W;
-    int rts = 0, most = 0;
-    for (u.b = b0; u.b < b1; ++u.b) {
+    int rts = 0, n_rt;
+    for (u.b = min(B, tid * per); u.b < min(B, tid * per + per); ++u.b) {
         load_seq(p, u.b, u.tok0, u.n, u.len);
-        const int r = row_tiles(p, u.n);
-        rts += r;
-        most = max(most, r);
-        for (u.rt = 0; u.rt < min(r, kFew); ++u.rt) mine += places();
+        rts += row_tiles(p, u.n);
     }
-    // this thread's row tiles: those of its sequences, or [e0, e1) of all
-    int e0 = 0, e1 = rts, at = b0;
-    const bool many = __syncthreads_or(most > kFew);
-    if (many) {
-        int n_rt;
-        first[tid] = cta_scan<THREADS>(rts, smr, n_rt) - rts;
-        __syncthreads();
-        const int pe = (n_rt + THREADS - 1) / THREADS;
-        e0 = min(n_rt, tid * pe);
-        e1 = min(n_rt, e0 + pe);
-        int k = 0;  // the thread whose run of sequences has row tile e0
-#pragma unroll
-        for (int step = THREADS > 512 ? 512 : THREADS > 256 ? 256 : 128; step; step >>= 1)
-            if (k + step < THREADS && first[k + step] <= e0) k += step;
-        at = k * per;
-        e1 -= first[k];
-        e0 -= first[k];
-    }
-    auto seek = [&] {  // u to row tile e0 of the sequences from `at` on
-        u.b = at;
-        u.rt = e0;
-        if (many || per > 1) load_seq(p, u.b, u.tok0, u.n, u.len);
+    __syncthreads();
+    first[tid] = cta_scan<THREADS>(rts, smr, n_rt) - rts;
+    __syncthreads();
+    const int pe = (n_rt + THREADS - 1) / THREADS, e0 = min(n_rt, tid * pe), e1 = min(n_rt, e0 + pe);
+    int k = 0;  // the thread whose run of sequences has row tile e0
+#pragma unroll 1
+    for (int step = 512; step; step >>= 1)
+        if (k + step < THREADS && first[k + step] <= e0) k += step;
+    auto seek = [&] {  // u to row tile e0
+        u.b = k * per;
+        u.rt = e0 - first[k];
+        load_seq(p, u.b, u.tok0, u.n, u.len);
         for (int r; u.rt >= (r = row_tiles(p, u.n));) {
             u.rt -= r;
             load_seq(p, ++u.b, u.tok0, u.n, u.len);
@@ -190,45 +185,97 @@ __device__ Share deal(const AttnParams& p, void* scratch) {
             load_seq(p, u.b, u.tok0, u.n, u.len);
         } while (u.n == 0);
     };
-    if (many) {
-        mine = 0;
-        if (e0 < e1) {
-            seek();
-            for (int e = e0;;) {
-                mine += places();
-                if (++e == e1) break;
-                step();
-            }
+    auto places = [&] {
+        unit_keys(p, u);
+        return (int64_t)(u.tiles + p.c.unit_cost) * p.c.hs;
+    };
+    int64_t mine = 0, W;
+    if (e0 < e1) {
+        seek();
+        for (int e = e0;;) {
+            mine += places();
+            if (++e == e1) break;
+            step();
         }
     }
     int64_t before = cta_scan<THREADS>(mine, sm, W) - mine;
-    Share s;
-    s.W = W;
-    s.R = (int)min((int64_t)gridDim.x, max((int64_t)1, W / p.c.min_share));
-    const bool idle = (int)blockIdx.x >= s.R || W == 0;
-    s.w0 = idle ? 0 : mul_div(W, blockIdx.x, s.R);
-    s.w1 = idle ? 0 : mul_div(W, blockIdx.x + 1, s.R);
-    if (!idle && s.w0 >= before && s.w0 < before + mine) {
+    const int R = (int)min((int64_t)gridDim.x, max((int64_t)1, W / p.c.min_share));
+    const bool idle = (int)blockIdx.x >= R || W == 0;
+    const int64_t w0 = idle ? 0 : W * blockIdx.x / R;
+    if (tid == 0) {
+        found[4] = W;
+        found[5] = R;
+        found[6] = w0;
+        found[7] = idle ? 0 : W * (blockIdx.x + 1) / R;
+    }
+    if (!idle && w0 >= before && w0 < before + mine) {
         seek();
-        for (int64_t t; s.w0 >= before + (t = places());) {
+        for (int64_t t; w0 >= before + (t = places());) {
             before += t;
             step();
         }
-        // (places() has set the unit's keys and tiles)
-        const int each = u.tiles + p.c.unit_cost;
-        const int64_t off = s.w0 - before;
-        u.hs = (int)(off >> 31 == 0 ? (uint32_t)off / (uint32_t)each : off / each);
-        found[0] = before + (int64_t)u.hs * each;
-        int* f = reinterpret_cast<int*>(found + 1);
-        f[0] = u.b, f[1] = u.rt, f[2] = u.hs, f[3] = u.n, f[4] = u.len, f[5] = u.tok0;
+        put_found(p, found, u, before, w0);
     }
     __syncthreads();
-    if (!idle) {
-        const int* f = reinterpret_cast<const int*>(found + 1);
-        s.unit0 = found[0];
-        s.u.b = f[0], s.u.rt = f[1], s.u.hs = f[2], s.u.n = f[3], s.u.len = f[4], s.u.tok0 = f[5];
-        unit_keys(p, s.u);
+}
+
+template <int THREADS>
+__device__ __forceinline__ Share deal(const AttnParams& p, void* scratch) {
+    constexpr int kWarps = THREADS / 32;
+    constexpr int kFew = 4;  // row tiles of a sequence that its thread may count alone
+    int64_t* sm = static_cast<int64_t*>(scratch);
+    int64_t* found = sm + 2 * kWarps;
+    const int B = p.a.d.B;
+    Share s;
+    Unit& u = s.u;
+    u.b = threadIdx.x;
+    u.n = 0;
+    if (u.b < B) load_seq(p, u.b, u.tok0, u.n, u.len);
+    const int rts = row_tiles(p, u.n);
+    uint64_t sum = 0;
+    bool long_ = B > THREADS || rts > kFew;
+    if (!long_)
+#pragma unroll 1
+        for (u.rt = 0; u.rt < rts; ++u.rt) {
+            unit_keys(p, u);
+            sum += (uint64_t)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
+        }
+    long_ |= sum >= 1u << 22;  // (below it no sum over the CTA passes 32 bits)
+    const unsigned mine = (unsigned)sum;
+    unsigned W = 0, before = 0;
+    bool many = __syncthreads_or(long_);
+    if (!many) {
+        before = cta_scan<THREADS>(mine, reinterpret_cast<unsigned*>(sm), W) - mine;
+        many = W >= 1u << 23;  // W * R in 32 bits, up to 512 CTAs
     }
+    if (many) {
+        deal_many<THREADS>(p, sm);
+        s.W = found[4];
+        s.R = (int)found[5];
+        s.w0 = found[6];
+        s.w1 = found[7];
+        get_found(p, found, s);
+        return s;
+    }
+    s.W = W;
+    const unsigned R = min(gridDim.x, max(1u, W / (unsigned)p.c.min_share));
+    s.R = R;
+    s.w0 = s.w1 = s.unit0 = 0;
+    if (blockIdx.x >= R || W == 0) return s;
+    const unsigned w0 = W * blockIdx.x / R;
+    s.w0 = w0;
+    s.w1 = (W * blockIdx.x + W) / R;
+    if (w0 >= before && w0 < before + mine) {
+        for (u.rt = 0;; ++u.rt) {
+            unit_keys(p, u);
+            const unsigned t = (unsigned)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
+            if (w0 < before + t) break;
+            before += t;
+        }
+        put_found(p, found, u, before, w0);
+    }
+    __syncthreads();
+    get_found(p, found, s);
     return s;
 }
 
@@ -270,8 +317,10 @@ bool make_kv_map(CUtensorMap* m, const void* base, const AttnArgs& a, int box_by
 // Launchers.  `part` and `counters` lie in the workspace; the counters are zero
 // between calls.
 size_t attn_rows_part_bytes(const moe_kv_dims_t& d);
-// `eight`: units of eight rows instead of sixteen (at most eight query heads per key/value head)
-cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
+// `eight`: units of eight rows instead of sixteen (at most eight query heads per key/value head).
+// `behind`: launched right behind launch_attn_tiles on the same sequences' others: its CTAs may take the
+// SMs that the chunks' CTAs leave, and it ends after them.
+cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, bool behind, float* part,
                              unsigned* counters, cudaStream_t st);
 size_t attn_tiles_part_bytes(const moe_kv_dims_t& d);
 cudaError_t launch_attn_tiles(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,

@@ -172,7 +172,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Share sh = deal<kRowsThreads>(p, smem);
-    if (sh.w0 >= sh.w1) return;
+    if (sh.w0 >= sh.w1) {
+        pdl_wait();
+        return;
+    }
     __syncthreads();
     WsHeader* hdr = p.a.hdr;
 
@@ -691,10 +694,11 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         }
         compute_sync();  // the buffers are free for the next unit
     } while (next_unit(p, sh, u, unit0));
+    pdl_wait();  // behind the chunks' kernel: what follows this one may count on both
 }
 
 template <int FMT, int D, int R8>
-cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* part,
+cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool behind, float* part,
                    unsigned* counters, cudaStream_t st) {
     using S = RowsShape<FMT, D, R8>;
     AttnParams p;
@@ -706,8 +710,10 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     p.c.hs = a.d.H_kv * p.c.subs;
     p.c.tk_log2 = __builtin_ctz(S::kTk);
     p.c.page_log2 = __builtin_ctz(a.d.page);
-    p.c.unit_cost = 1;
-    p.c.min_share = 2;
+    // (drafts, a wide int4 step and a bf16 step took 73.4, 40.7 and 33.1 us at 1, 67.1, 39.3 and 31.9 at 3,
+    // 67.2, 41.3 and 32.1 at 5)
+    p.c.unit_cost = 3;
+    p.c.min_share = 4;
     p.c.rows_lo = rows_lo;
     p.c.rows_hi = rows_hi;
     p.part = part;
@@ -719,15 +725,24 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     const void* kern = reinterpret_cast<const void*>(&attn_rows_kernel<FMT, D, R8>);
     cudaError_t e = ensure_dynamic_smem(kern, S::kSmem);
     if (e != cudaSuccess) return e;
-    attn_rows_kernel<FMT, D, R8><<<S::kCtas * sm_count(), kRowsThreads, S::kSmem, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(S::kCtas * sm_count());
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<FMT, D, R8>, p);
 }
 
 template <int FMT, int D>
-cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
+cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, bool behind, float* part,
                        unsigned* counters, cudaStream_t st) {
-    return eight ? launch<FMT, D, 1>(a, rows_lo, rows_hi, part, counters, st)
-                                 : launch<FMT, D, 2>(a, rows_lo, rows_hi, part, counters, st);
+    return eight ? launch<FMT, D, 1>(a, rows_lo, rows_hi, behind, part, counters, st)
+                                 : launch<FMT, D, 2>(a, rows_lo, rows_hi, behind, part, counters, st);
 }
 
 }  // namespace
@@ -737,19 +752,19 @@ size_t attn_rows_part_bytes(const moe_kv_dims_t& d) {
     return (size_t)(2 * sm_count()) * std::max(3 * 8, 2 * 16) * (d.D + 2) * sizeof(float);
 }
 
-cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, float* part,
+cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, bool behind, float* part,
                              unsigned* counters, cudaStream_t st) {
     const bool wide = a.d.D == 128;
     switch (a.d.format) {
         case kKvBf16:
-            return wide ? launch_for<kKvBf16, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
-                        : launch_for<kKvBf16, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
+            return wide ? launch_for<kKvBf16, 128>(a, rows_lo, rows_hi, eight, behind, part, counters, st)
+                        : launch_for<kKvBf16, 64>(a, rows_lo, rows_hi, eight, behind, part, counters, st);
         case kKvE4m3:
-            return wide ? launch_for<kKvE4m3, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
-                        : launch_for<kKvE4m3, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
+            return wide ? launch_for<kKvE4m3, 128>(a, rows_lo, rows_hi, eight, behind, part, counters, st)
+                        : launch_for<kKvE4m3, 64>(a, rows_lo, rows_hi, eight, behind, part, counters, st);
         case kKvInt4:
-            return wide ? launch_for<kKvInt4, 128>(a, rows_lo, rows_hi, eight, part, counters, st)
-                        : launch_for<kKvInt4, 64>(a, rows_lo, rows_hi, eight, part, counters, st);
+            return wide ? launch_for<kKvInt4, 128>(a, rows_lo, rows_hi, eight, behind, part, counters, st)
+                        : launch_for<kKvInt4, 64>(a, rows_lo, rows_hi, eight, behind, part, counters, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -27,7 +27,7 @@ Kernels kernels_for(const moe_kv_dims_t& d) {
 // Workspace: the header, the arrival counters of the joins (at a place that no
 // size moves, zero between calls; one set for each kernel), the partial results.
 constexpr size_t kCountersAt = sizeof(WsHeader);
-size_t counters_bytes() { return align256(sizeof(unsigned) * 3 * (size_t)sm_count()); }
+size_t counters_bytes() { return align256(sizeof(unsigned) * 4 * (size_t)sm_count()); }
 size_t part_at() { return kCountersAt + 2 * counters_bytes(); }
 
 }  // namespace

@@ -246,7 +246,7 @@ __device__ __forceinline__ Share deal(const AttnParams& p, void* scratch) {
     bool many = __syncthreads_or(long_);
     if (!many) {
         before = cta_scan<THREADS>(mine, reinterpret_cast<unsigned*>(sm), W) - mine;
-        many = W >= 1u << 23;  // W * R in 32 bits, up to 512 CTAs
+        many = W >= 1u << 22;  // W * R in 32 bits, up to 1024 CTAs
     }
     if (many) {
         deal_many<THREADS>(p, sm);

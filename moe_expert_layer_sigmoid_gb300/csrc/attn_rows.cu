@@ -108,7 +108,9 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 template <int FMT, int D, int R8>
 struct RowsShape {
     static constexpr int kRows = 8 * R8;
-    static constexpr int kCtas = R8 == 1 ? 3 : 2;               // per SM
+    // per SM, by registers; a fourth for narrow int4 heads, the work per byte of which is the largest (128
+    // sequences: int4 39.4 -> 36.8 us with four, E4M3 41.2 -> 43.3, bf16 54 either way)
+    static constexpr int kCtas = R8 == 2 ? 2 : FMT == kKvInt4 && D == 64 ? 4 : 3;
     static constexpr int kRowB = kv_row_bytes(FMT, D);          // bytes of a cache row
     static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;     // of a box's row: the swizzle span
     static constexpr int kHalves = kRowB / kBoxB;
@@ -116,7 +118,7 @@ struct RowsShape {
     static constexpr int kKm = kTk / 64;                        // blocks of 16 keys of a warp
     static constexpr int kTileB = kTk * kRowB;                  // bytes of a stage's keys
     static constexpr int kScB = FMT == kKvBf16 ? 0 : kTk * 4;   // and of their scales
-    static constexpr int kRing = R8 == 1 ? 65536 : 98304;
+    static constexpr int kRing = kCtas == 4 ? 40960 : kCtas == 3 ? 65536 : 98304;
     static constexpr int kStages = kRing / (2 * kTileB) < 8 ? kRing / (2 * kTileB) : 8;
     static constexpr int kChunks = kRowB / 16;                  // 16-byte chunks of a row
     static constexpr int kDm = D / 16;                          // blocks of 16 output columns
@@ -128,7 +130,7 @@ struct RowsShape {
     static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
     static constexpr int kSmem = kOffMisc + 16;
-    static_assert(kSmem <= (R8 == 1 ? 76800 : 115712), "the CTAs of an SM share its shared memory");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM share its shared memory");
     static_assert(kSmem >= deal_bytes(kRowsThreads), "scratch");
     static constexpr int kPart = kRows * D + 2 * kRows;         // floats of a partial result
 };
@@ -748,8 +750,8 @@ cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool
 }  // namespace
 
 size_t attn_rows_part_bytes(const moe_kv_dims_t& d) {
-    // two slots for each of three CTAs per SM with 8 rows, or two with 16
-    return (size_t)(2 * sm_count()) * std::max(3 * 8, 2 * 16) * (d.D + 2) * sizeof(float);
+    // two slots for each of up to four CTAs per SM with 8 rows, or two with 16
+    return (size_t)(2 * sm_count()) * std::max(4 * 8, 2 * 16) * (d.D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, bool behind, float* part,

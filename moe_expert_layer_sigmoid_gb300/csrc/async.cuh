@@ -48,6 +48,11 @@ __device__ __forceinline__ uint64_t wait_limit(const WsHeader* hdr) {
     return v ? v : kWaitNs;
 }
 
+// The stage whose copies a kernel's CTA 0 skips, counted from 1 (the test hook; 0: none).
+__device__ __forceinline__ uint32_t withheld_stage(const WsHeader* hdr) {
+    return blockIdx.x == 0 ? *reinterpret_cast<const volatile int32_t*>(&hdr->withhold_stage) : 0;
+}
+
 // Bounded wait: gives up after the wait limit (or once another warp gave up),
 // records the failure in the workspace header and returns false.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,

@@ -173,6 +173,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    const uint32_t withheld = withheld_stage(p.a.hdr);
     const Share sh = deal<kRowsThreads>(p, smem);
     if (sh.w0 >= sh.w1) {
         pdl_wait();
@@ -225,7 +226,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 const uint32_t box_bytes = box_rows * S::kRowB, sc_bytes = FMT == kKvBf16 ? 0 : box_rows * 4;
                 if (lane == 0) mbar_expect_tx(full(s), n_live * 2 * (box_bytes + sc_bytes));
                 __syncwarp();
-                if (live) {
+                if (live && it + 1 != withheld) {
                     int id = mine;
                     if (id < 0 || id >= p.a.d.n_pages) {
                         record_error(hdr, kErrBadPage);
@@ -388,7 +389,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         for (; tile < end; ++tile, ++it) {
             const int s = it % S::kStages;
             // once a wait gave up the flag is set; the warps then run on without waiting, in step
-            // with each other, to the end
+            // with each other, to the end.  They hand no stage back: one whose copies never came must
+            // not be armed a second time (its barrier's phase is still open), so the copies stop too
             if (ok) ok = mbar_wait(full(s), (it / S::kStages) & 1, abort_flag, hdr);
             const int kw0 = warp * 16 * kKm;                       // the warp's first key in the tile
             const int key = (u.tile0 + tile) * S::kTk + kw0;
@@ -566,7 +568,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty(s));
+            if (lane == 0 && ok) mbar_arrive(empty(s));
         }
 
         // ------------------------------------------------------ join the four warps

@@ -213,6 +213,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_trigger();  // the kernel of few rows may start where this one leaves room
+    const uint32_t withheld = withheld_stage(hdr);
     const Share sh = deal<S::kThreads>(p, smem);
     if (sh.w0 >= sh.w1) return;
     if (warp == 1) {
@@ -299,7 +300,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         const uint32_t sc_bytes = S::kQuant ? box_rows * 4 : 0;
                         if (lane == 0) mbar_expect_tx(done, n_live * (box_rows * S::kRowB + sc_bytes));
                         __syncwarp();
-                        if (live) {
+                        if (live && it + 1 != withheld) {
                             const CUtensorMap* tm = kv ? &p.tm_v : &p.tm_k;
                             const uint32_t d = sbase + (S::kQuant ? S::kOffRaw + s * S::kRawB : S::kOffKv + s * S::kTileB) +
                                                lane * box_rows * S::kBoxB;
@@ -830,7 +831,9 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) {
+                    // (nothing is handed on after an abort: codes that never came must not be asked for a
+                    // second time while their barrier's phase is open)
+                    if (lane == 0 && ok) {
                         mbar_arrive(bar(S::kBarFull + sl));
                         mbar_arrive(bar(S::kBarRawE + rw));
                     }

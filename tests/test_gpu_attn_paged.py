@@ -194,6 +194,26 @@ def test_device_checks():
     ok(b)
 
 
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("stage", [1, 2])
+@pytest.mark.parametrize("new,total", [([1], [200000]), ([100, 70], [900, 300]), ([1, 200, 1], [500, 700, 90])])
+def test_a_wait_that_runs_out(fmt, stage, new, total):
+    """A stage whose copies never come: every role gives up in order, the status says so, and the
+    workspace serves the next call as a fresh one does."""
+    b = ac.make(new, total, 8, 2, 128, 64, fmt, seed=5)
+    dims = b.dims(moe)
+    ws = moe.workspace(moe.moe_attn_workspace_bytes(dims))
+    moe.moe_debug_set_waits(ws, 5_000_000, stage)
+    run(b, ws)
+    assert moe.moe_check_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK
+    moe.moe_debug_set_waits(ws, 0, 0)
+    out, lse, _ = run(b, ws)
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK
+    fresh, z, _ = run(b)
+    assert torch.equal(out, fresh) and torch.equal(lse, z)
+    ac.check(b, out, lse)
+
+
 def test_binding_refuses():
     b = ac.make([1, 3], [20, 30], 4, 2, 64, 16, "e4m3", poison=False)
     d, c, ws = b.dims(moe), b.cache(moe), moe.workspace(moe.moe_attn_workspace_bytes(b.dims(moe)))

@@ -1,5 +1,6 @@
 /*
- * moe.h -- C ABI of libmoe.so, the GB300 (sm_103a) routed MoE FFN layer.
+ * moe.h -- C ABI of libmoe.so, the GB300 (sm_103a) routed MoE FFN layer, and
+ * of the paged key/value cache and attention next to it (at the end).
  *
  * The layer (thewafflehaus/butter PR #69, commit "feat(laguna): Laguna-S-2.1
  * decode on the CUDA engine"): a sigmoid top-k router with a score-correction

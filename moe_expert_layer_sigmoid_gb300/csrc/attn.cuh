@@ -125,9 +125,10 @@ __device__ __forceinline__ T cta_scan(T x, T* sm, T& total) {
 // Every thread of the CTA calls deal(); `scratch` is 8-aligned, of deal_bytes(THREADS), and nothing
 // else uses it until the CTA's next __syncthreads.  Sums the places of the sequences, deals the line and
 // finds the unit that holds this CTA's first place.  Everything a CTA does waits for it, and its code
-// is cold when it runs, so the common case (a sequence per thread at most, few row tiles
-// each, a line that 32 bits hold) is kept short; deal_many is for the others.
-constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 8) + 4 * threads; }
+// is cold when it runs, so the common cases (a sequence per thread at most, a line that 32 bits hold,
+// and few row tiles per sequence or no more in all than threads) are kept short; deal_many is for
+// the others (a 2048-token chunk waited 12,300 cycles for it).
+constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 8) + 16 * threads; }
 
 // The share of the line and its first unit, from the found one's first place of its row tile.
 __device__ __forceinline__ void put_found(const AttnParams& p, int64_t* found, Unit& u, int64_t before, int64_t w0) {
@@ -241,13 +242,42 @@ __device__ __forceinline__ Share deal(const AttnParams& p, void* scratch) {
             sum += (uint64_t)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
         }
     long_ |= sum >= 1u << 22;  // (below it no sum over the CTA passes 32 bits)
-    const unsigned mine = (unsigned)sum;
+    unsigned mine = (unsigned)sum;
     unsigned W = 0, before = 0;
-    bool many = __syncthreads_or(long_);
+    bool many = __syncthreads_or(long_), each = false;  // each: a thread has one row tile, u
     if (!many) {
         before = cta_scan<THREADS>(mine, reinterpret_cast<unsigned*>(sm), W) - mine;
-        many = W >= 1u << 22;  // W * R in 32 bits, up to 1024 CTAs
+    } else if (B <= THREADS) {
+        int n_rt;
+        int4* seqs = reinterpret_cast<int4*>(found + 8);  // n, length, first token, row tiles before
+        const int e = threadIdx.x, upto = cta_scan<THREADS>(rts, reinterpret_cast<int*>(sm + kWarps), n_rt);
+        if (n_rt <= THREADS) {
+            seqs[e] = make_int4(u.n, u.len, u.tok0, upto - rts);
+            __syncthreads();
+            u.n = 0;
+            mine = 0;
+            if (e < n_rt) {
+                int lo = 0;
+#pragma unroll 1
+                for (int hi = B; hi - lo > 1;) {
+                    const int mid = (lo + hi) >> 1;
+                    if (seqs[mid].w <= e) lo = mid;
+                    else hi = mid;
+                }
+                const int4 q = seqs[lo];
+                u.b = lo;
+                u.n = q.x, u.len = q.y, u.tok0 = q.z;
+                u.rt = e - q.w;
+                unit_keys(p, u);
+                sum = (uint64_t)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
+                mine = (unsigned)sum;
+            }
+            many = __syncthreads_or(e < n_rt && sum >= 1u << 22);
+            each = true;
+            if (!many) before = cta_scan<THREADS>(mine, reinterpret_cast<unsigned*>(sm), W) - mine;
+        }
     }
+    many |= W >= 1u << 22;  // W * R in 32 bits, up to 1024 CTAs
     if (many) {
         deal_many<THREADS>(p, sm);
         s.W = found[4];
@@ -266,12 +296,13 @@ __device__ __forceinline__ Share deal(const AttnParams& p, void* scratch) {
     s.w0 = w0;
     s.w1 = (W * blockIdx.x + W) / R;
     if (w0 >= before && w0 < before + mine) {
-        for (u.rt = 0;; ++u.rt) {
-            unit_keys(p, u);
-            const unsigned t = (unsigned)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
-            if (w0 < before + t) break;
-            before += t;
-        }
+        if (!each)
+            for (u.rt = 0;; ++u.rt) {
+                unit_keys(p, u);
+                const unsigned t = (unsigned)(u.tiles + p.c.unit_cost) * (unsigned)p.c.hs;
+                if (w0 < before + t) break;
+                before += t;
+            }
         put_found(p, found, u, before, w0);
     }
     __syncthreads();

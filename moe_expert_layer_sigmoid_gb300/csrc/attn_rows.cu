@@ -659,14 +659,16 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                     __stcg(to + 1, make_float4(f[4], f[5], f[6], f[7]));
                 }
                 if (tid < kRows) __stcg(reinterpret_cast<float2*>(q + kRows * D) + tid, joined(tid));
-                __threadfence();
                 compute_sync();
-                if (tid == 0) *last_flag = atomicAdd(arrived, 1u) == others;
+                if (tid == 0) {
+                    __threadfence();  // the whole group's writes: they come before it by the barrier
+                    *last_flag = atomicAdd(arrived, 1u) == others;
+                    __threadfence();
+                }
                 compute_sync();
                 last = *last_flag;
             }
             if (last) {
-                __threadfence();
                 if (tid == 0) *arrived = 0;
                 for (int i = tid; i < kPieces; i += 128) {
                     const int r = i / (D / 8);

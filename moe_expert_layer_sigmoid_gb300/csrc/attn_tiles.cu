@@ -712,16 +712,16 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                             __stcg(po + (col / 4 + e) * kTileRows + r, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
                     }
                     if (stats) __stcg(reinterpret_cast<float2*>(part + kTileRows * D) + r, make_float2(M, L));
-                    __threadfence();
                     all_sync();
-                    if (threadIdx.x == 128) *last_flag = atomicAdd(arrived, 1u) == others;
+                    if (threadIdx.x == 128) {
+                        __threadfence();  // the whole group's writes: they come before it by the barrier
+                        *last_flag = atomicAdd(arrived, 1u) == others;
+                        __threadfence();
+                    }
                     all_sync();
                     join = *last_flag;
                 }
-                if (join) {
-                    __threadfence();
-                    if (threadIdx.x == 128) *arrived = 0;
-                }
+                if (join && threadIdx.x == 128) *arrived = 0;
             }
             if (whole) {
                 const float inv = L > 0.0f ? 1.0f / L : 0.0f;

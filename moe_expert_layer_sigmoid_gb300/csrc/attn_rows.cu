@@ -129,7 +129,7 @@ struct RowsShape {
     static constexpr int kOffMl = kOffJoin + kRows * kLd * 4;
     static constexpr int kOffBar = kOffMl + 4 * kRows * 8;
     static constexpr int kOffMisc = kOffBar + 2 * kStages * 8;
-    static constexpr int kSmem = kOffMisc + 16;
+    static constexpr int kSmem = kOffMisc + 16 + sizeof(Share);
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM share its shared memory");
     static_assert(kSmem >= deal_bytes(kRowsThreads), "scratch");
     static constexpr int kPart = kRows * D + 2 * kRows;         // floats of a partial result
@@ -174,10 +174,15 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const uint32_t withheld = withheld_stage(p.a.hdr);
-    const Share sh = deal<kRowsThreads>(p, smem);
-    if (sh.w0 >= sh.w1) {
-        pdl_wait();
-        return;
+    // (the share stays in shared memory: it is looked at once per unit, and registers are short)
+    Share& sh = *reinterpret_cast<Share*>(smem + S::kOffMisc + 16);
+    {
+        const Share mine = deal<kRowsThreads>(p, smem);
+        if (mine.w0 >= mine.w1) {
+            pdl_wait();
+            return;
+        }
+        if (threadIdx.x == 0) sh = mine;
     }
     __syncthreads();
     WsHeader* hdr = p.a.hdr;

@@ -79,7 +79,7 @@ struct TilesShape {
                          kBarSf = kBarRawE + kRaws, kBarPf = kBarSf + 2, kBarOd = kBarPf + 2,
                          kBarQf = kBarOd + 2, kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kSmem = kOffMisc + 16;
+    static constexpr int kSmem = kOffMisc + 16 + sizeof(Share);
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
     // a partial result: both streams' rows, O as float4 columns of 128 rows, then maximum and sum
     static constexpr int kPartStream = kTileRows * D + 2 * kTileRows;
@@ -214,8 +214,13 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
     }
     pdl_trigger();  // the kernel of few rows may start where this one leaves room
     const uint32_t withheld = withheld_stage(hdr);
-    const Share sh = deal<S::kThreads>(p, smem);
-    if (sh.w0 >= sh.w1) return;
+    // (the share stays in shared memory: it is looked at once per unit, and registers are short)
+    Share& sh = *reinterpret_cast<Share*>(smem + S::kOffMisc + 16);
+    {
+        const Share mine = deal<S::kThreads>(p, smem);
+        if (mine.w0 >= mine.w1) return;
+        if (threadIdx.x == 0) sh = mine;
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(tmem_slot))

@@ -22,10 +22,10 @@
 //     that puts its largest element at 2^14, where f16 holds every bf16 down to 2^-28 of it.
 //   int4 keys: the nibble n + 8 alone is the f16 subnormal (n + 8) 2^-24 (2^-20 four bits up):
 //     one mask each, the queries take the other scale and the accumulators start at -8 sum q.
-//   E4M3 values: sign and the seven other bits, moved four down, are the bf16 of 2^-120 times the
-//     value; the weights take 2^112 along, less a power of two above the largest value scale so far
-//     (raised like the maximum), so that they stay in range.  Weights need bf16's range.
+//   E4M3 values: the two codes of a column pair side by side, then by way of f16 and fp32 to bf16, exact at
+//     every step (moving the bits takes fewer instructions, but all on one pipe).
 //   int4 values: 128 + (n + 8) by its bits, less 136.
+// Weights are bf16: they need its range.
 //
 // The running maximum is only raised when some score exceeds it by 2^8: a warp vote decides, and
 // most tiles need neither the shuffles nor the rescaling of the output.  Weights stay below 2^8
@@ -79,11 +79,6 @@ __device__ __forceinline__ uint32_t e4m3_f16(uint16_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
     return r;
 }
-// E4M3 codes in bytes 0 and 2 (odd = false) or 1 and 3 of w as two bf16, 2^-120 times the values.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, bool odd) {
-    const uint32_t x = odd ? w : __byte_perm(w, 0, 0x2404);  // the codes to bytes 1 and 3
-    return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-}
 // Nibbles i and i + 4 of w (two's complement) as two bf16: 128 + (n + 8) by its
 // bits, then less 136.
 __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int i) {
@@ -101,6 +96,12 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+// Two E4M3 codes to two bf16.
+__device__ __forceinline__ uint32_t e4m3_bf16(uint16_t w) {
+    const uint32_t h = e4m3_f16(w);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return bf16_pair(f.x, f.y);
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
 
@@ -267,7 +268,6 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
     const int g = lane >> 2, t = lane & 3, tid = threadIdx.x;
     constexpr int kSteps = D / 16;              // k16 steps of a score
     constexpr int kDm = S::kDm, kKm = S::kKm;
-    constexpr bool kRef = FMT == kKvE4m3;       // weights relative to a value scale
     Unit u = sh.u;
     int64_t unit0 = sh.unit0;
     uint32_t it = 0;
@@ -386,7 +386,6 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             m[n][0] = m[n][1] = kNoMax;
             l[n][0] = l[n][1] = 0.0f;
         }
-        float vlim = 0.0f, vf = 1.0f, vout = 1.0f;  // kRef: largest value scale in range, its factor, the output's
         // keys that every row of the unit sees need no mask
         const int inner0 = p.a.d.window ? max(0, u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - p.a.d.window) : 0;
         const int inner1 = u.len - u.n + u.rt * p.c.tq + 1;  // [inner0, inner1)
@@ -447,7 +446,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 const float* ks = reinterpret_cast<const float*>(smem + S::kOffSc + s * 2 * S::kScB) + kw0 + g;
                 const bool inner = key >= inner0 && key + 16 * kKm <= inner1;
                 const bool edge = key < u.key0 || key + 16 * kKm > u.key1;
-                float mx[R8][2], vw[kKm][2], vtop = 0.0f;
+                float mx[R8][2], vw[kKm][2];
 #pragma unroll
                 for (int n = 0; n < R8; ++n) mx[n][0] = mx[n][1] = kNoMax;
 #pragma unroll
@@ -458,7 +457,6 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                         if constexpr (FMT != kKvBf16) {
                             // keys outside [key0, key1) are nobody's: their scales may be anything
                             vw[km][h] = edge && (k < u.key0 || k >= u.key1) ? 0.0f : ks[S::kTk + 16 * km + 8 * h];
-                            vtop = fmaxf(vtop, vw[km][h]);
                         }
                         const float f = FMT != kKvBf16 ? ks[16 * km + 8 * h] : 1.0f;
 #pragma unroll
@@ -471,24 +469,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                                 mx[n][i] = fmaxf(mx[n][i], x);
                             }
                     }
-                bool raise = kRef && vtop > vlim;
+                bool raise = false;
 #pragma unroll
                 for (int n = 0; n < R8; ++n) raise |= mx[n][0] > m[n][0] + 8.0f || mx[n][1] > m[n][1] + 8.0f;
                 if (__any_sync(0xFFFFFFFFu, raise)) {
-                    float va = 1.0f;
-                    if (kRef) {
-#pragma unroll
-                        for (int d = 1; d < 32; d <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, d));
-                        if (vtop > vlim) {
-                            // scales up to 64 times this one's power of two keep p * scale * vf below 2^127
-                            const int e = min(max(((__float_as_int(vtop) >> 23) & 255) - 126, -14), 113);
-                            const float was = vout;
-                            vlim = pow2(e) * 64.0f;
-                            vf = pow2(112 - e);
-                            vout = pow2(e + 8);
-                            va = was / vout;
-                        }
-                    }
 #pragma unroll
                     for (int n = 0; n < R8; ++n)
 #pragma unroll
@@ -501,8 +485,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                             l[n][i] *= a;
 #pragma unroll
                             for (int j = 0; j < kDm; ++j) {
-                                o[j][n][i] *= a * va;
-                                o[j][n][2 + i] *= a * va;
+                                o[j][n][i] *= a;
+                                o[j][n][2 + i] *= a;
                             }
                         }
                 }
@@ -518,18 +502,17 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                             l[n][0] += p0;
                             l[n][1] += p1;
                             if constexpr (FMT != kKvBf16) {
-                                const float f = kRef ? vw[km][h] * vf : vw[km][h];
-                                p0 *= f;
-                                p1 *= f;
+                                p0 *= vw[km][h];
+                                p1 *= vw[km][h];
                             }
                             pb[km][n][h] = transposed(bf16_pair(p0, p1));
                         }
 #pragma unroll
                 for (int km = 0; km < kKm; ++km) {
-                    // bf16: what nobody's slots hold is cleared, not just weighted with 0 (codes are
-                    // finite whatever they are)
+                    // what nobody's slots hold is cleared, not just weighted with 0 (int4 codes are finite
+                    // whatever they are)
                     uint32_t vm[2] = {~0u, ~0u};
-                    if (FMT == kKvBf16 && edge) {
+                    if (FMT != kKvInt4 && edge) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int k = key + 16 * km + 8 * h + 2 * t;
@@ -541,11 +524,11 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                     for (int c = 0; c < S::kChunks; c += 2) {
                         uint32_t r[4];
                         ldsm4t(r, vt + chunk_at<S::kBoxB, S::kTk>(kw0 + 16 * km + (lane & 15), c + (lane >> 4)));
+                        if (FMT != kKvInt4 && edge) {
+                            r[0] &= vm[0], r[2] &= vm[0];
+                            r[1] &= vm[1], r[3] &= vm[1];
+                        }
                         if constexpr (FMT == kKvBf16) {
-                            if (edge) {
-                                r[0] &= vm[0], r[2] &= vm[0];
-                                r[1] &= vm[1], r[3] &= vm[1];
-                            }
                             const uint32_t a[4] = {r[0], r[2], r[1], r[3]};
 #pragma unroll
                             for (int n = 0; n < R8; ++n) mma16816<false>(o[c / 2][n], a, pb[km][n]);
@@ -554,8 +537,10 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t x = r[2 * i], y = r[2 * i + 1];
                                 if constexpr (FMT == kKvE4m3) {
-                                    const uint32_t a[4] = {e4m3_pair(x, false), e4m3_pair(x, true), e4m3_pair(y, false),
-                                                           e4m3_pair(y, true)};
+                                    // bytes 0 and 2 (column 2g of keys 2t, 2t + 1), then 1 and 3 (column 2g + 1)
+                                    const uint32_t xp = __byte_perm(x, 0, 0x3120), yp = __byte_perm(y, 0, 0x3120);
+                                    const uint32_t a[4] = {e4m3_bf16((uint16_t)xp), e4m3_bf16((uint16_t)(xp >> 16)),
+                                                           e4m3_bf16((uint16_t)yp), e4m3_bf16((uint16_t)(yp >> 16))};
 #pragma unroll
                                     for (int n = 0; n < R8; ++n) mma16816<false>(o[c + i][n], a, pb[km][n]);
                                 } else {
@@ -602,7 +587,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int r = 8 * n + 2 * t + i;
-                        const float a = ex2(m[n][i] - joined(r).x) * vout;
+                        const float a = ex2(m[n][i] - joined(r).x);
                         float* to = join + r * S::kLd;
 #pragma unroll
                         for (int j = 0; j < kDm; ++j)

@@ -6,7 +6,10 @@ namespace moe {
 namespace {
 
 // Sequences of at most this many rows (new tokens x query heads per key/value
-// head) run on the warp-level kernel, longer ones on the tcgen05 kernel.
+// head) run on the warp-level kernel, longer ones on the tcgen05 kernel: that one's
+// tiles have 128 rows, full or not, the other reads keys from L2 again for every 16.  Measured,
+// E4M3, 16 sequences of up to 6.8 thousand keys: with 16 to 48 rows each 73 us against
+// 95 us, with up to 128 rows 120 us against 97 us.
 constexpr int64_t kFewRows = 64;
 
 // Which kernels a call needs, from what the host knows of its sequences.  A

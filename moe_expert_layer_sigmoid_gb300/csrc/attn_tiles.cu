@@ -32,6 +32,10 @@
 // Warps: 0 copies, 1 products (and TMEM), 2-3 none, 4-11 stream A, 12-19 stream B (in each
 // four warps for the first 64 keys of a tile and four for the last), 20-23 conversion
 // of keys, 24-27 of values.
+//
+// Measured (GB300, 2048 tokens, D = 128): behind 27,953 keys 764 us in bf16, 1273 TFLOP/s, 65% of a library
+// product's rate; 1027 us in E4M3, 947 TFLOP/s, where the conversion's warps take issue slots (54% used
+// against 39%) from the softmax.  With no keys before it 57 us: fill, 14 pairs of key tiles per CTA.
 #include <atomic>
 #include <type_traits>
 

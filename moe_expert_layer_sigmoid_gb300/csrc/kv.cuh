@@ -17,8 +17,8 @@ struct KvRows {
     uint8_t* q;
     float* s;
     int64_t page_stride, head_stride, slot_stride;  // bytes
-    __device__ __forceinline__ uint8_t* row(int page, int h, int slot) const {
-        return q + page * page_stride + h * head_stride + slot * slot_stride;
+    __device__ __forceinline__ int64_t offset(int page, int h, int slot) const {
+        return page * page_stride + h * head_stride + slot * slot_stride;
     }
 };
 __host__ __device__ inline KvRows kv_rows(const moe_kv_t& c, bool keys) {

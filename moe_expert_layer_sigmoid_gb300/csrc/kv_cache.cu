@@ -5,9 +5,9 @@
 //   E4M3: s = absmax / 448, code = e4m3(x / s);  int4: s = absmax / 7,
 //   q = clamp(rint(x / s), -8, 7);  s = 0 gives codes 0.
 // Both kernels move each byte once: the bound is DRAM bandwidth, and for small
-// calls the launch.  D / 8 lanes take a row, 16 bytes of bf16 each, so a warp
-// has two (D = 128) or four rows' absolute maxima in a few shuffles; keys and
-// values go in one launch, the lane holding its 16 bytes of both.
+// calls the launch.  D / 16 lanes take a row, two pieces of 16 bytes of bf16 each, of the
+// keys and of the values, so what is done once per row is spread over 32 values, and
+// three (D = 128) or two exchanges make the absolute maxima of both.
 #include <cuda_fp8.h>
 
 #include "kv.cuh"
@@ -25,11 +25,35 @@ struct KvCopyParams {
     KvRows kr, vr;
     WsHeader* hdr;
     int T, H_kv, page, page_log2, n_slots;
+    // i / H_kv = i * h_mul >> h_shift for every i < 2^31: h_mul is 2^h_shift / H_kv rounded up, and the
+    // rounding adds less than i / 2^h_shift <= 1 / H_kv
+    uint32_t h_mul;
+    int h_shift;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The largest magnitude of a lane's two pieces of a row, in one of the two halves each.
+__device__ __forceinline__ uint32_t absmax_pair(uint4 a, uint4 b) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    return max_bf16x2(max_bf16x2(max_bf16x2(a.x & kAbs, a.y & kAbs), max_bf16x2(a.z & kAbs, a.w & kAbs)),
+                      max_bf16x2(max_bf16x2(b.x & kAbs, b.y & kAbs), max_bf16x2(b.z & kAbs, b.w & kAbs)));
+}
+
+// f / s rounded once, from the rounded reciprocal r of s: f * r corrected by its own remainder
+// (P. Markstein, IBM J. Res. Dev. 34, 1990), which is exact while nothing is tiny or infinite.
+// Written so that a zero keeps its sign.
+__device__ __forceinline__ float quotient(float f, float s, float r) {
+    const float y = f * r;
+    return __fmaf_rn(-__fmaf_rn(y, s, -f), r, y);
 }
 
 // The codes of two quotients: two E4M3 bytes, or two nibbles.
@@ -39,102 +63,101 @@ __device__ __forceinline__ uint32_t pair_code(float a, float b) {
     return (__float2int_rn(fminf(fmaxf(a, -8.0f), 7.0f)) & 15) | (__float2int_rn(fminf(fmaxf(b, -8.0f), 7.0f)) & 15) << 4;
 }
 
-// Quantises the row that D / 8 neighbouring lanes hold (8 values each) and
-// stores codes and scale where `put`; every lane of the warp takes part (the
-// lanes of a row all put or all do not).
-template <int FMT, int D>
-__device__ __forceinline__ void store_row(uint4 x, const KvRows& r, int page, int h, int slot,
-                                          int page_slots, int H_kv, int sub, bool put) {
-    uint8_t* row = r.row(page, h, slot);
-    if (FMT == kKvBf16) {
-        if (put) *reinterpret_cast<uint4*>(row + 16 * sub) = x;
-        return;
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float f[8], m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-        m = fmaxf(m, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-    }
-#pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float s = m / (FMT == kKvE4m3 ? 448.0f : 7.0f);
-    if (!put) return;
-    uint32_t code[2] = {0, 0};
-    if (s > 0.0f) {
-        // The recipe's code is that of the fp32 quotient f / s, and bf16 values over a bf16 maximum lie on
-        // midpoints between codes so often that its last bit matters.  A division for each element
-        // made the kernel issue-bound (115 us against 62 us of DRAM time at 65537 tokens of 8
-        // E4M3 heads).  With the rounded reciprocal r of the row's scale, f * r corrected by
-        // its own remainder is the rounded quotient (P. Markstein, IBM J. Res. Dev. 34, 1990); the remainder
-        // is exact while s is not tiny.
-        const float r = 1.0f / s;
-        if (s < 0x1p-80f) {
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                // (by pairs from the row's words: no indexing of registers)
-                const uint32_t x2 = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-                const uint32_t d = pair_code<FMT>(bf16_lo(x2) / s, bf16_hi(x2) / s);
-                if (FMT != kKvE4m3) code[0] |= d << (8 * i);
-                else if (i < 2) code[0] |= d << (16 * i);
-                else code[1] |= d << (16 * i - 32);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = f[i] * r, q = __fmaf_rn(__fmaf_rn(-y, s, f[i]), r, y);
-                f[i] = copysignf(q, f[i]);  // (-0 stays -0)
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t d = pair_code<FMT>(f[2 * i], f[2 * i + 1]);
-                if (FMT == kKvE4m3) code[i / 2] |= d << (16 * (i & 1));
-                else code[0] |= d << (8 * i);
-            }
-        }
-    }
-    if (FMT == kKvE4m3) *reinterpret_cast<uint2*>(row + 8 * sub) = make_uint2(code[0], code[1]);
-    else *reinterpret_cast<uint32_t*>(row + 4 * sub) = code[0];
-    if (sub == 0) r.s[((int64_t)page * H_kv + h) * page_slots + slot] = s;
-}
-
-// The eight values that a lane's codes stand for, as bf16.
+// The codes of eight values, `plain` for scales that the corrected product does not hold for.
 template <int FMT>
-__device__ __forceinline__ uint4 load_row(const KvRows& r, int page, int h, int slot, int page_slots,
-                                          int H_kv, int sub) {
-    const uint8_t* row = r.row(page, h, slot);
-    if (FMT == kKvBf16) return *reinterpret_cast<const uint4*>(row + 16 * sub);
-    const float s = r.s[((int64_t)page * H_kv + h) * page_slots + slot];
-    uint32_t w[4];
-    if (FMT == kKvE4m3) {
-        const uint2 c = *reinterpret_cast<const uint2*>(row + 8 * sub);
-#pragma unroll
+__device__ __forceinline__ uint2 codes_of(uint4 x, float s, float r, bool plain) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t d[4];
+    if (plain) {
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            const uint32_t c2 = ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 0xFFFFu;
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c2, __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            w[i] = pack_bf16(f.x * s, f.y * s);
+            // (by pairs from the row's words: no indexing of registers)
+            const uint32_t x2 = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+            const uint32_t c = pair_code<FMT>(bf16_lo(x2) / s, bf16_hi(x2) / s);
+            if (i == 0) d[0] = c;
+            else if (i == 1) d[1] = c;
+            else if (i == 2) d[2] = c;
+            else d[3] = c;
         }
     } else {
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(row + 4 * sub);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int lo = (int)(c << (28 - 8 * i)) >> 28, hi = (int)(c << (24 - 8 * i)) >> 28;
-            w[i] = pack_bf16((float)lo * s, (float)hi * s);
-        }
+        for (int i = 0; i < 4; ++i)
+            d[i] = pair_code<FMT>(quotient(bf16_lo(w[i]), s, r), quotient(bf16_hi(w[i]), s, r));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if (FMT == kKvE4m3) return make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
+    return make_uint2(d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24, 0);
+}
+
+// Stores a lane's two pieces of a row whose largest magnitude is m, as bf16 or as codes with their scale.
+template <int FMT, int D>
+__device__ __forceinline__ void store_row(const uint4 (&x)[2], float m, uint8_t* row, float* scale, int sub) {
+    constexpr int kLanes = D / 16;
+    if (FMT == kKvBf16) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) reinterpret_cast<uint4*>(row)[sub + j * kLanes] = x[j];
+        return;
+    }
+    constexpr float kTop = FMT == kKvE4m3 ? 448.0f : 7.0f;
+    // The recipe's code is that of the fp32 quotient, and bf16 values over a bf16 maximum lie on
+    // midpoints between codes so often that its last bit matters.  A division for each element
+    // made the kernel issue-bound (115 us against 62 us of DRAM time at 65537 tokens of 8
+    // E4M3 heads).
+    const bool plain = m < 0x1p-70f || m == __int_as_float(0x7F800000);
+    const float s = plain ? m / kTop : quotient(m, kTop, 1.0f / kTop);
+    uint2 c[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+    if (s > 0.0f) {
+        const float r = 1.0f / s;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c[j] = codes_of<FMT>(x[j], s, r, plain);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (FMT == kKvE4m3) reinterpret_cast<uint2*>(row)[sub + j * kLanes] = c[j];
+        else reinterpret_cast<uint32_t*>(row)[sub + j * kLanes] = c[j].x;
+    }
+    if (sub == 0) *scale = s;
+}
+
+// A lane's two pieces of a row, as bf16.
+template <int FMT, int D>
+__device__ __forceinline__ void load_row(uint4 (&x)[2], const uint8_t* row, const float* scale, int sub) {
+    constexpr int kLanes = D / 16;
+    const float s = FMT == kKvBf16 ? 0.0f : *scale;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int at = sub + j * kLanes;
+        uint32_t w[4];
+        if (FMT == kKvBf16) {
+            x[j] = reinterpret_cast<const uint4*>(row)[at];
+            continue;
+        } else if (FMT == kKvE4m3) {
+            const uint2 c = reinterpret_cast<const uint2*>(row)[at];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c2 = ((i < 2 ? c.x : c.y) >> (16 * (i & 1))) & 0xFFFFu;
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c2, __NV_E4M3);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                w[i] = pack_bf16(f.x * s, f.y * s);
+            }
+        } else {
+            const uint32_t c = reinterpret_cast<const uint32_t*>(row)[at];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int lo = (int)(c << (28 - 8 * i)) >> 28, hi = (int)(c << (24 - 8 * i)) >> 28;
+                w[i] = pack_bf16((float)lo * s, (float)hi * s);
+            }
+        }
+        x[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 template <int FMT, int D, bool WRITE>
 __global__ void __launch_bounds__(256) kv_copy_kernel(const KvCopyParams p) {
-    constexpr int kLanes = D / 8;  // lanes of a row
+    constexpr int kLanes = D / 16;  // lanes of a row
     const unsigned i = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;  // row: token and head (below 2^31)
     const int sub = threadIdx.x % kLanes;
     const bool live = i < (unsigned)p.T * (unsigned)p.H_kv;
-    const int t = live ? i / (unsigned)p.H_kv : 0, h = live ? i - t * (unsigned)p.H_kv : 0;
+    const int t = live ? (int)((uint64_t)i * p.h_mul >> p.h_shift) : 0, h = live ? (int)i - t * p.H_kv : 0;
     int slot = live ? p.slots[t] : -1;
     if (slot >= p.n_slots) {
         if (sub == 0) record_error(p.hdr, kErrBadSlot);
@@ -142,27 +165,50 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const KvCopyParams p) {
     }
     const bool put = slot >= 0;
     const int page = put ? slot >> p.page_log2 : 0, at = put ? slot & (p.page - 1) : 0;
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    // (one offset for both pools and one for both scales)
+    const int64_t row = p.kr.offset(page, h, at), scale = ((int64_t)page * p.H_kv + h) * p.page + at;
+    uint4 k[2], v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) k[j] = v[j] = make_uint4(0, 0, 0, 0);
     if (WRITE) {
         if (put) {
-            k = *reinterpret_cast<const uint4*>(p.k + t * p.ldk + h * D + 8 * sub);
-            v = *reinterpret_cast<const uint4*>(p.v + t * p.ldv + h * D + 8 * sub);
+            const uint4* pk = reinterpret_cast<const uint4*>(p.k + t * p.ldk + h * D) + sub;
+            const uint4* pv = reinterpret_cast<const uint4*>(p.v + t * p.ldv + h * D) + sub;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                k[j] = pk[j * kLanes];
+                v[j] = pv[j * kLanes];
+            }
         }
-        store_row<FMT, D>(k, p.kr, page, h, at, p.page, p.H_kv, sub, put);
-        store_row<FMT, D>(v, p.vr, page, h, at, p.page, p.H_kv, sub, put);
+        float mk = 0.0f, mv = 0.0f;
+        if (FMT != kKvBf16) {
+            // Magnitudes of bf16 are bf16: keys' in the low half and values' in the high one, one exchange for both.
+            const uint32_t a = absmax_pair(k[0], k[1]), b = absmax_pair(v[0], v[1]);
+            uint32_t m = max_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            mk = fmaxf(bf16_lo(m), 0.0f);  // (a row of NaN alone has none)
+            mv = fmaxf(bf16_hi(m), 0.0f);
+        }
+        if (!put) return;
+        store_row<FMT, D>(k, mk, p.kr.q + row, p.kr.s + scale, sub);
+        store_row<FMT, D>(v, mv, p.vr.q + row, p.vr.s + scale, sub);
     } else if (live) {
         if (put) {
-            k = load_row<FMT>(p.kr, page, h, at, p.page, p.H_kv, sub);
-            v = load_row<FMT>(p.vr, page, h, at, p.page, p.H_kv, sub);
+            load_row<FMT, D>(k, p.kr.q + row, p.kr.s + scale, sub);
+            load_row<FMT, D>(v, p.vr.q + row, p.vr.s + scale, sub);
         }
-        reinterpret_cast<uint4*>(p.k_out)[(int64_t)i * kLanes + sub] = k;
-        reinterpret_cast<uint4*>(p.v_out)[(int64_t)i * kLanes + sub] = v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            reinterpret_cast<uint4*>(p.k_out)[(int64_t)i * (D / 8) + sub + j * kLanes] = k[j];
+            reinterpret_cast<uint4*>(p.v_out)[(int64_t)i * (D / 8) + sub + j * kLanes] = v[j];
+        }
     }
 }
 
 template <bool WRITE>
 cudaError_t launch_copy(const KvCopyParams& p, const moe_kv_dims_t& d, cudaStream_t st) {
-    const int rows = 256 / (d.D / 8);  // of a CTA
+    const int rows = 256 / (d.D / 16);  // of a CTA
     const unsigned grid = (unsigned)(((int64_t)d.T * d.H_kv + rows - 1) / rows);
     const bool wide = d.D == 128;
     switch (d.format) {
@@ -192,6 +238,9 @@ KvCopyParams copy_params(const int32_t* slots, const moe_kv_dims_t& d, const moe
     p.hdr = hdr;
     p.T = d.T;
     p.H_kv = d.H_kv;
+    p.h_shift = 31;
+    while ((1ll << (p.h_shift - 31)) < p.H_kv) ++p.h_shift;
+    p.h_mul = (uint32_t)(((1ull << p.h_shift) + p.H_kv - 1) / p.H_kv);
     p.page = d.page;
     p.page_log2 = __builtin_ctz(d.page);
     p.n_slots = d.n_pages * d.page;

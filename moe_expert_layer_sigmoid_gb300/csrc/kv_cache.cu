@@ -56,36 +56,44 @@ __device__ __forceinline__ float quotient(float f, float s, float r) {
     return __fmaf_rn(-__fmaf_rn(y, s, -f), r, y);
 }
 
-// The codes of two quotients: two E4M3 bytes, or two nibbles.
+// The codes of eight quotients.  int4: no quotient by s rounds to more than 7 in magnitude, so the
+// recipe's clamp has nothing to do; adding 1.5 * 2^23 leaves the rounded number in the low bits.
 template <int FMT>
-__device__ __forceinline__ uint32_t pair_code(float a, float b) {
-    if (FMT == kKvE4m3) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    return (__float2int_rn(fminf(fmaxf(a, -8.0f), 7.0f)) & 15) | (__float2int_rn(fminf(fmaxf(b, -8.0f), 7.0f)) & 15) << 4;
-}
-
-// The codes of eight values, `plain` for scales that the corrected product does not hold for.
-template <int FMT>
-__device__ __forceinline__ uint2 codes_of(uint4 x, float s, float r, bool plain) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t d[4];
-    if (plain) {
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            // (by pairs from the row's words: no indexing of registers)
-            const uint32_t x2 = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-            const uint32_t c = pair_code<FMT>(bf16_lo(x2) / s, bf16_hi(x2) / s);
-            if (i == 0) d[0] = c;
-            else if (i == 1) d[1] = c;
-            else if (i == 2) d[2] = c;
-            else d[3] = c;
-        }
-    } else {
+__device__ __forceinline__ uint2 codes_of(const float (&f)[8]) {
+    if (FMT == kKvE4m3) {
+        uint32_t d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            d[i] = pair_code<FMT>(quotient(bf16_lo(w[i]), s, r), quotient(bf16_hi(w[i]), s, r));
+            d[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        return make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
     }
-    if (FMT == kKvE4m3) return make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
-    return make_uint2(d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24, 0);
+    uint32_t d = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t low = (1u << (4 * i)) - 1;  // what is in place
+        d = (d & low) | (__float_as_uint(f[i] + 12582912.0f) << (4 * i) & ~low);
+    }
+    return make_uint2(d, 0);
+}
+
+// The codes of eight values; `plain` for scales that the corrected product does not hold for.
+template <int FMT>
+__device__ __forceinline__ uint2 quantised(uint4 x, float s, float r, bool plain) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], s, r);
+    }
+    return codes_of<FMT>(f);
 }
 
 // Stores a lane's two pieces of a row whose largest magnitude is m, as bf16 or as codes with their scale.
@@ -108,7 +116,7 @@ __device__ __forceinline__ void store_row(const uint4 (&x)[2], float m, uint8_t*
     if (s > 0.0f) {
         const float r = 1.0f / s;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c[j] = codes_of<FMT>(x[j], s, r, plain);
+        for (int j = 0; j < 2; ++j) c[j] = quantised<FMT>(x[j], s, r, plain);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -152,7 +160,7 @@ __device__ __forceinline__ void load_row(uint4 (&x)[2], const uint8_t* row, cons
 }
 
 template <int FMT, int D, bool WRITE>
-__global__ void __launch_bounds__(256) kv_copy_kernel(const KvCopyParams p) {
+__global__ void __launch_bounds__(256, 5) kv_copy_kernel(const KvCopyParams p) {
     constexpr int kLanes = D / 16;  // lanes of a row
     const unsigned i = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;  // row: token and head (below 2^31)
     const int sub = threadIdx.x % kLanes;

@@ -4,7 +4,7 @@
 // Each cached byte is used for few rows only, so the floor is the cache's bytes
 // from HBM; what stands in the way is the work per byte in the SM, so the design keeps
 // copies in flight and that work small.  A CTA is four warps of compute and one that issues
-// TMA copies into a ring of stages, three CTAs per SM (two with 16 rows).  Every
+// TMA copies into a ring of stages, three CTAs per SM (two with 16 rows, four with int4 rows of 64).  Every
 // warp takes its own quarter of a stage's keys through scores, softmax and values
 // with no exchange with the others; the warps' (maximum, sum, output) are joined once
 // per unit.
@@ -711,8 +711,8 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool beh
     p.c.hs = a.d.H_kv * p.c.subs;
     p.c.tk_log2 = __builtin_ctz(S::kTk);
     p.c.page_log2 = __builtin_ctz(a.d.page);
-    // (drafts, a wide int4 step and a bf16 step took 73.4, 40.7 and 33.1 us at 1, 67.1, 39.3 and 31.9 at 3,
-    // 67.2, 41.3 and 32.1 at 5)
+    // (drafts, a wide int4 step and a bf16 step take 65.2, 35.8 and 31.6 us at 2, 63.6, 35.3 and 31.1 at 3,
+    // 63.6, 36.7 and 31.2 at 4, 65.4, 37.1 and 31.3 at 6)
     p.c.unit_cost = 3;
     p.c.min_share = 4;
     p.c.rows_lo = rows_lo;
@@ -743,7 +743,7 @@ template <int FMT, int D>
 cudaError_t launch_for(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, bool eight, bool behind, float* part,
                        unsigned* counters, cudaStream_t st) {
     return eight ? launch<FMT, D, 1>(a, rows_lo, rows_hi, behind, part, counters, st)
-                                 : launch<FMT, D, 2>(a, rows_lo, rows_hi, behind, part, counters, st);
+                 : launch<FMT, D, 2>(a, rows_lo, rows_hi, behind, part, counters, st);
 }
 
 }  // namespace

@@ -869,7 +869,8 @@ cudaError_t launch(const AttnArgs& a, int64_t rows_lo, int64_t rows_hi, float* p
     p.c.hs = a.d.H_kv;
     p.c.tk_log2 = 7;
     p.c.page_log2 = __builtin_ctz(a.d.page);
-    // (a 2048-token chunk and a mixed batch took 70.7 and 66.1 us at 1, 57.8 and 63.3 at 3, 61.9 and 62.9 at 6)
+    // (a 2048-token chunk and a mixed batch take 57.4 and 48.2 us at 2, 56.9 and 48.0 at 3, 57.4 and 47.9 at 4, 60.4
+    // and 48.1 at 6)
     p.c.unit_cost = 3;
     p.c.min_share = 4;
     p.c.rows_lo = rows_lo;

@@ -1,0 +1,31 @@
+// Index arithmetic of the attention kernels, in plain C++ that a host compiler takes too: its
+// edges are checked there.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define MOE_HD __host__ __device__ __forceinline__
+#else
+#define MOE_HD inline
+#endif
+
+namespace moe {
+
+// The chunk kernel's ring of code tiles.  Keys and values take turns (copy number `it` is even
+// for keys, odd for values) and each is converted by a group of its own.  A wait by parity tells a
+// phase only from the one before it, so a group has to see every phase of the barriers it waits on.  With
+// one "full" barrier to a slot and an odd number of slots it would see every second one: the copy before its
+// own, still in flight, would leave the barrier with the parity that it waits for.  So there are two to
+// a slot, and each belongs to one group.  The copying warp waits for both groups' slots in order: one
+// "free" barrier to a slot.
+template <int SLOTS>
+struct CodeRing {
+    static constexpr uint32_t kFull = 2 * SLOTS;  // "full" barriers
+    static MOE_HD uint32_t slot(uint32_t it) { return it % SLOTS; }
+    static MOE_HD uint32_t full(uint32_t it) { return it % kFull; }
+    static MOE_HD uint32_t full_parity(uint32_t it) { return (it / kFull) & 1; }
+    static MOE_HD uint32_t free_parity(uint32_t it) { return ((it / SLOTS) & 1) ^ 1; }
+};
+
+}  // namespace moe

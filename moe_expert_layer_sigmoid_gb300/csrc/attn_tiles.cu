@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "attn.cuh"
+#include "attn_index.h"
 #include "umma.cuh"
 
 namespace moe {
@@ -56,11 +57,13 @@ struct TilesShape {
     static constexpr int kBoxB = kRowB < 128 ? kRowB : 128;
     static constexpr int kTileB = kTk * D * 2;                // a bf16 tile
     static constexpr int kSlots = kQuant ? 3 : 4;             // bf16 tiles of keys or values
-    // Tiles of codes.  No more than bf16 slots: then a tile's codes are only there once the tile three
-    // before it is converted, so the two conversion groups cannot be a whole round of slots apart and
-    // take one phase of a slot's barrier for another.
+    // Tiles of codes.  No more than bf16 slots: a tile's codes are only there (CodeRing's barriers tell
+    // exactly) once the tile three before it is converted, for which the slot's product before that was done.
+    // So the wait for the bf16 slot of a tile cannot take the release before the last for the last.
     static constexpr int kRaws = kQuant ? 3 : 0;
     static_assert(kRaws <= kSlots, "phases");
+    using Ring = CodeRing<kQuant ? kRaws : 1>;
+    static constexpr int kRawFulls = kQuant ? Ring::kFull : 0;
     static constexpr int kRawB = kTk * kRowB;
     // Key and value scales of a tile.  Four slots: while V of tile i is in use (K of tile i + 2 would take its
     // place) no codes after K of tile i + 3 are loaded.
@@ -78,8 +81,8 @@ struct TilesShape {
     static constexpr int kOffStage = kOffSc + kScSlots * kScB;
     static constexpr int kOffMl = kOffStage + 16 * 512;  // the streams' maxima and sums: [stream][half][row]
     static constexpr int kOffBar = kOffMl + 4 * kTileRows * 8;
-    // barriers: FULL, EMPTY [kSlots]; RAWF, RAWE [kRaws]; SF, PF, OD [2]; QF, QE, TD
-    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRawF = 2 * kSlots, kBarRawE = kBarRawF + kRaws,
+    // barriers: FULL, EMPTY [kSlots]; RAWF [kRawFulls], RAWE [kRaws]; SF, PF, OD [2]; QF, QE, TD
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarRawF = 2 * kSlots, kBarRawE = kBarRawF + kRawFulls,
                          kBarSf = kBarRawE + kRaws, kBarPf = kBarSf + 2, kBarOd = kBarPf + 2,
                          kBarQf = kBarOd + 2, kBarQe = kBarQf + 1, kBarTd = kBarQe + 1, kNumBars = kBarTd + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -199,10 +202,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             mbar_init(bar(S::kBarFull + s), S::kQuant ? 4 : 1);
             mbar_init(bar(S::kBarEmpty + s), 1);
         }
-        for (int s = 0; s < S::kRaws; ++s) {
-            mbar_init(bar(S::kBarRawF + s), 1);
-            mbar_init(bar(S::kBarRawE + s), 4);
-        }
+        for (int s = 0; s < S::kRawFulls; ++s) mbar_init(bar(S::kBarRawF + s), 1);
+        for (int s = 0; s < S::kRaws; ++s) mbar_init(bar(S::kBarRawE + s), 4);
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(S::kBarSf + x), 1);
             mbar_init(bar(S::kBarPf + x), 8);
@@ -243,7 +244,11 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             const int page = 1 << p.c.page_log2;
             const int box_rows = page < kTk ? page : kTk;
             const int boxes = kTk / box_rows;
+            using Ring = typename S::Ring;
             constexpr uint32_t kRing = S::kQuant ? S::kRaws : kSlots;
+            // the barrier and its parity that copy k completes
+            auto full = [&](uint32_t k) { return bar(S::kQuant ? S::kBarRawF + Ring::full(k) : S::kBarFull + k % kSlots); };
+            auto parity = [&](uint32_t k) { return S::kQuant ? Ring::full_parity(k) : (k / kSlots) & 1; };
             uint32_t it = 0;   // slots filled
             uint32_t tiles = 0, n_q = 0;
             bool ok = true;
@@ -298,12 +303,13 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     const int at = key & (page - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-                        const int s = it % kRing;
-                        if (!mbar_wait(bar((S::kQuant ? S::kBarRawE : S::kBarEmpty) + s), ((it / kRing) & 1) ^ 1, abort_flag, hdr)) {
+                        const int s = it % kRing;  // (its wait takes one phase after the other)
+                        if (!mbar_wait(bar((S::kQuant ? S::kBarRawE : S::kBarEmpty) + s),
+                                       S::kQuant ? Ring::free_parity(it) : ((it / kSlots) & 1) ^ 1, abort_flag, hdr)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t done = bar((S::kQuant ? S::kBarRawF : S::kBarFull) + s);
+                        const uint32_t done = full(it);
                         const uint32_t sc_bytes = S::kQuant ? box_rows * 4 : 0;
                         if (lane == 0) mbar_expect_tx(done, n_live * (box_rows * S::kRowB + sc_bytes));
                         __syncwarp();
@@ -326,7 +332,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             if (!ok && n_q) mbar_drain(bar(S::kBarQf), (n_q - 1) & 1, hdr);
             if (!ok)  // no copy may be in flight when the CTA ends
                 for (uint32_t k = it > kRing ? it - kRing : 0; k < it; ++k)
-                    mbar_drain(bar((S::kQuant ? S::kBarRawF : S::kBarFull) + k % kRing), (k / kRing) & 1, hdr);
+                    mbar_drain(full(k), parity(k), hdr);
         } else if (warp == 1) {
             // ---------------------------------------------------------- products
             // The whole warp follows the loop, so that its values are uniform; one thread issues.
@@ -792,6 +798,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
         // -------------------------------------------------------------- conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegConv));
         if constexpr (S::kQuant) {
+            using Ring = typename S::Ring;
             const int r = threadIdx.x & 127, kv = warp >= 24;  // row (key) of the tile; keys or values
             uint32_t it = kv, tiles = 0;
             bool ok = true;
@@ -801,8 +808,8 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 for (; tile < end; ++tile, ++tiles, it += 2) {
                     const int key = (u.tile0 + tile) * kTk + r;
                     const bool seen = key >= u.key0 && key < u.key1;
-                    const int sl = it % kSlots, rw = it % S::kRaws;
-                    if (ok) ok = mbar_wait(bar(S::kBarRawF + rw), (it / S::kRaws) & 1, abort_flag, hdr);
+                    const int sl = it % kSlots, rw = Ring::slot(it);
+                    if (ok) ok = mbar_wait(bar(S::kBarRawF + Ring::full(it)), Ring::full_parity(it), abort_flag, hdr);
                     if (ok) ok = mbar_wait(bar(S::kBarEmpty + sl), ((it / kSlots) & 1) ^ 1, abort_flag, hdr);
                     const uint8_t* raw = smem + S::kOffRaw + rw * S::kRawB + r * S::kRowB;
                     uint8_t* slot = smem + S::kOffKv + sl * S::kTileB + r * 128;

@@ -18,6 +18,7 @@
 // follows them.
 #pragma once
 
+#include "attn_index.h"
 #include "kv.cuh"
 #include "tma.cuh"
 
@@ -64,12 +65,9 @@ __device__ __forceinline__ void load_seq(const AttnParams& p, int b, int& tok0, 
     tok0 = __ldg(p.a.q_off + b);
     const int t1 = __ldg(p.a.q_off + b + 1);
     len = __ldg(p.a.kv_len + b);
-    n = t1 - tok0;
-    if (tok0 < 0 || n < 0 || t1 > p.a.d.T || len < 0 ||
-        (int64_t)len > ((int64_t)p.a.d.max_pages << p.c.page_log2)) {
-        if (n != 0) record_error(p.a.hdr, kErrBadSeq);
-        n = 0;
-    }
+    n = 0;
+    if (seq_ok(tok0, t1, len, p.a.d.T, (int64_t)p.a.d.max_pages << p.c.page_log2)) n = t1 - tok0;
+    else if (t1 != tok0) record_error(p.a.hdr, kErrBadSeq);
     const int64_t rows = (int64_t)n * (p.a.d.H / p.a.d.H_kv);
     if (rows <= p.c.rows_lo || rows > p.c.rows_hi) n = 0;
 }

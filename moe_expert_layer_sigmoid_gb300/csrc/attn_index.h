@@ -28,4 +28,10 @@ struct CodeRing {
     static MOE_HD uint32_t free_parity(uint32_t it) { return ((it / SLOTS) & 1) ^ 1; }
 };
 
+// Whether a sequence's rows [tok0, t1) lie in the batch's T and its length in the page table.  (By comparisons
+// only: the difference of two offsets that are anything may wrap to a number of tokens that looks sound.)
+MOE_HD bool seq_ok(int tok0, int t1, int len, int T, int64_t max_len) {
+    return tok0 >= 0 && t1 >= tok0 && t1 <= T && len >= 0 && len <= max_len;
+}
+
 }  // namespace moe

@@ -40,7 +40,6 @@
 #include <type_traits>
 
 #include "attn.cuh"
-#include "attn_index.h"
 #include "umma.cuh"
 
 namespace moe {

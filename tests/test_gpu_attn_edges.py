@@ -1,0 +1,26 @@
+"""Attention over the paged cache at the edges of what a call may hold."""
+import pytest
+import torch
+
+import attn_cases as ac
+import moe_expert_layer_sigmoid_gb300 as moe
+from test_gpu_attn_paged import run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("end", [-2 ** 31, -2 ** 31 + 4, -1, 2 ** 31 - 1])
+@pytest.mark.parametrize("n", [4, 60])
+def test_offsets_that_hold_anything(fmt, end, n):
+    """Offsets whose difference does not fit 32 bits: the two sequences that share one are left out and
+    recorded, the others are as ever."""
+    b = ac.make([5, n, 3, 1, 40], [30, 70, 20, 50, 90], 8, 2, 64, 16, fmt, seed=3)
+    b.q_off[2] = end
+    out, lse, ws = run(b)
+    assert moe.moe_check_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK
+    ref, z, bo, bl = ac.reference(b)
+    at = torch.tensor(list(range(5)) + list(range(8 + n, 49 + n)), device="cuda")
+    assert ((out.double() - ref)[at].abs() <= bo[at]).all()
+    assert ((lse.double() - z)[at].abs() <= bl[at]).all()
+    assert (out[5:8 + n] == 7).all() and (lse[5:8 + n] == 7).all()

@@ -75,7 +75,7 @@ __device__ __forceinline__ void load_seq(const AttnParams& p, int b, int& tok0, 
 __device__ __forceinline__ void unit_keys(const AttnParams& p, Unit& u) {
     const int i0 = u.rt * p.c.tq, i1 = min(u.n, i0 + p.c.tq) - 1;
     u.key1 = max(0, u.len - u.n + i1 + 1);
-    u.key0 = p.a.d.window ? max(0, u.len - u.n + i0 - p.a.d.window + 1) : 0;
+    u.key0 = first_key(u.len - u.n + i0, p.a.d.window);
     u.tile0 = u.key0 >> p.c.tk_log2;
     u.tiles = max(1, (int)(((int64_t)u.key1 + (1 << p.c.tk_log2) - 1) >> p.c.tk_log2) - u.tile0);
 }

@@ -34,4 +34,8 @@ MOE_HD bool seq_ok(int tok0, int t1, int len, int T, int64_t max_len) {
     return tok0 >= 0 && t1 >= tok0 && t1 <= T && len >= 0 && len <= max_len;
 }
 
+// The first key that the token at `pos` sees through a window (0: all).  (No difference is taken before it is
+// known to be a key: a window may be any number, a position may lie before the start.)
+MOE_HD int first_key(int pos, int window) { return window && pos >= window ? pos - window + 1 : 0; }
+
 }  // namespace moe

@@ -378,7 +378,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             for (int i = 0; i < 2; ++i) {
                 const int tok = token_of(8 * n + 2 * t + i);
                 pos[n][i] = tok >= 0 ? u.len - u.n + tok : -1;
-                first[n][i] = p.a.d.window ? max(0, pos[n][i] - p.a.d.window + 1) : 0;
+                first[n][i] = first_key(pos[n][i], p.a.d.window);
             }
         float o[kDm][R8][4];
 #pragma unroll
@@ -392,7 +392,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             l[n][0] = l[n][1] = 0.0f;
         }
         // keys that every row of the unit sees need no mask
-        const int inner0 = p.a.d.window ? max(0, u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - p.a.d.window) : 0;
+        const int inner0 = first_key(u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - 1, p.a.d.window);
         const int inner1 = u.len - u.n + u.rt * p.c.tq + 1;  // [inner0, inner1)
 
         for (; tile < end; ++tile, ++it) {

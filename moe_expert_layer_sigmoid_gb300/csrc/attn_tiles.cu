@@ -175,7 +175,7 @@ __device__ __forceinline__ Stretch stretch(const AttnParams& p, const Share& sh,
         // the stream's tokens [a, b) of the sequence, their keys [k0, k1)
         const int a = i0 + (s.split ? 0 : x * half), b = min(u.n, s.split ? i0 + have : a + half);
         const int k1 = max(0, u.len - u.n + b);
-        const int k0 = p.a.d.window ? max(0, u.len - u.n + a - p.a.d.window + 1) : 0;
+        const int k0 = first_key(u.len - u.n + a, p.a.d.window);
         s.lo[x] = max(s.t0, k0 / kTk - u.tile0);
         s.hi[x] = k1 > k0 ? min(s.t1, (k1 + kTk - 1) / kTk - u.tile0) : s.lo[x];
     }
@@ -468,7 +468,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             const bool live = r < half * G && tok < v.n;
             orow = live ? (int64_t)(v.tok0 + tok) * p.a.d.H + hd : -1;
             pos = live ? v.len - v.n + tok : -1;
-            first = p.a.d.window ? max(0, pos - p.a.d.window + 1) : 0;
+            first = first_key(pos, p.a.d.window);
         };
         // 16 columns of the warp's rows (bf16 pairs) to `out`, by way of shared memory, 16 rows at a time:
         // each two lanes store 32 bytes of a row
@@ -498,7 +498,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             // keys that all of the stream's rows see need no mask
             const int i0 = u.rt * p.c.tq + (s.split ? 0 : x * half);
             const int inner1 = u.len - u.n + i0 + 1;
-            const int inner0 = p.a.d.window ? u.len - u.n + min(u.n, i0 + half) - p.a.d.window : 0;
+            const int inner0 = first_key(u.len - u.n + min(u.n, i0 + half) - 1, p.a.d.window);
             // the stream's tiles: i0 .. (every other one with one row tile)
             const int step = s.split ? 2 : 1;
             const int beg = s.split ? s.t0 + x : x ? s.lo[1] : s.lo[0], end = x ? s.hi[1] : s.hi[0];

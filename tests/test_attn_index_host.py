@@ -11,6 +11,7 @@ SOURCE = """
 #include "attn_index.h"
 extern "C" {
 int seq_ok(int tok0, int t1, int len, int T, int64_t max_len) { return moe::seq_ok(tok0, t1, len, T, max_len); }
+int first_key(int pos, int window) { return moe::first_key(pos, window); }
 }
 """
 MIN, MAX = -2 ** 31, 2 ** 31 - 1
@@ -30,3 +31,9 @@ def test_offsets_that_hold_anything(L):
         for most in (16, 36, 2 ** 31 - 16):
             want = 0 <= tok0 <= t1 <= T and 0 <= len_ <= most
             assert L.seq_ok(tok0, t1, len_, T, most) == want, (tok0, t1, len_, T, most)
+
+
+def test_first_key(L):
+    for pos in [MIN, MIN + 1, -100, -1, 0, 1, 99, 100, 101, 5000, MAX - 17, MAX]:
+        for window in [0, 1, 2, 99, 100, 101, 5000, MAX - 1, MAX]:
+            assert L.first_key(pos, window) == (max(0, pos - window + 1) if window else 0), (pos, window)

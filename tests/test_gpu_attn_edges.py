@@ -4,7 +4,7 @@ import torch
 
 import attn_cases as ac
 import moe_expert_layer_sigmoid_gb300 as moe
-from test_gpu_attn_paged import run
+from test_gpu_attn_paged import ok, run
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +24,13 @@ def test_offsets_that_hold_anything(fmt, end, n):
     assert ((out.double() - ref)[at].abs() <= bo[at]).all()
     assert ((lse.double() - z)[at].abs() <= bl[at]).all()
     assert (out[5:8 + n] == 7).all() and (lse[5:8 + n] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30, 130, 3])
+@pytest.mark.parametrize("G", [1, 4, 24])
+def test_windows_with_tokens_before_the_start(fmt, window, G):
+    """A window of any size, the largest standing for none, where some tokens sit before the start."""
+    new = [10, 3, 1, 200, 40, 1]
+    total = [5, 1, 0, 100, 17, 300]
+    ok(ac.make(new, total, 2 * G, 2, 128, 16, fmt, window=window, seed=G))

@@ -77,7 +77,7 @@ __device__ __forceinline__ void unit_keys(const AttnParams& p, Unit& u) {
     u.key1 = max(0, u.len - u.n + i1 + 1);
     u.key0 = first_key(u.len - u.n + i0, p.a.d.window);
     u.tile0 = u.key0 >> p.c.tk_log2;
-    u.tiles = max(1, (int)(((int64_t)u.key1 + (1 << p.c.tk_log2) - 1) >> p.c.tk_log2) - u.tile0);
+    u.tiles = max(1, tiles_until(u.key1, p.c.tk_log2) - u.tile0);
 }
 
 __device__ __forceinline__ int row_tiles(const AttnParams& p, int n) {

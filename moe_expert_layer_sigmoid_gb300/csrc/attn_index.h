@@ -38,4 +38,15 @@ MOE_HD bool seq_ok(int tok0, int t1, int len, int T, int64_t max_len) {
 // known to be a key: a window may be any number, a position may lie before the start.)
 MOE_HD int first_key(int pos, int window) { return window && pos >= window ? pos - window + 1 : 0; }
 
+// Tiles of `count` keys from `key` on against the keys [from, to), none of the three below 0.  A length may be up
+// to 2^31 - 16, so the end of its last tile only fits 32 bits without a sign.
+MOE_HD bool tile_inside(int key, int count, int from, int to) {
+    return key >= from && (uint32_t)key + count <= (uint32_t)to;
+}
+MOE_HD bool tile_meets(int key, int count, int from, int to) {
+    return key < to && (uint32_t)key + count > (uint32_t)from;
+}
+// Tiles of 2^log2 keys that hold the keys [0, to), to >= 0.
+MOE_HD int tiles_until(int to, int log2) { return (int)(((uint32_t)to + (1u << log2) - 1) >> log2); }
+
 }  // namespace moe

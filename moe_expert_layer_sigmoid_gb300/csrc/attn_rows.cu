@@ -209,7 +209,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             const int hk = u.hs / p.c.subs;
             const int32_t* row = p.a.pages + (int64_t)u.b * p.a.d.max_pages;
             const int pg0 = u.key0 >> p.c.page_log2;
-            const int pg1 = (int)(((int64_t)u.key1 + page - 1) >> p.c.page_log2);  // pages [pg0, pg1) are seen
+            const int pg1 = tiles_until(u.key1, p.c.page_log2);  // pages [pg0, pg1) are seen
             auto fetch = [&](int at) {
                 const int i = at + lane;
                 return i >= pg0 && i < pg1 ? __ldg(row + i) : 0;
@@ -393,7 +393,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
         }
         // keys that every row of the unit sees need no mask
         const int inner0 = first_key(u.len - u.n + min(u.n, u.rt * p.c.tq + p.c.tq) - 1, p.a.d.window);
-        const int inner1 = u.len - u.n + u.rt * p.c.tq + 1;  // [inner0, inner1)
+        const int inner1 = max(0, u.len - u.n + u.rt * p.c.tq + 1);  // [inner0, inner1)
 
         for (; tile < end; ++tile, ++it) {
             const int s = it % S::kStages;
@@ -403,7 +403,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
             if (ok) ok = mbar_wait(full(s), (it / S::kStages) & 1, abort_flag, hdr);
             const int kw0 = warp * 16 * kKm;                       // the warp's first key in the tile
             const int key = (u.tile0 + tile) * S::kTk + kw0;
-            if (key < u.key1 && key + 16 * kKm > u.key0) {
+            if (tile_meets(key, 16 * kKm, u.key0, u.key1)) {
                 const uint32_t kt = sbase + s * 2 * S::kTileB, vt = kt + S::kTileB;
                 float sv[kKm][R8][4];
 #pragma unroll
@@ -449,8 +449,8 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                     }
                 // to the exponent's domain: scale * log2(e), the keys' scales, the masks
                 const float* ks = reinterpret_cast<const float*>(smem + S::kOffSc + s * 2 * S::kScB) + kw0 + g;
-                const bool inner = key >= inner0 && key + 16 * kKm <= inner1;
-                const bool edge = key < u.key0 || key + 16 * kKm > u.key1;
+                const bool inner = tile_inside(key, 16 * kKm, inner0, inner1);
+                const bool edge = !tile_inside(key, 16 * kKm, u.key0, u.key1);
                 float mx[R8][2], vw[kKm][2];
 #pragma unroll
                 for (int n = 0; n < R8; ++n) mx[n][0] = mx[n][1] = kNoMax;

@@ -177,7 +177,7 @@ __device__ __forceinline__ Stretch stretch(const AttnParams& p, const Share& sh,
         const int k1 = max(0, u.len - u.n + b);
         const int k0 = first_key(u.len - u.n + a, p.a.d.window);
         s.lo[x] = max(s.t0, k0 / kTk - u.tile0);
-        s.hi[x] = k1 > k0 ? min(s.t1, (k1 + kTk - 1) / kTk - u.tile0) : s.lo[x];
+        s.hi[x] = k1 > k0 ? min(s.t1, tiles_until(k1, 7) - u.tile0) : s.lo[x];
     }
     return s;
 }
@@ -276,7 +276,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
                 const int32_t* row = p.a.pages + (int64_t)u.b * p.a.d.max_pages;
                 const int pg0 = u.key0 >> p.c.page_log2;
-                const int pg1 = (int)(((int64_t)u.key1 + page - 1) >> p.c.page_log2);
+                const int pg1 = tiles_until(u.key1, p.c.page_log2);
                 auto fetch = [&](int at) {
                     const int i = at + lane;
                     return i >= pg0 && i < pg1 ? __ldg(row + i) : 0;
@@ -497,22 +497,23 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             float m = kNoMax, l = 0.0f;
             // keys that all of the stream's rows see need no mask
             const int i0 = u.rt * p.c.tq + (s.split ? 0 : x * half);
-            const int inner1 = u.len - u.n + i0 + 1;
+            const int inner1 = max(0, u.len - u.n + i0 + 1);
             const int inner0 = first_key(u.len - u.n + min(u.n, i0 + half) - 1, p.a.d.window);
             // the stream's tiles: i0 .. (every other one with one row tile)
             const int step = s.split ? 2 : 1;
             const int beg = s.split ? s.t0 + x : x ? s.lo[1] : s.lo[0], end = x ? s.hi[1] : s.hi[0];
-            int key = (u.tile0 + beg) * kTk;
+            uint32_t from = (uint32_t)(u.tile0 + beg) * kTk;  // the tile's first key (past the last tile it may be 2^31)
             uint32_t vk = 2 * (tiles0 + (uint32_t)(beg - s.t0)) + 1;  // the value tile's slot index
             // keys outside [key0, key1) are nobody's: their slots may hold anything.  bf16 values are cleared
             // there, not just weighted with 0, by the first stream that takes the tile: by B where A has none.
             const int key0 = u.key0, key1 = u.key1;
-            const int clear0 = s.split || x == 0 ? 0 : (u.tile0 + s.hi[0]) * kTk;
+            const int clear0 = s.split || x == 0 ? 0 : s.hi[0];
 #pragma unroll 1
-            for (int i = beg; i < end; i += step, key += step * kTk, vk += 2 * step) {
+            for (int i = beg; i < end; i += step, from += step * kTk, vk += 2 * step) {
+                const int key = (int)from;
                 wait(S::kBarSf + x, n_sf++);
                 tc_fence_after();
-                if (!S::kQuant && (key < key0 || key + kTk > key1) && (key >= clear0 || (x == 1 && i < s.lo[0]))) {
+                if (!S::kQuant && !tile_inside(key, kTk, key0, key1) && (i >= clear0 || (x == 1 && i < s.lo[0]))) {
                     wait(S::kBarFull + vk % kSlots, vk / kSlots);
                     if (key + r < key0 || key + r >= key1) {
                         uint8_t* z = smem + S::kOffKv + (vk % kSlots) * S::kTileB + r * 128;
@@ -522,7 +523,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                     }
                     fence_async();
                 }
-                const bool inner = key >= inner0 && key + kTk <= inner1;
+                const bool inner = tile_inside(key, kTk, inner0, inner1);
                 // quantised: the half's key scales (times the call's; in place since before the products
                 // that S comes from), then its value scales
                 const uint32_t ksc = sbase + S::kOffSc + ((vk / 2) % S::kScSlots) * S::kScB + 256 * hf;

@@ -34,3 +34,26 @@ def test_windows_with_tokens_before_the_start(fmt, window, G):
     new = [10, 3, 1, 200, 40, 1]
     total = [5, 1, 0, 100, 17, 300]
     ok(ac.make(new, total, 2 * G, 2, 128, 16, fmt, window=window, seed=G))
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("new", [1, 3, 100, 250])
+@pytest.mark.parametrize("page,left", [(64, 0), (64, 10), (16, 0), (16, 7)])
+def test_the_longest_length(fmt, new, page, left):
+    """Sequences that end within a tile of 2^31 keys, seen through a window; behind the last key of the page
+    lies what must never matter."""
+    far = 2 ** 31 - page          # keys of the longest page table
+    total = far - left
+    window, near = 300, 2048      # keys the window can reach, in whole pages
+    b = ac.make([new], [near - left], 8, 2, 64, page, fmt, window=window, seed=new)
+    # the same pages at the end of a page table of 2^31 keys: positions are 2^31 less a constant
+    pages = torch.full((1, far // page), 0x7FFFFFF0, dtype=torch.int32, device="cuda")
+    pages[0, -(near // page):] = b.pages[0, :near // page]
+    ref = ac.reference(b)
+    dims = b.dims(moe, max_pages=far // page)
+    b.pages = pages
+    b.kv_len.fill_(total)
+    out, lse, ws = run(b, dims=dims)
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK
+    assert ((out.double() - ref[0]).abs() <= ref[2]).all()
+    assert ((lse.double() - ref[1]).abs() <= ref[3]).all()

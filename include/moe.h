@@ -567,7 +567,7 @@ size_t moe_attn_workspace_bytes(const moe_kv_dims_t* dims);
  *   pages   (device) int32 [B][max_pages]: key j of sequence b is slot j % page
  *           of page pages[b][j / page].  Only the entries of pages that hold a
  *           key some token sees are read.
- *   scale   factor of the scores, finite
+ *   scale   factor of the scores, of any sign; scale * log2(e) is finite in fp32
  *   out     (device) out: bf16 [T][H][D], contiguous, 16-byte aligned
  *   lse     (device) out, nullable: fp32 [T][H]
  *   ws      workspace of moe_attn_workspace_bytes(dims), zero-filled before its

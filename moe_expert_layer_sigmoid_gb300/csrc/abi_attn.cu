@@ -3,7 +3,7 @@
 // stream; nothing here allocates or synchronises.
 #include <cmath>
 
-#include "kv.cuh"
+#include "attn.cuh"
 
 using namespace moe;
 
@@ -90,7 +90,7 @@ moe_status_t moe_attn_paged(const uint16_t* q, int64_t ldq, const int32_t* q_off
     if ((st = check_ws(ws, ws_bytes, moe_attn_workspace_bytes(dims))) != MOE_OK) return st;
     if (dims->T == 0) return MOE_OK;
     if (dims->B == 0 || !rows_ok(q, ldq, dims->T, (int64_t)dims->H * dims->D) || !q_off ||
-        !kv_len || !pages || !kv_ok(cache, *dims) || !std::isfinite(scale) || !act_ok(out) ||
+        !kv_len || !pages || !kv_ok(cache, *dims) || !std::isfinite(scale * kLog2e) || !act_ok(out) ||
         reinterpret_cast<uintptr_t>(lse) % 4)
         return MOE_ERR_INVALID_ARG;
     const AttnArgs a{q,      ldq,   q_off, kv_len, pages, *dims,

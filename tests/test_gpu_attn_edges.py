@@ -1,4 +1,6 @@
 """Attention over the paged cache at the edges of what a call may hold."""
+import dataclasses
+
 import pytest
 import torch
 
@@ -57,3 +59,39 @@ def test_the_longest_length(fmt, new, page, left):
     assert moe.moe_check_device_status(ws) == moe.MOE_OK
     assert ((out.double() - ref[0]).abs() <= ref[2]).all()
     assert ((lse.double() - ref[1]).abs() <= ref[3]).all()
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("scale", [-0.3125, 0.0, -0.0, 1.0, -1.0, 2.0 ** -12, 2.0 ** -140])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("D", [64, 128])
+def test_factors_of_the_scores(fmt, scale, window, D):
+    """Any factor: a negative one turns the order of the scores, zero makes plain means; few rows and chunks,
+    tokens before the start, a window, masks at every edge."""
+    b = ac.make([1, 4, 90, 1, 20, 150], [300, 77, 200, 1, 9, 150], 8, 2, D, 16, fmt, window=window, seed=D)
+    out, lse, ws = run(dataclasses.replace(b, scale=scale))
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK
+    # the same scores from the other sign of the queries, so that the bounds' magnitudes stay positive
+    ac.check(dataclasses.replace(b, scale=abs(scale), q=-b.q if scale < 0 else b.q), out, lse)
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+def test_two_streams_at_once(fmt):
+    """Calls at work at the same time on two streams, a workspace each, give what they give alone."""
+    bs = [ac.make([1, 200, 3, 1], [3000, 900, 700, 50], 8, 2, 128, 16, fmt, seed=1),
+          ac.make([150, 1, 1, 20], [400, 5000, 33, 20], 16, 2, 64, 32, fmt, seed=2)]
+    alone = [run(b)[:2] for b in bs]
+    wss = [moe.workspace(moe.moe_attn_workspace_bytes(b.dims(moe))) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    got = [[] for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, b in enumerate(bs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(b, wss[i])[:2])
+    torch.cuda.synchronize()
+    for i, b in enumerate(bs):
+        assert moe.moe_check_device_status(wss[i]) == moe.MOE_OK
+        for out, lse in got[i]:
+            assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+        ac.check(b, *alone[i])

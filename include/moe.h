@@ -575,8 +575,14 @@ size_t moe_attn_workspace_bytes(const moe_kv_dims_t* dims);
  *           smaller dims
  * Numerics: products and sums in fp32; a weight e^(s_j - m) (times the value
  * row's scale) is rounded to bf16 before it meets the value codes, its
- * unrounded value enters the denominator.  Keys and values that some token sees
- * must be finite; what lies in slots that no token sees never matters.
+ * unrounded value enters the denominator.  Where few rows read a coded cache (as
+ * max_new, T and B tell; a chunk's queries stay bf16), a query is held in f16,
+ * scaled by the power of two that suits its largest element: each element is off
+ * by at most 2^-39 of the largest with E4M3 and 2^-35 with int4, and exact from
+ * 2^-31 (2^-27) of it up.  Their int4 scores are sums of q (n + 8) less 8 sum q, so
+ * what fp32 rounds there goes by |q| (|n| + 16) instead of |q n|.
+ * Keys and values that some token sees must be finite; what lies in slots that no
+ * token sees never matters.
  * Device checks (moe_check_device_status): a sequence with q_off descending or
  * past T, or kv_len outside [0, max_pages * page], is left out; a page id
  * outside the pool is read as page 0. */

@@ -19,9 +19,13 @@
 // any order, so the k index (and for values the order of the output columns) is
 // permuted to whatever the unpacking leaves:
 //   E4M3 keys: f16 by the conversion of two codes; the query row is scaled by the power of two
-//     that puts its largest element at 2^14, where f16 holds every bf16 down to 2^-28 of it.
+//     that puts its largest element into [2^14, 2^15), where f16 holds every bf16 from 2^-31 of it up and
+//     is off by 2^-39 of it at most below (its last bit is 2^-24).
 //   int4 keys: the nibble n + 8 alone is the f16 subnormal (n + 8) 2^-24 (2^-20 four bits up):
-//     one mask each, the queries take the other scale and the accumulators start at -8 sum q.
+//     one mask each, the queries take the other scale and the accumulators start at -8 sum q.  Half of the
+//     query's elements are held at 2^-4 of the others, so the two limits are 2^-27 and 2^-35; and the sums
+//     round by |q| (|n| + 16) instead of |q n|, which bf16 weights hide (their rounding is 2^-8) unless one
+//     element outweighs the others by a thousand and meets codes of 0.
 //   E4M3 values: the two codes of a column pair side by side, then by way of f16 and fp32 to bf16, exact at
 //     every step (moving the bits takes fewer instructions, but all on one pipe).
 //   int4 values: 128 + (n + 8) by its bits, less 136.

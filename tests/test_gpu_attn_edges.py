@@ -95,3 +95,36 @@ def test_two_streams_at_once(fmt):
         for out, lse in got[i]:
             assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
         ac.check(b, *alone[i])
+
+
+@pytest.mark.parametrize("fmt,tier", [("bf16", 10), ("bf16", 30), ("e4m3", 10), ("e4m3", 20), ("e4m3", 30),
+                                      ("int4", 4), ("int4", 10)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_queries_of_a_wide_range(fmt, tier, D):
+    """One element of each query is 2^tier times the others and meets keys of 0, so the others make the scores:
+    few rows of a coded cache hold them in f16, scaled to the largest, and sum shifted int4 codes."""
+    b = ac.make([1, 2, 1, 40], [300, 77, 9, 90], 8, 2, D, 16, fmt, seed=D + tier)
+    c = 6
+    if fmt == "int4":
+        b.k[..., c // 2] &= 0xF0
+    else:
+        b.k[..., c] = 0
+    q = torch.randn(b.q.shape, generator=torch.Generator().manual_seed(tier)) * 2.0 ** -tier
+    q[..., c] = 1.0
+    b = dataclasses.replace(b, q=q.to(torch.bfloat16).cuda(), scale=2.0 ** (tier - 3))
+    out, lse, ws = run(b)
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK
+    ref, z, bo, bl = ac.reference(b)
+    # What the header states on top of the reference's bound: an element off by 2^-39 (int4: 2^-35) of the
+    # largest, here 1, and int4 sums that round by |q| (|n| + 16) instead of |q n|.  `e` is the change of a score; a
+    # weight moves by its own and the largest one's, numerator and denominator alike.
+    k, v = (ac.values(x, None if s is None else s.nan_to_num(0.0), fmt).nan_to_num(0.0)
+            for x, s in ((b.k, b.ks), (b.v, b.vs)))
+    e = 0.0
+    if fmt != "bf16":
+        e = 2.0 ** (-39 if fmt == "e4m3" else -35) * k.abs().sum(-1).max().item() * b.scale
+    if fmt == "int4":
+        e += D * 2.0 ** -23 * 16 * b.ks.nan_to_num(0.0).max().item() * q.abs().sum(-1).max().item() * b.scale
+    assert e < 0.1
+    assert ((out.double() - ref).abs() <= bo + 4 * e * v.abs().max()).all()
+    assert ((lse.double() - z).abs() <= bl + 2 * e).all()

@@ -571,8 +571,11 @@ size_t moe_attn_workspace_bytes(const moe_kv_dims_t* dims);
  *   out     (device) out: bf16 [T][H][D], contiguous, 16-byte aligned
  *   lse     (device) out, nullable: fp32 [T][H]
  *   ws      workspace of moe_attn_workspace_bytes(dims), zero-filled before its
- *           first use; every call leaves it ready for the next, on these or
- *           smaller dims
+ *           first use; every call of moe_attn_paged, moe_kv_write and
+ *           moe_kv_read leaves it ready for their next, on these or smaller dims.
+ *           Not one that the layer's calls use: they keep intermediates
+ *           where this call counts the parts of a result, and outputs would be
+ *           left out.  (Filled with zeros again it serves.)
  * Numerics: products and sums in fp32; a weight e^(s_j - m) (times the value
  * row's scale) is rounded to bf16 before it meets the value codes, its
  * unrounded value enters the denominator.  Where few rows read a coded cache (as

@@ -529,7 +529,7 @@ def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, p
                    lse: torch.Tensor | None, ws, stream=None):
     """Attention of the new tokens q bf16 [T][H][D] (tokens may lie apart) over the cache, which
     holds their keys and values: out bf16 [T][H][D], lse fp32 [T][H] or None.  q_off int32
-    [B+1], kv_len int32 [B], pages int32 [B][max_pages]; see include/moe.h."""
+    [B+1], kv_len int32 [B], pages int32 [B][max_pages]; ws is not the layer's.  See include/moe.h."""
     T, B, H, D = dims.T, dims.B, dims.H, dims.D
     _kv_check(dims, cache, dims.H_kv, D)
     qp, ldq = _rows(q, T, H, D, "q")

@@ -73,6 +73,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The bounded wait of a whole warp whose lanes exchange values afterwards: they go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, hdr));
+}
+
 // Teardown wait for this thread's own asynchronous work (copies or MMAs it
 // issued) after an abort: ignores the abort flag, still bounded by the limit.
 __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, WsHeader* hdr) {

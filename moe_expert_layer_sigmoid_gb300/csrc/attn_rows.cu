@@ -234,7 +234,7 @@ attn_rows_kernel(const __grid_constant__ AttnParams p) {
                 const bool live = lane < boxes && pg + lane >= pg0 && pg + lane < pg1 &&
                                   key + lane * box_rows < u.key1;
                 const uint32_t n_live = __popc(__ballot_sync(0xFFFFFFFFu, live));
-                if (!mbar_wait(empty(s), ((it / S::kStages) & 1) ^ 1, abort_flag, hdr)) {
+                if (!warp_wait(empty(s), ((it / S::kStages) & 1) ^ 1, abort_flag, hdr)) {
                     ok = false;
                     break;
                 }

@@ -259,7 +259,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                 const int hk = u.hs;
                 // the queries, {64 columns, heads, tokens} boxes: row r of a stream is token r / heads,
                 // head r % heads.  Rows of other sequences' tokens may come along: rows do not mix.
-                if (!mbar_wait(bar(S::kBarQe), (n_q & 1) ^ 1, abort_flag, hdr)) {
+                if (!warp_wait(bar(S::kBarQe), (n_q & 1) ^ 1, abort_flag, hdr)) {
                     ok = false;
                     break;
                 }
@@ -303,7 +303,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                         const int s = it % kRing;  // (its wait takes one phase after the other)
-                        if (!mbar_wait(bar((S::kQuant ? S::kBarRawE : S::kBarEmpty) + s),
+                        if (!warp_wait(bar((S::kQuant ? S::kBarRawE : S::kBarEmpty) + s),
                                        S::kQuant ? Ring::free_parity(it) : ((it / kSlots) & 1) ^ 1, abort_flag, hdr)) {
                             ok = false;
                             break;
@@ -343,7 +343,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
             bool ok = true;
             bool fresh[2];       // no product in the stream's O yet
             auto wait = [&](int b, uint32_t par) {
-                if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), par & 1, abort_flag, hdr));
+                if (ok) ok = warp_wait(bar(b), par & 1, abort_flag, hdr);
                 tc_fence_after();
                 return ok;
             };

@@ -8,8 +8,8 @@ namespace {
 // Sequences of at most this many rows (new tokens x query heads per key/value
 // head) run on the warp-level kernel, longer ones on the tcgen05 kernel: that one's
 // tiles have 128 rows, full or not, the other reads the keys from L2 and turns their
-// codes into operands again for every 16.  Measured, whole calls of D = 128 and up to 8 thousand keys, 8
-// key/value heads, in us (warp-level / tcgen05):
+// codes into operands again for every 16.  Measured, whole calls of D = 128 and up to 8
+// thousand keys, 8 key/value heads, in us (warp-level / tcgen05):
 //                        32 rows       48 rows       64 rows       80 rows
 //   16 sequences, bf16   64.1 / 62.3   77.7 / 62.8  114.4 / 62.8  131.2 / 62.8
 //                 E4M3   53.6 / 84.5   80.1 / 84.2  100.3 / 84.8
@@ -20,8 +20,10 @@ namespace {
 //                E4M3                                47.3 / 48.4
 //   2 sequences, bf16    29.1 / 38.5   31.1 / 38.7
 //                E4M3                                35.2 / 44.0
-// (D = 64, 16 sequences: bf16 41.3 / 47.6 at 32, 52.4 / 47.9 at 48; E4M3 50.1 / 59.1 at 48, 63.7 / 60.0 at
-// 64.)  A call of few sequences and heads leaves SMs to the extra units.
+// (D = 64, 16 sequences: bf16 41.3 / 47.6 at 32, 52.4 / 47.9 at 48; E4M3 50.1 / 59.1 at 48,
+// 63.7 / 60.0 at 64.)  A call of few sequences and heads leaves SMs to the extra units.
+// bf16 rows of 32 stay on the warp-level kernel for D = 64, where it gains 13%, and lose 3%
+// with D = 128.
 int64_t few_rows(const moe_kv_dims_t& d) {
     if (4 * (int64_t)d.B * d.H_kv <= sm_count()) return 64;
     return d.format == kKvBf16 ? 32 : 48;

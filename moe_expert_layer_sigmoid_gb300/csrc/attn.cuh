@@ -125,7 +125,8 @@ __device__ __forceinline__ T cta_scan(T x, T* sm, T& total) {
 // finds the unit that holds this CTA's first place.  Everything a CTA does waits for it, and its code
 // is cold when it runs, so the common cases (a sequence per thread at most, a line that 32 bits hold,
 // and few row tiles per sequence or no more in all than threads) are kept short; deal_many is for
-// the others (a 2048-token chunk waited 12,300 cycles for it).
+// the others (a 2048-token chunk waited 12,300 cycles for it; 160 decode sequences of 1638 E4M3 keys
+// take 102.6 us, 161 of 1628 take 107.4).
 constexpr int deal_bytes(int threads) { return 8 * (2 * (threads / 32) + 8) + 16 * threads; }
 
 // The share of the line and its first unit, from the found one's first place of its row tile.

@@ -35,10 +35,11 @@
 // most tiles need neither the shuffles nor the rescaling of the output.  Weights stay below 2^8
 // and the sums are fp32, so nothing is lost.
 //
-// Measured (GB300, whole call): 200 thousand E4M3 keys in three sequences, 4 key/value heads of 128, 77 us, 5.3 TB/s,
-// 78% of a copy's bandwidth (issue slots 47%, ALU 46%).  128 sequences of up to 8190 int4 keys, D = 64,
+// Measured (GB300, whole call): 191 thousand E4M3 keys in three sequences, 8 key/value heads of 128, 77 us, 5.3 TB/s,
+// 78% of a copy's bandwidth (issue slots 46%, ALU 46%).  128 sequences of up to 8190 int4 keys, D = 64,
 // 36 us: issue-bound (54%, ALU 49%).  29 sequences of 71 to 4009 bf16 keys 31 us, 3.9 TB/s: latency of
-// dealing, first loads and joins (issue 22%).
+// dealing, first loads and joins (issue 22%).  The forms of 16 rows and D = 128 spill (E4M3 64 bytes stored and
+// 96 loaded, int4 124 and 144, bf16 12 and 12 at 168 registers), the others do not.
 #include "attn.cuh"
 
 namespace moe {

@@ -14,8 +14,9 @@
 //   - even and odd key tiles of one row tile, joined at the end, when it has not.
 //
 // TMEM (512 columns): S of A and B at 0 and 128, O at 256 and 384.  P (bf16, two
-// keys per column) overwrites S, each half of the keys its own half's first columns; the next S of a stream is issued after the
-// P V that reads P, and the tensor core runs one thread's products in order.
+// keys per column) overwrites S, each half of the keys its own half's first columns; the
+// next S of a stream is issued after the P V that reads P, and the tensor core runs one
+// thread's products in order.
 //
 // Two threads own a row, each half of a tile's keys, no shuffles.  A tile takes one pass over S, with the
 // running maximum as it stands; a barrier with a vote tells whether some score exceeds it by 2^8, and in
@@ -33,9 +34,11 @@
 // four warps for the first 64 keys of a tile and four for the last), 20-23 conversion
 // of keys, 24-27 of values.
 //
-// Measured (GB300, 2048 tokens, D = 128): behind 27,953 keys 764 us in bf16, 1273 TFLOP/s, 65% of a library
-// product's rate; 1027 us in E4M3, 947 TFLOP/s, where the conversion's warps take issue slots (54% used
-// against 39%) from the softmax.  With no keys before it 57 us: fill, 14 pairs of key tiles per CTA.
+// Measured (GB300, 2048 tokens, D = 128): behind 27,953 keys 746 us in bf16, 1303 TFLOP/s, 67% of a library
+// product's rate; 1020 us in E4M3, 953 TFLOP/s, and 986 in int4, where the conversion's warps take issue slots
+// (53% used against 40%) from the softmax.  With no keys before it 57 us: 14 pairs of key tiles per CTA, which
+// the long chunk walks in half of that, so the rest is what a CTA does before and after its walk.  All forms
+// spill in the softmax's loop (coded caches 328 bytes stored and 448 loaded at 72 registers, bf16 80 and 124 at 96).
 #include <atomic>
 #include <type_traits>
 

@@ -9,9 +9,11 @@
 // keys and of the values, so what is done once per row is spread over 32 values, and
 // three (D = 128) or two exchanges make the absolute maxima of both.
 //
-// Measured (GB300, 65537 tokens of 8 heads of 128, written and read back): bf16 163 us, 6.6 TB/s, 97% of a
-// copy's bandwidth; E4M3 138 us, 5.9 TB/s (the read 6.5 TB/s, the write 5.3, 46% ALU, 57% of issue slots);
-// int4 133 us, 5.1 TB/s, by the arithmetic of its codes.
+// Measured (GB300, 65537 tokens of 8 heads of 128, us and TB/s; a copy's bandwidth is 6.8):
+//   bf16 write 81.7, 6.6    read 82.0, 6.5
+//   E4M3 write 73.4, 5.5    read 66.8, 6.1
+//   int4 write 71.8, 4.7    read 61.8, 5.5
+// The writes of codes are held up by their arithmetic (E4M3 46% ALU, 57% of issue slots).
 #include <cuda_fp8.h>
 
 #include "kv.cuh"

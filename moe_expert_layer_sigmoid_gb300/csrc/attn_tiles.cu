@@ -19,8 +19,9 @@
 // thread's products in order.
 //
 // Two threads own a row, each half of a tile's keys, no shuffles.  A tile takes one pass over S, with the
-// running maximum as it stands; a barrier with a vote tells whether some score exceeds it by 2^8, and in
-// those few tiles (S is still whole: P is stored after the vote) the halves exchange their maxima, O is
+// running maximum as it stands; a barrier with a vote tells whether some score exceeds it by 2^8 (rows that
+// no token fills have no vote: their queries are whatever lies in shared memory, and the others' maxima, so their
+// rounding, would depend on it), and in those few tiles (S is still whole: P is stored after the vote) the halves exchange their maxima, O is
 // rescaled (read, scaled and written back in TMEM) and the pass done again.  When S of tile i is ready,
 // P V of tile i - 1 is too, so O may be touched without a further wait.  The loop's issue slots and
 // registers are what the tensor core waits for most, so S is read 32 columns at a time and the
@@ -631,7 +632,7 @@ attn_tiles_kernel(const __grid_constant__ AttnParams p) {
                         "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 256, p;\n"
                         " selp.b32 %0, 1, 0, q;\n}"
                         : "=r"(raise)
-                        : "r"((int)(fmaxf(t0, t1) > 8.0f)), "r"(2 + x)
+                        : "r"((int)(pos >= 0 && fmaxf(t0, t1) > 8.0f)), "r"(2 + x)
                         : "memory");
                     if (!raise) break;
                 }

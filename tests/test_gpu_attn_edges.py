@@ -128,3 +128,21 @@ def test_queries_of_a_wide_range(fmt, tier, D):
     assert e < 0.1
     assert ((out.double() - ref).abs() <= bo + 4 * e * v.abs().max()).all()
     assert ((lse.double() - z).abs() <= bl + 2 * e).all()
+
+
+@pytest.mark.parametrize("fmt", ac.FORMATS)
+@pytest.mark.parametrize("G", [3, 5, 7, 24, 33, 100])
+@pytest.mark.parametrize("D", [64, 128])
+def test_same_bits_whatever_ran_before(fmt, G, D):
+    """Groups that leave rows of a tile without a token: what other calls left in shared memory does not
+    tell in the last bit."""
+    b = ac.make([60, 1, 90], [700, 300, 1500], 2 * G, 2, D, 16, fmt, window=1000, seed=G)
+    other = ac.make([300], [300], 16, 2, D, 16, fmt, seed=1)
+    first, ws = None, moe.workspace(moe.moe_attn_workspace_bytes(b.dims(moe)))
+    for factor in (1.0, 1e-3, 30.0, 1e4, -1e6, float("nan"), 0.0):
+        run(dataclasses.replace(other, q=other.q * factor))
+        out, lse, _ = run(b, ws)
+        if first is None:
+            first = out, lse
+            ac.check(b, out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), factor

@@ -35,11 +35,12 @@
 // four warps for the first 64 keys of a tile and four for the last), 20-23 conversion
 // of keys, 24-27 of values.
 //
-// Measured (GB300, 2048 tokens, D = 128): behind 27,953 keys 746 us in bf16, 1303 TFLOP/s, 67% of a library
-// product's rate; 1020 us in E4M3, 953 TFLOP/s, and 986 in int4, where the conversion's warps take issue slots
-// (53% used against 40%) from the softmax.  With no keys before it 57 us: 14 pairs of key tiles per CTA, which
-// the long chunk walks in half of that, so the rest is what a CTA does before and after its walk.  All forms
-// spill in the softmax's loop (coded caches 328 bytes stored and 448 loaded at 72 registers, bf16 80 and 124 at 96).
+// Measured (GB300, 2048 tokens, D = 128): behind 27,953 keys 730 to 754 us in bf16 (by clocks), 1290 to
+// 1334 TFLOP/s, 66 to 68% of a library product's rate; 1020 us in E4M3, 953 TFLOP/s, and 986 in int4, where the
+// conversion's warps take issue slots (53% used against 40%) from the softmax.  With no keys before it
+// 57 us: 14 pairs of key tiles per CTA, which the long chunk walks in half of that, so the rest is what a
+// CTA does before and after its walk.  All forms spill in the softmax's loop (coded caches 328 bytes stored and
+// 448 loaded at 72 registers, bf16 80 and 124 at 96).
 #include <atomic>
 #include <type_traits>
 

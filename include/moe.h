@@ -1,6 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe.so, the GB300 (sm_103a) routed MoE FFN layer, and
- * of the paged key/value cache and attention next to it (at the end).
+ * of what stands next to it in a decoder block (at the end): the paged
+ * key/value cache and attention, page planning, rotary positions, the norms
+ * between blocks, and projections in 4-bit floats.
  *
  * The layer (thewafflehaus/butter PR #69, commit "feat(laguna): Laguna-S-2.1
  * decode on the CUDA engine"): a sigmoid top-k router with a score-correction
@@ -593,6 +595,254 @@ moe_status_t moe_attn_paged(const uint16_t* q, int64_t ldq, const int32_t* q_off
                             const int32_t* kv_len, const int32_t* pages,
                             const moe_kv_dims_t* dims, const moe_kv_t* cache, float scale,
                             uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ============================================================================
+ * Page planning: block tables and slot maps from request lengths, on the
+ * device, so that a captured step follows its lengths.  The program keeps one
+ * state per pool of pages:
+ *   kv_len      int32 [B]             tokens of each sequence
+ *   first       int32 [B]             index of the first page a sequence still holds
+ *                                     (0 without a window)
+ *   pages       int32 [B][max_pages]  page ids; -1 where none is held
+ *   free_pages  int32 [n_pages]       a stack of ids, the first n_free of them free
+ *   n_free      int32 [1]
+ * all (device).  A new state has kv_len, first 0, pages -1, free_pages any order
+ * of 0 .. n_pages - 1 and n_free = n_pages.
+ * ========================================================================= */
+typedef struct {
+    int32_t* kv_len;
+    int32_t* first;
+    int32_t* pages;
+    int32_t* free_pages;
+    int32_t* n_free;
+} moe_kv_pages_t;
+
+/* moe_kv_plan -- one step of a batch: sequence b gets new_len[b] more tokens, or
+ * loses -new_len[b] of its last ones where that is negative (rejected drafts; at
+ * least kv_len[b] of them end the sequence).  In this order:
+ *  1. Pages go back to the stack: those past the last token left of a shortened
+ *     sequence (all of an ended one, whose kv_len and first become 0); with
+ *     dims.window > 0 those of the others in which no token from position
+ *     kv_len[b] on sees a key any more.  They are listed by sequence, then by
+ *     index, and the stack gets the last of the list first, so dropping the
+ *     tokens that the call before added restores the stack.  Their entries
+ *     become -1.
+ *  2. New pages come off the top of the stack, by sequence, then by index.  A
+ *     sequence that grows is served if the tokens asked for by it and all before
+ *     it are at most dims.T and, where it needs a page, the pages asked for by
+ *     it and all before it are free; if not it keeps its length, and the device
+ *     check flag is set.
+ *  3. The maps of the step's tokens: q_off int32 [B+1] is the exclusive sum of
+ *     the tokens served; token i of sequence b is row t = q_off[b] + i with
+ *     pos[t] = its position (the length before the call, plus i) and slots[t] its slot,
+ *     pages[b][pos / page] * page + pos % page.  Rows from q_off[B] on get -1 in
+ *     both.  pos and slots: int32 [T].
+ * Then kv_len, q_off and pages serve moe_attn_paged, pos and slots
+ * moe_rope_kv_write or moe_kv_write, whose dims.T may be this call's.
+ *   new_len  (device) int32 [B]
+ *   dims     T (rows of pos and slots), B, page, n_pages, max_pages and window
+ *            are used, the others only checked
+ *   ws       a workspace of at least 256 bytes, zero-filled before its first use
+ * T = 0 and B = 0 are carried out too (pos and slots may be NULL for T = 0; what
+ * has B elements for B = 0).  The outputs and the state do not overlap.  One
+ * call at a time works on a state.
+ * Device checks: kv_len outside [0, max_pages * page], first outside its pages,
+ * a sequence that would pass max_pages * page, and one shortened into pages that
+ * the window has given back are left as they are; n_free outside [0, n_pages] is
+ * brought to it; ids that the stack has no room for are dropped; a token whose page id is
+ * outside the pool gets the slot -1. */
+moe_status_t moe_kv_plan(const int32_t* new_len, const moe_kv_dims_t* dims, const moe_kv_pages_t* st,
+                         int32_t* q_off, int32_t* pos, int32_t* slots, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* ============================================================================
+ * Rotary positions.  The first `rot` elements of a head are rot / 2 pairs; at
+ * position p pair i is turned by the angle p * f_i:
+ *   y1 = x1 c - x2 s,   y2 = x2 c + x1 s,   c = m cos(p f_i), s = m sin(p f_i),
+ * each product and sum rounded in fp32.  Pair i is elements i and i + rot / 2, or
+ * 2i and 2i + 1 (MOE_ROPE_PAIRS).  The other elements stay.  Rotary scaling for
+ * long contexts follows the attention side of thewafflehaus/butter PR #69 (its
+ * rope over scaled frequencies, and its RMS norm of each query and key head
+ * before).
+ * ========================================================================= */
+typedef enum {
+    MOE_ROPE_NONE = 0,   /* f_i = base^(-2i / rot)                                    */
+    MOE_ROPE_LINEAR = 1, /* f_i / factor                                              */
+    MOE_ROPE_RAMP = 2,   /* (1 - g) f_i + g f_i / factor, g = clamp((i - a) / (b - a), 0, 1):
+                            a = max(floor(e(hi)), 0), b = min(ceil(e(lo)), rot - 1), b - a at
+                            least 0.001, e(t) = rot ln(orig_len / (2 pi t)) / (2 ln base) the
+                            pair that turns t times in orig_len positions             */
+    MOE_ROPE_BAND = 3    /* the same with g = 1 - clamp((t_i - lo) / (hi - lo), 0, 1),
+                            t_i = orig_len f_i / (2 pi) the pair's turns              */
+} moe_rope_scaling_t;
+
+typedef struct {
+    double base;      /* above 1                                              */
+    double factor;    /* >= 1 (LINEAR, RAMP, BAND)                            */
+    double orig_len;  /* > 0 (RAMP, BAND)                                     */
+    double lo, hi;    /* turns, 0 < lo < hi (RAMP, BAND)                      */
+    double magnitude; /* m, above 0 and finite in fp32                        */
+    int32_t rot;      /* elements turned: a multiple of 16, at most 256       */
+    int32_t scaling;  /* moe_rope_scaling_t                                   */
+} moe_rope_config_t;
+
+/* moe_rope_table -- the table that the calls below read: row r, of rot fp32, holds
+ * the rot / 2 values c and then the rot / 2 values s of position pos0 + r.  The
+ * angle is reduced in fixed point: c and s are within 2^-22 m of the exact values for
+ * positions up to 2^24 (above, the frequency's 53 bits count).
+ *   table (device) out: fp32 [n_pos][rot], 16-byte aligned
+ *   pos0, n_pos  >= 0, pos0 + n_pos <= 2^31, n_pos * rot < 2^40
+ */
+moe_status_t moe_rope_table(const moe_rope_config_t* config, int32_t pos0, int32_t n_pos, float* table,
+                            void* stream);
+
+#define MOE_ROPE_PAIRS 0x1u   /* a pair is two neighbours                                       */
+#define MOE_ROPE_INVERSE 0x2u /* turn back: s -> -s (with m = 1 the inverse and the gradient)    */
+
+/* How rows are turned.  rot: multiple of 16, at most D.  q_norm, k_norm (fp32 [D],
+   16-byte aligned, or NULL): each head x becomes x / sqrt(mean(x^2) + eps) * norm first,
+   in fp32; eps >= 0. */
+typedef struct {
+    const float* table;
+    const float* q_norm;
+    const float* k_norm;
+    int32_t n_pos; /* rows of the table */
+    int32_t rot;
+    uint32_t flags;
+    float eps;
+} moe_rope_t;
+
+/* moe_rope_rows -- rows of any heads, for use without a cache.
+ *   x    (device) bf16 [T][H][D], token t at x + t * ldx elements; 16-byte aligned, ldx a multiple
+ *        of 8, at least H * D when T > 1.  D 64 or 128, T * H < 2^31
+ *   pos  (device) int32 [T], rows of the table; a token whose position is
+ *        negative is left out, and one past the table too, with the device check flag
+ *   rope q_norm is applied, k_norm not used
+ *   out  (device) out: bf16, laid out like x with ldo; may be x itself (with
+ *        ldo = ldx), else it does not overlap x
+ *   ws   as moe_kv_plan */
+moe_status_t moe_rope_rows(const uint16_t* x, int64_t ldx, const int32_t* pos, int32_t T, int32_t H,
+                           int32_t D, const moe_rope_t* rope, uint16_t* out, int64_t ldo, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* moe_rope_kv_write -- new queries turned, new keys turned and written into the
+ * cache with the new values, in one launch: moe_rope_rows on q and k and
+ * moe_kv_write in one, except that a turned key is not rounded to bf16 before it
+ * becomes codes (the scale and the codes are those of the fp32 values).
+ *   q, k, v  (device) bf16 [T][H or H_kv][D], as in moe_rope_rows (ldq, ldk, ldv)
+ *   pos      (device) int32 [T], as in moe_rope_rows; of a token that is left
+ *            out nothing is written, neither its query nor its key and value
+ *   slots    (device) int32 [T], as in moe_kv_write; a negative slot leaves out
+ *            the key and value only
+ *   q_out    (device) out: bf16 [T][H][D] with ldo; may be q itself (ldo = ldq),
+ *            else it does not overlap q, k and v
+ * The other arguments as in moe_kv_write. */
+moe_status_t moe_rope_kv_write(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk,
+                               const uint16_t* v, int64_t ldv, const int32_t* pos,
+                               const int32_t* slots, const moe_rope_t* rope,
+                               const moe_kv_dims_t* dims, const moe_kv_t* cache, uint16_t* q_out,
+                               int64_t ldo, void* ws, size_t ws_bytes, void* stream);
+
+/* ============================================================================
+ * The norms between blocks, fused with what lies between them:
+ *   u = y                                        (the block's output)
+ *   u = u / sqrt(mean(u^2) + eps) * w_post       if w_post
+ *   u = u * g                                    if there is a gate: g, or 1 / (1 + e^-g)
+ *   r' = residual + scale * u                    (fp32; rounded once into residual_out)
+ *   x = r' / sqrt(mean(r'^2) + eps) * w_pre      if w_pre: the next block's input, from
+ *                                                the unrounded r'
+ * ========================================================================= */
+typedef enum {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_TOKEN = 1,   /* fp32 [T]    */
+    MOE_GATE_CHANNEL = 2, /* fp32 [d]    */
+    MOE_GATE_FULL = 3     /* bf16 [T][d] */
+} moe_gate_t;
+
+#define MOE_NORM_SIGMOID 0x1u      /* the gate is 1 / (1 + e^-g)                   */
+#define MOE_NORM_RESIDUAL_F32 0x2u /* residual and residual_out are fp32, not bf16 */
+
+typedef struct {
+    int32_t T;
+    int32_t d;      /* a multiple of 8, at most 32768 */
+    int32_t gate;   /* moe_gate_t                     */
+    uint32_t flags; /* MOE_NORM_*                     */
+    float eps;      /* >= 0                           */
+    float scale;    /* finite                         */
+} moe_norm_dims_t;
+
+/* moe_block_norm -- the above, one launch.
+ *   y            (device) bf16 [T][d], or NULL (the first norm of a model): then
+ *                r' = residual, residual_out is not written and may be NULL, and
+ *                gate and w_post must be NULL
+ *   residual     (device) bf16 or fp32 [T][d]
+ *   gate         (device) by dims.gate; NULL for MOE_GATE_NONE
+ *   w_post       (device) fp32 [d] or NULL
+ *   w_pre        (device) fp32 [d] or NULL
+ *   residual_out (device) out: like residual; may be residual itself
+ *   x            (device) out: bf16 [T][d]; may be y itself; NULL exactly when w_pre is
+ * All contiguous and 16-byte aligned (a MOE_GATE_TOKEN gate 4-byte).  Values whose
+ * squares add up past the range of fp32 are outside what the norms are for. */
+moe_status_t moe_block_norm(const uint16_t* y, const void* residual, const void* gate,
+                            const float* w_post, const float* w_pre, const moe_norm_dims_t* dims,
+                            void* residual_out, uint16_t* x, void* stream);
+
+/* ============================================================================
+ * Microscaled 4-bit floats: rows of E2M1 codes with one E4M3 scale for each 16
+ * of them and one fp32 scale per row, beside the W8A8 recipe above (the page's dense
+ * FP4 projections: thewafflehaus/FFAI PR #72).
+ *   s = absmax(row) / 2688 (448 * 6)
+ *   b = e4m3(absmax(block of 16) / (6 s)),  code = e2m1(x / (b s))
+ * (fp32 operations, ties to even, conversions saturate; 6 s = 0 gives b = 0, and b s = 0
+ * codes 0).  An element stands for code * (b * s).  E2M1: 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 with a sign (codes 0..7, +8).
+ *   q  uint8 [rows][K/2]: byte j holds element 2j in bits 0-3 and 2j+1 in bits 4-7
+ *   b  E4M3 bytes in tiles of 128 rows and 4 blocks, the order the tensor core
+ *      reads: the scale of row r and block j is byte
+ *      ((r / 128) * (K / 64) + j / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4
+ *      of moe_fp4_scale_bytes(rows, K); bytes of rows past the last are not read
+ *      into any result
+ *   s  fp32 [rows]
+ * q and b 16-byte, s 4-byte aligned; K a multiple of 64, at most 65536.  Rows must be finite.
+ * ========================================================================= */
+typedef struct {
+    const uint8_t* q;
+    const uint8_t* b;
+    const float* s;
+} moe_fp4_t;
+
+/* Bytes of b (0 for sizes the calls below refuse). */
+size_t moe_fp4_scale_bytes(int64_t rows, int64_t K);
+
+/* moe_pack_fp4, moe_quant_rows_fp4 -- fp32 weights, or bf16 activations, [rows][K]
+ * (device, 16-byte aligned) to q, b, s (device).  rows < 2^31 - 128, rows * K
+ * < 2^40. */
+moe_status_t moe_pack_fp4(const float* w, int64_t rows, int64_t K, uint8_t* q, uint8_t* b, float* s,
+                          void* stream);
+moe_status_t moe_quant_rows_fp4(const uint16_t* x, int64_t rows, int64_t K, uint8_t* q, uint8_t* b,
+                                float* s, void* stream);
+
+/* moe_unpack_fp4 -- what the rows stand for: out bf16 [rows][K] (device, 16-byte
+ * aligned), each element's fp32 value rounded to bf16. */
+moe_status_t moe_unpack_fp4(moe_fp4_t w, int64_t rows, int64_t K, uint16_t* out, void* stream);
+
+/* Workspace of moe_linear_fp4 for up to T tokens (0 for sizes it refuses). */
+size_t moe_linear_fp4_workspace_bytes(int32_t T, int32_t N, int32_t K);
+
+/* moe_linear_fp4 -- a projection: x quantised as above, then
+ *   out[t][n] = bf16( sum_j x^_tj w^_nj ),
+ * x^ and w^ what the codes stand for: code products with their block scales
+ * summed in fp32 over K, then the two row scales.
+ *   x    (device) bf16 [T][K], token t at x + t * ldx elements; 16-byte aligned,
+ *        ldx a multiple of 8, at least K when T > 1
+ *   w    weights of moe_pack_fp4, N rows
+ *   out  (device) out: bf16 [T][N], contiguous, 16-byte aligned
+ *   ws   moe_linear_fp4_workspace_bytes(T, N, K), zero-filled before its first
+ *        use; calls of any sizes that fit leave it ready for the next.  Not one
+ *        that other calls use.
+ * N a multiple of 8, N < 2^24, T < 2^24. */
+moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N, int32_t K,
+                            moe_fp4_t w, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -30,6 +30,22 @@ MOE_KV_BF16 = 0
 MOE_KV_E4M3 = 1
 MOE_KV_INT4 = 2
 
+MOE_ROPE_NONE = 0
+MOE_ROPE_LINEAR = 1
+MOE_ROPE_RAMP = 2
+MOE_ROPE_BAND = 3
+
+MOE_ROPE_PAIRS = 0x1
+MOE_ROPE_INVERSE = 0x2
+
+MOE_GATE_NONE = 0
+MOE_GATE_TOKEN = 1
+MOE_GATE_CHANNEL = 2
+MOE_GATE_FULL = 3
+
+MOE_NORM_SIGMOID = 0x1
+MOE_NORM_RESIDUAL_F32 = 0x2
+
 MOE_FLAG_FORCE_GEMV = 0x1
 MOE_FLAG_FORCE_GROUPED = 0x2
 MOE_FLAG_NO_SCHED = 0x4
@@ -45,7 +61,9 @@ EXPORTS = (
     "moe_down_combine_w4a16", "moe_pack_w8", "moe_quant_rows_fp8",
     "moe_layer_workspace_bytes_w8a8", "moe_layer_forward_w8a8", "moe_gateup_swiglu_w8a8",
     "moe_down_w8a8", "moe_debug_set_waits", "moe_kv_write", "moe_kv_read",
-    "moe_attn_workspace_bytes", "moe_attn_paged",
+    "moe_attn_workspace_bytes", "moe_attn_paged", "moe_kv_plan", "moe_rope_table", "moe_rope_rows",
+    "moe_rope_kv_write", "moe_block_norm", "moe_fp4_scale_bytes", "moe_pack_fp4", "moe_quant_rows_fp4",
+    "moe_unpack_fp4", "moe_linear_fp4_workspace_bytes", "moe_linear_fp4",
 )
 
 
@@ -98,6 +116,41 @@ class Kv(ctypes.Structure):
     shape = None
 
 
+class KvPages(ctypes.Structure):
+    """moe_kv_pages_t: the state of a pool's pages (device pointers).  kv_pages makes one and
+    records its sizes for the calls' checks."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("kv_len", "first", "pages", "free_pages", "n_free")]
+    sizes = None
+
+
+class RopeConfig(ctypes.Structure):
+    """moe_rope_config_t: which angles a rotary table holds."""
+    _fields_ = [(n, ctypes.c_double) for n in ("base", "factor", "orig_len", "lo", "hi", "magnitude")] + \
+               [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """moe_rope_t: how rows are turned (device pointers).  rope makes one and records the width of
+    its norms for the calls' checks."""
+    _fields_ = [("table", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("n_pos", ctypes.c_int32), ("rot", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("eps", ctypes.c_float)]
+    D = None
+
+
+class NormDims(ctypes.Structure):
+    """moe_norm_dims_t."""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class Fp4(ctypes.Structure):
+    """moe_fp4_t: 4-bit codes, block scales and row scales (device pointers).  fp4 makes one and
+    records its shape for the calls' checks."""
+    _fields_ = [("q", ctypes.c_void_p), ("b", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+    shape = None
+
+
 _lib = None
 
 
@@ -112,6 +165,7 @@ def lib() -> ctypes.CDLL:
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(Dims)
     KD, KC, f32 = ctypes.POINTER(KvDims), ctypes.POINTER(Kv), ctypes.c_float
+    R = ctypes.POINTER(Rope)
     sigs = {
         "moe_status_string": ([i32], ctypes.c_char_p),
         "moe_pack_w4": ([p, i64, i64, i32, p, p, p], i32),
@@ -142,6 +196,17 @@ def lib() -> ctypes.CDLL:
         "moe_kv_read": ([p, KD, KC, p, p, p, sz, p], i32),
         "moe_attn_workspace_bytes": ([KD], sz),
         "moe_attn_paged": ([p, i64, p, p, p, KD, KC, f32, p, p, p, sz, p], i32),
+        "moe_kv_plan": ([p, KD, ctypes.POINTER(KvPages), p, p, p, p, sz, p], i32),
+        "moe_rope_table": ([ctypes.POINTER(RopeConfig), i32, i32, p, p], i32),
+        "moe_rope_rows": ([p, i64, p, i32, i32, i32, R, p, i64, p, sz, p], i32),
+        "moe_rope_kv_write": ([p, i64, p, i64, p, i64, p, p, R, KD, KC, p, i64, p, sz, p], i32),
+        "moe_block_norm": ([p, p, p, p, p, ctypes.POINTER(NormDims), p, p, p], i32),
+        "moe_fp4_scale_bytes": ([i64, i64], sz),
+        "moe_pack_fp4": ([p, i64, i64, p, p, p, p], i32),
+        "moe_quant_rows_fp4": ([p, i64, i64, p, p, p, p], i32),
+        "moe_unpack_fp4": ([Fp4, i64, i64, p, p], i32),
+        "moe_linear_fp4_workspace_bytes": ([i32, i32, i32], sz),
+        "moe_linear_fp4": ([p, i64, i32, i32, i32, Fp4, p, p, sz, p], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -168,7 +233,7 @@ def _ptr(t):
 
 # 16-bit float patterns may travel as int16 or as the matching torch dtype
 _BITS16 = (torch.int16, torch.bfloat16, torch.float16)
-_ALIASES = {torch.int16: _BITS16}
+_ALIASES = {torch.int16: _BITS16, torch.bfloat16: (torch.bfloat16, torch.int16)}
 
 
 def _dev(t: torch.Tensor, dtype, name: str):
@@ -542,3 +607,230 @@ def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, p
         ws.data_ptr(), ws.numel(), _stream(stream))
     if status:
         raise MoeError(status, "moe_attn_paged")
+
+
+# ------------------------------------- page planning, rotary positions, block norms, 4-bit floats
+
+def _here(**tensors):
+    """Refuses tensors that are not on the current device, whose stream the calls go to."""
+    dev = torch._C._cuda_getDevice()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+
+
+def _not_half(**tensors):
+    """Refuses f16 tensors, which the row checks take for bit patterns."""
+    for name, t in tensors.items():
+        if t.dtype is torch.float16:
+            raise ValueError(f"{name} must be bf16, got {t.dtype}")
+
+
+def kv_pages(kv_len: torch.Tensor, first: torch.Tensor, pages: torch.Tensor, free_pages: torch.Tensor,
+             n_free: torch.Tensor) -> KvPages:
+    """The state that moe_kv_plan keeps, from its int32 tensors: kv_len and first [B], pages
+    [B][max_pages], free_pages [n_pages], n_free [1].  The handle keeps them alive."""
+    B = kv_len.numel()
+    if pages.dim() != 2 or pages.shape[0] != B:
+        raise ValueError("pages must be [B][max_pages]")
+    _here(kv_len=kv_len, first=first, pages=pages, free_pages=free_pages, n_free=n_free)
+    st = KvPages(_ints(kv_len, B, "kv_len"), _ints(first, B, "first"), _dev(pages, torch.int32, "pages"),
+                 _dev(free_pages, torch.int32, "free_pages"), _ints(n_free, 1, "n_free"))
+    st.sizes = (B, pages.shape[1], free_pages.numel())
+    st.tensors = (kv_len, first, pages, free_pages, n_free)
+    return st
+
+
+def moe_kv_plan(new_len: torch.Tensor, dims: KvDims, state: KvPages, q_off: torch.Tensor, pos: torch.Tensor,
+                slots: torch.Tensor, ws, stream=None):
+    """One step of a batch planned: new_len int32 [B] tokens more (or, negative, fewer) per sequence; the
+    state's lengths and pages follow, and q_off int32 [B+1], pos and slots int32 [T] name the new
+    tokens.  See include/moe.h."""
+    T, B = dims.T, dims.B
+    if state.sizes is not None and state.sizes != (B, dims.max_pages, dims.n_pages):
+        raise ValueError("the state's sizes are not those of dims")
+    _here(new_len=new_len, q_off=q_off, pos=pos, slots=slots, ws=ws)
+    status = (_lib or lib()).moe_kv_plan(
+        _ints(new_len, B, "new_len"), ctypes.byref(dims), ctypes.byref(state), _ints(q_off, B + 1, "q_off"),
+        _ints(pos, T, "pos"), _ints(slots, T, "slots"), ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_kv_plan")
+
+
+def moe_rope_table(config: RopeConfig, pos0: int, table: torch.Tensor, stream=None):
+    """The rotary table fp32 [n_pos][rot] of positions pos0 on: cosines, then sines."""
+    if table.dim() != 2 or table.shape[1] != config.rot:
+        raise ValueError("table must be [n_pos][rot]")
+    _here(table=table)
+    status = (_lib or lib()).moe_rope_table(ctypes.byref(config), pos0, table.shape[0],
+                                            _dev(table, torch.float32, "table"), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_rope_table")
+
+
+def rope(table: torch.Tensor, flags: int = 0, q_norm: torch.Tensor | None = None,
+         k_norm: torch.Tensor | None = None, eps: float = 0.0) -> Rope:
+    """How rows are turned: a table fp32 [n_pos][rot], MOE_ROPE_* flags, and the weights fp32 [D] of the
+    heads' norms, if any.  The handle keeps them alive."""
+    if table.dim() != 2:
+        raise ValueError("table must be [n_pos][rot]")
+    _here(table=table, q_norm=q_norm, k_norm=k_norm)
+    widths = {t.numel() for t in (q_norm, k_norm) if t is not None}
+    if len(widths) > 1:
+        raise ValueError("q_norm and k_norm must be [D]")
+    r = Rope(_dev(table, torch.float32, "table"), None if q_norm is None else _dev(q_norm, torch.float32, "q_norm"),
+             None if k_norm is None else _dev(k_norm, torch.float32, "k_norm"), table.shape[0], table.shape[1],
+             flags, eps)
+    r.D = widths.pop() if widths else None
+    r.tensors = (table, q_norm, k_norm)
+    return r
+
+
+def _rope_check(rope: Rope, D: int):
+    if rope.D is not None and rope.D != D:
+        raise ValueError(f"the norms must be [D] with D = {D}")
+
+
+def moe_rope_rows(x: torch.Tensor, pos: torch.Tensor, rope: Rope, out: torch.Tensor, ws, stream=None):
+    """Rows bf16 [T][H][D] (tokens may lie apart), normalised by q_norm where rope has it, turned to their
+    positions int32 [T].  out may be x."""
+    if x.dim() != 3:
+        raise ValueError("x must be [T][H][D]")
+    T, H, D = x.shape
+    _rope_check(rope, D)
+    _here(x=x, pos=pos, out=out, ws=ws)
+    _not_half(x=x, out=out)
+    xp, ldx = _rows(x, T, H, D, "x")
+    op, ldo = _rows(out, T, H, D, "out")
+    status = (_lib or lib()).moe_rope_rows(xp, ldx, _ints(pos, T, "pos"), T, H, D, ctypes.byref(rope), op, ldo,
+                                           ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_rope_rows")
+
+
+def moe_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, slots: torch.Tensor,
+                      rope: Rope, dims: KvDims, cache: Kv, q_out: torch.Tensor, ws, stream=None):
+    """New queries bf16 [T][H][D] turned into q_out (which may be q), new keys [T][H_kv][D] turned and
+    written into the cache's slots with the values (tokens of each may lie apart)."""
+    T, H, D = dims.T, dims.H, dims.D
+    _kv_check(dims, cache, dims.H_kv, D)
+    _rope_check(rope, D)
+    _here(q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out, ws=ws)
+    _not_half(q=q, k=k, v=v, q_out=q_out)
+    qp, ldq = _rows(q, T, H, D, "q")
+    kp, ldk = _rows(k, T, dims.H_kv, D, "k")
+    vp, ldv = _rows(v, T, dims.H_kv, D, "v")
+    op, ldo = _rows(q_out, T, H, D, "q_out")
+    status = (_lib or lib()).moe_rope_kv_write(
+        qp, ldq, kp, ldk, vp, ldv, _ints(pos, T, "pos"), _ints(slots, T, "slots"), ctypes.byref(rope),
+        ctypes.byref(dims), ctypes.byref(cache), op, ldo, ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_rope_kv_write")
+
+
+def _sized(t: torch.Tensor | None, n: int, dtype, name: str):
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return _dev(t, dtype, name)
+
+
+def moe_block_norm(y: torch.Tensor | None, residual: torch.Tensor, gate: torch.Tensor | None,
+                   w_post: torch.Tensor | None, w_pre: torch.Tensor | None, dims: NormDims,
+                   residual_out: torch.Tensor | None, x: torch.Tensor | None, stream=None):
+    """residual_out = residual + scale * gate * norm(y) and x = norm(residual_out), each part where it
+    is given: y, x bf16 [T][d], residual bf16 or fp32 (MOE_NORM_RESIDUAL_F32), the norms' weights fp32 [d],
+    the gate by dims.gate.  residual_out may be residual and x may be y.  See include/moe.h."""
+    n, d = dims.T * dims.d, dims.d
+    res = torch.float32 if dims.flags & MOE_NORM_RESIDUAL_F32 else torch.bfloat16
+    size, kind = {MOE_GATE_TOKEN: (dims.T, torch.float32), MOE_GATE_CHANNEL: (d, torch.float32)}.get(
+        dims.gate, (n, torch.bfloat16))
+    _here(y=y, residual=residual, gate=gate, w_post=w_post, w_pre=w_pre, residual_out=residual_out, x=x)
+    status = (_lib or lib()).moe_block_norm(
+        _sized(y, n, torch.bfloat16, "y"), _sized(residual, n, res, "residual"), _sized(gate, size, kind, "gate"),
+        _sized(w_post, d, torch.float32, "w_post"), _sized(w_pre, d, torch.float32, "w_pre"), ctypes.byref(dims),
+        _sized(residual_out, n, res, "residual_out"), _sized(x, n, torch.bfloat16, "x"), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_block_norm")
+
+
+def moe_fp4_scale_bytes(rows: int, K: int) -> int:
+    return lib().moe_fp4_scale_bytes(rows, K)
+
+
+def fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor) -> Fp4:
+    """Rows in 4-bit floats: q uint8 [rows][K/2], b uint8 block scales in their tiles, s fp32 [rows].  The
+    handle keeps them alive."""
+    if q.dim() != 2 or s.numel() != q.shape[0] or b.numel() != moe_fp4_scale_bytes(q.shape[0], 2 * q.shape[1]):
+        raise ValueError("q must be [rows][K/2], s [rows] and b moe_fp4_scale_bytes(rows, K) bytes")
+    _here(q=q, b=b, s=s)
+    w = Fp4(_dev(q, torch.uint8, "q"), _dev(b, torch.uint8, "b"), _dev(s, torch.float32, "s"))
+    w.shape, w.tensors = (q.shape[0], 2 * q.shape[1]), (q, b, s)
+    return w
+
+
+def _fp4_out(x: torch.Tensor, q, b, s):
+    if x.dim() != 2:
+        raise ValueError("rows must be [rows][K]")
+    rows, K = x.shape
+    n = moe_fp4_scale_bytes(rows, K)
+    if q is None:
+        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    if b is None:  # (zeros: the tiles' bytes past the last row are not written)
+        b = torch.zeros(n, dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _here(x=x, q=q, b=b, s=s)
+    return rows, K, q, b, s, (_sized(q, rows * (K // 2), torch.uint8, "q"), _sized(b, n, torch.uint8, "b"),
+                              _sized(s, rows, torch.float32, "s"))
+
+
+def moe_pack_fp4(w: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor | None = None,
+                 s: torch.Tensor | None = None, stream=None):
+    """fp32 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
+    rows, K, q, b, s, to = _fp4_out(w, q, b, s)
+    _check((_lib or lib()).moe_pack_fp4(_dev(w, torch.float32, "w"), rows, K, *to, _stream(stream)), "moe_pack_fp4")
+    return q, b, s
+
+
+def moe_quant_rows_fp4(x: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor | None = None,
+                       s: torch.Tensor | None = None, stream=None):
+    """bf16 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
+    rows, K, q, b, s, to = _fp4_out(x, q, b, s)
+    _check((_lib or lib()).moe_quant_rows_fp4(_dev(x, torch.bfloat16, "x"), rows, K, *to, _stream(stream)),
+           "moe_quant_rows_fp4")
+    return q, b, s
+
+
+def moe_unpack_fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """What rows in 4-bit floats stand for, bf16 [rows][K]."""
+    w = fp4(q, b, s)
+    rows, K = w.shape
+    if out is None:
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.device)
+    _here(out=out)
+    _check((_lib or lib()).moe_unpack_fp4(w, rows, K, _sized(out, rows * K, torch.bfloat16, "out"), _stream(stream)),
+           "moe_unpack_fp4")
+    return out
+
+
+def moe_linear_fp4_workspace_bytes(T: int, N: int, K: int) -> int:
+    return lib().moe_linear_fp4_workspace_bytes(T, N, K)
+
+
+def moe_linear_fp4(x: torch.Tensor, w: Fp4, out: torch.Tensor, ws, stream=None):
+    """out bf16 [T][N] = the projection of x bf16 [T][K] (tokens may lie apart), quantised to 4-bit floats,
+    by weights w of moe_pack_fp4."""
+    if w.shape is None:
+        raise ValueError("w must come from fp4()")
+    N, K = w.shape
+    if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1) or x.dtype not in _ALIASES[torch.bfloat16]:
+        raise ValueError("x must be bf16 [T][K] with contiguous tokens")
+    T = x.shape[0]
+    _here(x=x, out=out, ws=ws)
+    status = (_lib or lib()).moe_linear_fp4(
+        x.data_ptr(), x.stride(0) if T > 1 else K, T, N, K, w, _sized(out, T * N, torch.bfloat16, "out"),
+        ws.data_ptr(), ws.numel(), _stream(stream))
+    if status:
+        raise MoeError(status, "moe_linear_fp4")

@@ -7,7 +7,7 @@
 
 using namespace moe;
 
-namespace {
+namespace moe {
 
 moe_status_t check_kv_dims(const moe_kv_dims_t* d) {
     if (!d) return MOE_ERR_INVALID_ARG;
@@ -46,7 +46,7 @@ moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 moe_status_t map_err(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-}  // namespace
+}  // namespace moe
 
 extern "C" {
 

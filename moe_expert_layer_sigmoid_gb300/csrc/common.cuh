@@ -23,6 +23,8 @@ enum : int32_t {
     kErrBadSlot = 1 << 4,        // a cache slot past the pool
     kErrBadSeq = 1 << 5,         // a sequence's token range or length outside its bounds
     kErrBadPage = 1 << 6,        // a page id outside the pool
+    kErrNoRoom = 1 << 7,         // tokens or pages did not last for every sequence of a plan
+    kErrBadPos = 1 << 8,         // a position past the rotary table
 };
 
 // Workspace header: the first 256 bytes of every workspace.

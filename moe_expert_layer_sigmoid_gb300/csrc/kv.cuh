@@ -48,4 +48,11 @@ cudaError_t launch_kv_read(const int32_t* slots, const moe_kv_dims_t& d, const m
 size_t attn_workspace_bytes(const moe_kv_dims_t& d);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 
+// Host-side argument checks of the calls on a cache (abi_attn.cu).
+moe_status_t check_kv_dims(const moe_kv_dims_t* d);
+bool kv_ok(const moe_kv_t* c, const moe_kv_dims_t& d);
+bool rows_ok(const void* p, int64_t ld, int32_t T, int64_t width);
+moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need);
+moe_status_t map_err(cudaError_t e);
+
 }  // namespace moe

@@ -1,0 +1,260 @@
+// Page planning: block tables and slot maps from request lengths.
+//
+// Three exclusive sums over the batch (pages given back, then tokens and pages of the
+// sequences that can be served) place everything; what follows is a copy of ids, and a
+// search in the sums for each token.  The bytes are few (8 per token): a call is a launch,
+// the sums' latency and, with many tokens, their search.  So it is one launch, of one CTA or of
+// one cluster whose CTAs all make the same sums (the batch's lengths are a few KB) and share
+// the copies and the tokens: nothing is handed from one CTA to another but the state itself, behind
+// two cluster barriers.  No result depends on timing.
+#include "kv.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanParams {
+    const int32_t* new_len;
+    moe_kv_pages_t st;
+    int32_t *q_off, *pos, *slots;
+    WsHeader* hdr;
+    int T, B, page_log2, n_pages, max_pages, window;
+};
+
+// One sequence's step, before it is known whether there is room.
+struct Step {
+    int after;       // its tokens before the new ones
+    int first;       // the first page it holds from now on
+    int lo, hi;      // entries whose pages go back
+    int want, need;  // tokens and pages asked for
+};
+
+__device__ __forceinline__ int pages_of(int tokens, int lg) {
+    return (int)(((unsigned)tokens + (1u << lg) - 1) >> lg);
+}
+
+__device__ __forceinline__ Step step_of(const PlanParams& p, int b, bool& bad) {
+    const int n = p.new_len[b], L = p.st.kv_len[b], f = p.st.first[b];
+    Step s{L, f, 0, 0, 0, 0};
+    const int64_t most = (int64_t)p.max_pages << p.page_log2;
+    if (L < 0 || L > most || f < 0 || f > pages_of(L, p.page_log2)) {
+        bad = true;
+        return s;
+    }
+    if (n < 0) {
+        const int64_t left = (int64_t)L + n;
+        const int after = left > 0 ? (int)left : 0;
+        // the window's last keys went back with their pages: a shorter sequence would need some again
+        if (after > 0 && ((int64_t)f << p.page_log2) > max(0, after - p.window + 1)) {
+            bad = true;
+            return s;
+        }
+        s.after = after;
+        s.first = after > 0 ? f : 0;
+        s.lo = max(pages_of(after, p.page_log2), f);
+        s.hi = pages_of(L, p.page_log2);
+        return s;
+    }
+    if (n > most - L) {
+        bad = true;
+        return s;
+    }
+    if (p.window > 0) s.first = max(f, max(0, L - p.window + 1) >> p.page_log2);
+    s.lo = f;
+    s.hi = s.first;
+    s.want = n;
+    s.need = pages_of(L + n, p.page_log2) - pages_of(L, p.page_log2);
+    return s;
+}
+
+struct Sums {
+    int64_t a, b, c;
+};
+
+// Exclusive sums over the CTA's threads; `total` gets the sums of all.
+__device__ __forceinline__ Sums scan(Sums v, Sums* part, Sums& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Sums x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xFFFFFFFFu, x.a, o), b = __shfl_up_sync(0xFFFFFFFFu, x.b, o),
+                      c = __shfl_up_sync(0xFFFFFFFFu, x.c, o);
+        if (lane >= o) {
+            x.a += a;
+            x.b += b;
+            x.c += c;
+        }
+    }
+    __syncthreads();  // (the sums of an earlier scan have been read)
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    Sums before{0, 0, 0};
+    total = before;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const Sums t = part[w];
+        if (w < warp) {
+            before.a += t.a;
+            before.b += t.b;
+            before.c += t.c;
+        }
+        total.a += t.a;
+        total.b += t.b;
+        total.c += t.c;
+    }
+    return Sums{before.a + x.a - v.a, before.b + x.b - v.b, before.c + x.c - v.c};
+}
+
+// The last b of [0, B) with off[b] <= i, off ascending from 0.
+__device__ __forceinline__ int find(const int32_t* off, int B, int i) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// All CTAs of the launch (one cluster), their writes to global memory visible to each other.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams p) {
+    extern __shared__ int32_t smem[];
+    __shared__ Sums part[kPlanWarps];
+    int32_t* after = smem;             // [B] tokens before the new ones
+    int32_t* q_off = after + p.B;      // [B] first row (while summing: tokens asked for)
+    int32_t* given = q_off + p.B;      // [B] first of the new pages in the order of taking (pages asked for)
+    int32_t* back = given + p.B;       // [B] first of the returned pages in their list
+    int32_t* lo = back + p.B;          // [B] entry of that page
+    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+    const bool chief = blockIdx.x == 0;
+    int errors = 0;
+
+    Sums mine{0, 0, 0}, all;
+    for (int b = b0; b < b1; ++b) {
+        bool bad = false;
+        const Step s = step_of(p, b, bad);
+        if (bad) errors |= kErrBadSeq;
+        after[b] = s.after;
+        q_off[b] = s.want;
+        given[b] = s.need;
+        back[b] = s.hi - s.lo;
+        lo[b] = s.lo;
+        mine.a += s.want;
+        mine.b += s.need;
+        mine.c += s.hi - s.lo;
+    }
+    Sums at = scan(mine, part, all);
+    const int kept = p.st.n_free[0];
+    const int had = min(max(kept, 0), p.n_pages);
+    const int returned = (int)min(all.c, (int64_t)(1 << 30));  // (of a state that is whole: at most n_pages)
+    const int total = (int)min((int64_t)had + returned, (int64_t)p.n_pages);
+    if (had != kept || had + (int64_t)returned > p.n_pages) errors |= kErrBadPage;
+    mine = Sums{0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const int want = q_off[b], need = given[b], gone = back[b];
+        at.a += want;
+        at.b += need;
+        const bool fits = at.a <= p.T && (need == 0 || at.b <= total);
+        if (!fits) {
+            if (want) errors |= kErrNoRoom;
+            q_off[b] = given[b] = 0;
+        } else {
+            mine.a += want;
+            mine.b += need;
+        }
+        back[b] = (int)min(at.c, (int64_t)(1 << 30));
+        at.c += gone;
+    }
+    at = scan(mine, part, all);
+    const int tokens = (int)all.a, taken = (int)all.b;
+    // Every CTA has read the state; now it changes.  (Entries that go back are read behind the barrier too, but
+    // each by the one thread that then clears it.)
+    for (int b = b0; b < b1; ++b) {
+        const int want = q_off[b], need = given[b];
+        q_off[b] = (int)at.a;
+        given[b] = (int)at.b;
+        at.a += want;
+        at.b += need;
+    }
+    __syncthreads();
+    cluster_barrier();
+
+    const int threads = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + threadIdx.x;
+    for (int r = me; r < returned; r += threads) {
+        const int b = find(back, p.B, r);
+        int32_t* e = p.st.pages + (int64_t)b * p.max_pages + lo[b] + (r - back[b]);
+        const int to = had + returned - 1 - r;
+        if (to < p.n_pages) p.st.free_pages[to] = *e;
+        *e = -1;
+    }
+    if (chief) {
+        for (int b = b0; b < b1; ++b) {
+            bool bad = false;
+            const Step s = step_of(p, b, bad);
+            const int next = b + 1 < p.B ? q_off[b + 1] : tokens;
+            p.q_off[b] = q_off[b];
+            p.st.kv_len[b] = s.after + (next - q_off[b]);
+            p.st.first[b] = s.first;
+        }
+        if (threadIdx.x == 0) {
+            p.q_off[p.B] = tokens;
+            p.st.n_free[0] = total - taken;
+        }
+        if (errors) record_error(p.hdr, errors);
+    }
+    if (returned > 0) {
+        __syncthreads();
+        cluster_barrier();
+    }
+    for (int r = me; r < taken; r += threads) {
+        const int b = find(given, p.B, r);
+        p.st.pages[(int64_t)b * p.max_pages + pages_of(after[b], p.page_log2) + (r - given[b])] =
+            p.st.free_pages[total - 1 - r];
+    }
+    const int mask = (1 << p.page_log2) - 1;
+    for (int t = me; t < p.T; t += threads) {
+        int pos = -1, slot = -1;
+        if (t < tokens) {
+            const int b = find(q_off, p.B, t);
+            pos = after[b] + (t - q_off[b]);
+            const int i = pos >> p.page_log2, fresh = i - pages_of(after[b], p.page_log2);
+            const int id = fresh < 0 ? p.st.pages[(int64_t)b * p.max_pages + i]
+                                     : p.st.free_pages[total - 1 - (given[b] + fresh)];
+            if ((unsigned)id < (unsigned)p.n_pages) slot = (id << p.page_log2) + (pos & mask);
+            else record_error(p.hdr, kErrBadPage);
+        }
+        p.pos[t] = pos;
+        p.slots[t] = slot;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const int32_t* new_len, const moe_kv_dims_t& d, const moe_kv_pages_t& st,
+                           int32_t* q_off, int32_t* pos, int32_t* slots, WsHeader* hdr, cudaStream_t stream) {
+    const PlanParams p{new_len, st, q_off, pos, slots, hdr, d.T, d.B, __builtin_ctz(d.page), d.n_pages,
+                       d.max_pages, d.window};
+    const size_t smem = 5 * sizeof(int32_t) * (size_t)d.B;
+    cudaError_t err = ensure_dynamic_smem((const void*)kv_plan_kernel, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(d.T > 2 * kPlanThreads ? 8 : 1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cfg.gridDim.x;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_plan_kernel, p);
+}
+
+}  // namespace moe

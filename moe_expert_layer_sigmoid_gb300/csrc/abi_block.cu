@@ -170,14 +170,14 @@ moe_status_t moe_unpack_fp4(moe_fp4_t w, int64_t rows, int64_t K, uint16_t* out,
 }
 
 size_t moe_linear_fp4_workspace_bytes(int32_t T, int32_t N, int32_t K) {
-    return check_linear(T, N, K) == MOE_OK ? fp4_ws(T, N, K).bytes : 0;
+    return check_linear(T, N, K) == MOE_OK ? fp4_ws(T, K).bytes : 0;
 }
 
 moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N, int32_t K,
                             moe_fp4_t w, uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
     moe_status_t st = check_linear(T, N, K);
     if (st != MOE_OK) return st;
-    const Fp4Ws at = fp4_ws(T, N, K);
+    const Fp4Ws at = fp4_ws(T, K);
     if ((st = check_ws(ws, ws_bytes, at.bytes)) != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     if (!rows_ok(x, ldx, T, K) || !act_ok(w.q) || !act_ok(w.b) || !aligned4(w.s) || !act_ok(out))
@@ -187,7 +187,7 @@ moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N
     const cudaStream_t stm = static_cast<cudaStream_t>(stream);
     const cudaError_t err = launch_quant_fp4(x, true, ldx, T, K, xq, stm);
     if (err != cudaSuccess) return map_err(err);
-    return map_err(launch_linear_fp4(moe_fp4_t{xq.q, xq.b, xq.s}, w, T, N, K, out, ws, stm));
+    return map_err(launch_linear_fp4(moe_fp4_t{xq.q, xq.b, xq.s}, w, T, N, K, out, ws, at, stm));
 }
 
 }  // extern "C"

@@ -55,6 +55,7 @@ template <typename Src, int PER>
 __global__ void __launch_bounds__(1024) quant_kernel(const Src* __restrict__ src, int64_t ld, int64_t rows, int K,
                                                      Fp4Rows out) {
     __shared__ float part[32];
+    pdl_trigger();  // the projection's kernel fetches weights meanwhile
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const int blocks = K / 16, lane = threadIdx.x & 31;
     float f[PER][16], m[PER];

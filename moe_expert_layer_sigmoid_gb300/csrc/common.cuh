@@ -253,6 +253,20 @@ __device__ __forceinline__ void ffma2(float& a0, float& a1, float s, float v0, f
         : "f"(v0), "f"(v1), "f"(s));
 }
 
+// 16 or 8 bytes of global memory to shared memory behind the thread's back; a thread's copies are grouped by commits
+// and waited for all but the last N groups.  What a thread copies for itself needs no barrier.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* from) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(smem);
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Programmatic dependent launch: let the next kernel in the stream start its
 // prologue / wait until the previous kernel has completed and its writes are
 // visible.  Both are no-ops for a kernel launched without the attribute.

@@ -233,7 +233,7 @@ def _ptr(t):
 
 # 16-bit float patterns may travel as int16 or as the matching torch dtype
 _BITS16 = (torch.int16, torch.bfloat16, torch.float16)
-_ALIASES = {torch.int16: _BITS16, torch.bfloat16: (torch.bfloat16, torch.int16)}
+_ALIASES = {torch.int16: _BITS16}
 
 
 def _dev(t: torch.Tensor, dtype, name: str):
@@ -611,19 +611,44 @@ def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, p
 
 # ------------------------------------- page planning, rotary positions, block norms, 4-bit floats
 
-def _here(**tensors):
-    """Refuses tensors that are not on the current device, whose stream the calls go to."""
-    dev = torch._C._cuda_getDevice()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+_current_device = torch._C._cuda_getDevice
+_BF16, _F32, _I32, _U8 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,), (torch.uint8,)
 
 
-def _not_half(**tensors):
-    """Refuses f16 tensors, which the row checks take for bit patterns."""
-    for name, t in tensors.items():
-        if t.dtype is torch.float16:
-            raise ValueError(f"{name} must be bf16, got {t.dtype}")
+def _flat(t, n: int, dtypes, dev: int, name: str):
+    """Pointer of a contiguous tensor of n values on the current device, whose stream the calls go to; None
+    stays None.  (One test on the way through: these calls take a few microseconds, most of them here.)"""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.numel() == n and t.dtype in dtypes and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _heads(t, shape, dev: int, name: str):
+    """Pointer and token stride of bf16 [T][H][D] on the current device whose tokens may lie apart."""
+    if t.get_device() == dev and t.dtype in _BF16 and t.shape == shape:
+        ld, head, one = t.stride()
+        T, H, D = shape
+        if one == 1 and (head == D or H == 1):
+            return t.data_ptr(), ld if T > 1 else H * D
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype not in _BF16:
+        raise ValueError(f"{name} must be {_BF16[0]}, got {t.dtype}")
+    raise ValueError(f"{name} must be [T][H][D] with contiguous tokens, got {tuple(t.shape)}")
+
+
+def _space(ws, dev: int):
+    if ws.get_device() != dev:
+        raise ValueError("ws must be a CUDA tensor on the current device")
+    return ws.data_ptr(), ws.nbytes
 
 
 def kv_pages(kv_len: torch.Tensor, first: torch.Tensor, pages: torch.Tensor, free_pages: torch.Tensor,
@@ -633,9 +658,10 @@ def kv_pages(kv_len: torch.Tensor, first: torch.Tensor, pages: torch.Tensor, fre
     B = kv_len.numel()
     if pages.dim() != 2 or pages.shape[0] != B:
         raise ValueError("pages must be [B][max_pages]")
-    _here(kv_len=kv_len, first=first, pages=pages, free_pages=free_pages, n_free=n_free)
-    st = KvPages(_ints(kv_len, B, "kv_len"), _ints(first, B, "first"), _dev(pages, torch.int32, "pages"),
-                 _dev(free_pages, torch.int32, "free_pages"), _ints(n_free, 1, "n_free"))
+    dev = _current_device()
+    st = KvPages(_flat(kv_len, B, _I32, dev, "kv_len"), _flat(first, B, _I32, dev, "first"),
+                 _flat(pages, pages.numel(), _I32, dev, "pages"),
+                 _flat(free_pages, free_pages.numel(), _I32, dev, "free_pages"), _flat(n_free, 1, _I32, dev, "n_free"))
     st.sizes = (B, pages.shape[1], free_pages.numel())
     st.tensors = (kv_len, first, pages, free_pages, n_free)
     return st
@@ -649,10 +675,10 @@ def moe_kv_plan(new_len: torch.Tensor, dims: KvDims, state: KvPages, q_off: torc
     T, B = dims.T, dims.B
     if state.sizes is not None and state.sizes != (B, dims.max_pages, dims.n_pages):
         raise ValueError("the state's sizes are not those of dims")
-    _here(new_len=new_len, q_off=q_off, pos=pos, slots=slots, ws=ws)
+    dev = _current_device()
     status = (_lib or lib()).moe_kv_plan(
-        _ints(new_len, B, "new_len"), ctypes.byref(dims), ctypes.byref(state), _ints(q_off, B + 1, "q_off"),
-        _ints(pos, T, "pos"), _ints(slots, T, "slots"), ws.data_ptr(), ws.numel(), _stream(stream))
+        _flat(new_len, B, _I32, dev, "new_len"), dims, state, _flat(q_off, B + 1, _I32, dev, "q_off"),
+        _flat(pos, T, _I32, dev, "pos"), _flat(slots, T, _I32, dev, "slots"), *_space(ws, dev), _stream(stream))
     if status:
         raise MoeError(status, "moe_kv_plan")
 
@@ -661,9 +687,9 @@ def moe_rope_table(config: RopeConfig, pos0: int, table: torch.Tensor, stream=No
     """The rotary table fp32 [n_pos][rot] of positions pos0 on: cosines, then sines."""
     if table.dim() != 2 or table.shape[1] != config.rot:
         raise ValueError("table must be [n_pos][rot]")
-    _here(table=table)
-    status = (_lib or lib()).moe_rope_table(ctypes.byref(config), pos0, table.shape[0],
-                                            _dev(table, torch.float32, "table"), _stream(stream))
+    status = (_lib or lib()).moe_rope_table(config, pos0, table.shape[0],
+                                            _flat(table, table.numel(), _F32, _current_device(), "table"),
+                                            _stream(stream))
     if status:
         raise MoeError(status, "moe_rope_table")
 
@@ -674,14 +700,13 @@ def rope(table: torch.Tensor, flags: int = 0, q_norm: torch.Tensor | None = None
     heads' norms, if any.  The handle keeps them alive."""
     if table.dim() != 2:
         raise ValueError("table must be [n_pos][rot]")
-    _here(table=table, q_norm=q_norm, k_norm=k_norm)
     widths = {t.numel() for t in (q_norm, k_norm) if t is not None}
     if len(widths) > 1:
         raise ValueError("q_norm and k_norm must be [D]")
-    r = Rope(_dev(table, torch.float32, "table"), None if q_norm is None else _dev(q_norm, torch.float32, "q_norm"),
-             None if k_norm is None else _dev(k_norm, torch.float32, "k_norm"), table.shape[0], table.shape[1],
-             flags, eps)
-    r.D = widths.pop() if widths else None
+    D, dev = widths.pop() if widths else None, _current_device()
+    r = Rope(_flat(table, table.numel(), _F32, dev, "table"), _flat(q_norm, D, _F32, dev, "q_norm"),
+             _flat(k_norm, D, _F32, dev, "k_norm"), table.shape[0], table.shape[1], flags, eps)
+    r.D = D
     r.tensors = (table, q_norm, k_norm)
     return r
 
@@ -698,12 +723,10 @@ def moe_rope_rows(x: torch.Tensor, pos: torch.Tensor, rope: Rope, out: torch.Ten
         raise ValueError("x must be [T][H][D]")
     T, H, D = x.shape
     _rope_check(rope, D)
-    _here(x=x, pos=pos, out=out, ws=ws)
-    _not_half(x=x, out=out)
-    xp, ldx = _rows(x, T, H, D, "x")
-    op, ldo = _rows(out, T, H, D, "out")
-    status = (_lib or lib()).moe_rope_rows(xp, ldx, _ints(pos, T, "pos"), T, H, D, ctypes.byref(rope), op, ldo,
-                                           ws.data_ptr(), ws.numel(), _stream(stream))
+    dev = _current_device()
+    status = (_lib or lib()).moe_rope_rows(
+        *_heads(x, (T, H, D), dev, "x"), _flat(pos, T, _I32, dev, "pos"), T, H, D, rope,
+        *_heads(out, (T, H, D), dev, "out"), *_space(ws, dev), _stream(stream))
     if status:
         raise MoeError(status, "moe_rope_rows")
 
@@ -715,25 +738,13 @@ def moe_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: to
     T, H, D = dims.T, dims.H, dims.D
     _kv_check(dims, cache, dims.H_kv, D)
     _rope_check(rope, D)
-    _here(q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out, ws=ws)
-    _not_half(q=q, k=k, v=v, q_out=q_out)
-    qp, ldq = _rows(q, T, H, D, "q")
-    kp, ldk = _rows(k, T, dims.H_kv, D, "k")
-    vp, ldv = _rows(v, T, dims.H_kv, D, "v")
-    op, ldo = _rows(q_out, T, H, D, "q_out")
+    dev, wide, narrow = _current_device(), (T, H, D), (T, dims.H_kv, D)
     status = (_lib or lib()).moe_rope_kv_write(
-        qp, ldq, kp, ldk, vp, ldv, _ints(pos, T, "pos"), _ints(slots, T, "slots"), ctypes.byref(rope),
-        ctypes.byref(dims), ctypes.byref(cache), op, ldo, ws.data_ptr(), ws.numel(), _stream(stream))
+        *_heads(q, wide, dev, "q"), *_heads(k, narrow, dev, "k"), *_heads(v, narrow, dev, "v"),
+        _flat(pos, T, _I32, dev, "pos"), _flat(slots, T, _I32, dev, "slots"), rope, dims, cache,
+        *_heads(q_out, wide, dev, "q_out"), *_space(ws, dev), _stream(stream))
     if status:
         raise MoeError(status, "moe_rope_kv_write")
-
-
-def _sized(t: torch.Tensor | None, n: int, dtype, name: str):
-    if t is None:
-        return None
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
-    return _dev(t, dtype, name)
 
 
 def moe_block_norm(y: torch.Tensor | None, residual: torch.Tensor, gate: torch.Tensor | None,
@@ -742,15 +753,15 @@ def moe_block_norm(y: torch.Tensor | None, residual: torch.Tensor, gate: torch.T
     """residual_out = residual + scale * gate * norm(y) and x = norm(residual_out), each part where it
     is given: y, x bf16 [T][d], residual bf16 or fp32 (MOE_NORM_RESIDUAL_F32), the norms' weights fp32 [d],
     the gate by dims.gate.  residual_out may be residual and x may be y.  See include/moe.h."""
-    n, d = dims.T * dims.d, dims.d
-    res = torch.float32 if dims.flags & MOE_NORM_RESIDUAL_F32 else torch.bfloat16
-    size, kind = {MOE_GATE_TOKEN: (dims.T, torch.float32), MOE_GATE_CHANNEL: (d, torch.float32)}.get(
-        dims.gate, (n, torch.bfloat16))
-    _here(y=y, residual=residual, gate=gate, w_post=w_post, w_pre=w_pre, residual_out=residual_out, x=x)
+    T, d, kind, dev = dims.T, dims.d, dims.gate, _current_device()
+    n, res = T * d, _F32 if dims.flags & MOE_NORM_RESIDUAL_F32 else _BF16
+    if gate is not None:
+        gate = _flat(gate, T if kind == MOE_GATE_TOKEN else d if kind == MOE_GATE_CHANNEL else n,
+                     _F32 if kind in (MOE_GATE_TOKEN, MOE_GATE_CHANNEL) else _BF16, dev, "gate")
     status = (_lib or lib()).moe_block_norm(
-        _sized(y, n, torch.bfloat16, "y"), _sized(residual, n, res, "residual"), _sized(gate, size, kind, "gate"),
-        _sized(w_post, d, torch.float32, "w_post"), _sized(w_pre, d, torch.float32, "w_pre"), ctypes.byref(dims),
-        _sized(residual_out, n, res, "residual_out"), _sized(x, n, torch.bfloat16, "x"), _stream(stream))
+        _flat(y, n, _BF16, dev, "y"), _flat(residual, n, res, dev, "residual"), gate,
+        _flat(w_post, d, _F32, dev, "w_post"), _flat(w_pre, d, _F32, dev, "w_pre"), dims,
+        _flat(residual_out, n, res, dev, "residual_out"), _flat(x, n, _BF16, dev, "x"), _stream(stream))
     if status:
         raise MoeError(status, "moe_block_norm")
 
@@ -764,8 +775,8 @@ def fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor) -> Fp4:
     handle keeps them alive."""
     if q.dim() != 2 or s.numel() != q.shape[0] or b.numel() != moe_fp4_scale_bytes(q.shape[0], 2 * q.shape[1]):
         raise ValueError("q must be [rows][K/2], s [rows] and b moe_fp4_scale_bytes(rows, K) bytes")
-    _here(q=q, b=b, s=s)
-    w = Fp4(_dev(q, torch.uint8, "q"), _dev(b, torch.uint8, "b"), _dev(s, torch.float32, "s"))
+    dev = _current_device()
+    w = Fp4(_flat(q, q.numel(), _U8, dev, "q"), _flat(b, b.numel(), _U8, dev, "b"), _flat(s, s.numel(), _F32, dev, "s"))
     w.shape, w.tensors = (q.shape[0], 2 * q.shape[1]), (q, b, s)
     return w
 
@@ -781,16 +792,17 @@ def _fp4_out(x: torch.Tensor, q, b, s):
         b = torch.zeros(n, dtype=torch.uint8, device=x.device)
     if s is None:
         s = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _here(x=x, q=q, b=b, s=s)
-    return rows, K, q, b, s, (_sized(q, rows * (K // 2), torch.uint8, "q"), _sized(b, n, torch.uint8, "b"),
-                              _sized(s, rows, torch.float32, "s"))
+    dev = _current_device()
+    return rows, K, q, b, s, (_flat(q, rows * (K // 2), _U8, dev, "q"), _flat(b, n, _U8, dev, "b"),
+                              _flat(s, rows, _F32, dev, "s"))
 
 
 def moe_pack_fp4(w: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor | None = None,
                  s: torch.Tensor | None = None, stream=None):
     """fp32 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
     rows, K, q, b, s, to = _fp4_out(w, q, b, s)
-    _check((_lib or lib()).moe_pack_fp4(_dev(w, torch.float32, "w"), rows, K, *to, _stream(stream)), "moe_pack_fp4")
+    _check((_lib or lib()).moe_pack_fp4(_flat(w, rows * K, _F32, _current_device(), "w"), rows, K, *to, _stream(stream)),
+           "moe_pack_fp4")
     return q, b, s
 
 
@@ -798,8 +810,8 @@ def moe_quant_rows_fp4(x: torch.Tensor, q: torch.Tensor | None = None, b: torch.
                        s: torch.Tensor | None = None, stream=None):
     """bf16 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
     rows, K, q, b, s, to = _fp4_out(x, q, b, s)
-    _check((_lib or lib()).moe_quant_rows_fp4(_dev(x, torch.bfloat16, "x"), rows, K, *to, _stream(stream)),
-           "moe_quant_rows_fp4")
+    _check((_lib or lib()).moe_quant_rows_fp4(_flat(x, rows * K, _BF16, _current_device(), "x"), rows, K, *to,
+                                              _stream(stream)), "moe_quant_rows_fp4")
     return q, b, s
 
 
@@ -809,9 +821,8 @@ def moe_unpack_fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor, out: torch
     rows, K = w.shape
     if out is None:
         out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.device)
-    _here(out=out)
-    _check((_lib or lib()).moe_unpack_fp4(w, rows, K, _sized(out, rows * K, torch.bfloat16, "out"), _stream(stream)),
-           "moe_unpack_fp4")
+    _check((_lib or lib()).moe_unpack_fp4(w, rows, K, _flat(out, rows * K, _BF16, _current_device(), "out"),
+                                          _stream(stream)), "moe_unpack_fp4")
     return out
 
 
@@ -825,12 +836,14 @@ def moe_linear_fp4(x: torch.Tensor, w: Fp4, out: torch.Tensor, ws, stream=None):
     if w.shape is None:
         raise ValueError("w must come from fp4()")
     N, K = w.shape
-    if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1) or x.dtype not in _ALIASES[torch.bfloat16]:
-        raise ValueError("x must be bf16 [T][K] with contiguous tokens")
-    T = x.shape[0]
-    _here(x=x, out=out, ws=ws)
+    dev = _current_device()
+    if x.dim() != 2 or x.get_device() != dev or x.dtype not in _BF16:
+        raise ValueError("x must be a bf16 CUDA tensor [T][K] on the current device")
+    (T, width), (ld, one) = x.shape, x.stride()
+    if width != K or one != 1:
+        raise ValueError(f"x must be [T][{K}] with contiguous tokens, got {tuple(x.shape)}")
     status = (_lib or lib()).moe_linear_fp4(
-        x.data_ptr(), x.stride(0) if T > 1 else K, T, N, K, w, _sized(out, T * N, torch.bfloat16, "out"),
-        ws.data_ptr(), ws.numel(), _stream(stream))
+        x.data_ptr(), ld if T > 1 else K, T, N, K, w, _flat(out, T * N, _BF16, dev, "out"), *_space(ws, dev),
+        _stream(stream))
     if status:
         raise MoeError(status, "moe_linear_fp4")

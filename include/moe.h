@@ -840,7 +840,7 @@ size_t moe_linear_fp4_workspace_bytes(int32_t T, int32_t N, int32_t K);
  *   ws   moe_linear_fp4_workspace_bytes(T, N, K), zero-filled before its first
  *        use; calls of any sizes that fit leave it ready for the next.  Not one
  *        that other calls use.
- * N a multiple of 8, N < 2^24, T < 2^24. */
+ * N a multiple of 8, N < 2^24, T < 2^24, T * N < 2^40. */
 moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N, int32_t K,
                             moe_fp4_t w, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 

@@ -49,7 +49,7 @@ moe_status_t check_linear(int32_t T, int32_t N, int32_t K) {
     if (T < 0 || N <= 0) return MOE_ERR_INVALID_ARG;
     const moe_status_t st = check_fp4(N, K);
     if (st != MOE_OK) return st;
-    return N % 8 || N >= 1 << 24 || T >= 1 << 24 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+    return N % 8 || N >= 1 << 24 || T >= 1 << 24 || (int64_t)T * N >= (int64_t)1 << 40 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 moe_status_t quant(const void* src, bool bf16, int64_t rows, int64_t K, uint8_t* q, uint8_t* b, float* s,
@@ -136,10 +136,10 @@ moe_status_t moe_block_norm(const uint16_t* y, const void* residual, const void*
         !(std::isfinite(dims->eps) && dims->eps >= 0.0f) || !std::isfinite(dims->scale))
         return MOE_ERR_INVALID_ARG;
     if (dims->d % 8 || dims->d > 32768) return MOE_ERR_UNSUPPORTED;
+    if (dims->T == 0) return MOE_OK;
     if ((gate != nullptr) != (dims->gate != MOE_GATE_NONE) || (w_pre != nullptr) != (x != nullptr))
         return MOE_ERR_INVALID_ARG;
     if (!y && (gate || w_post || !w_pre)) return MOE_ERR_INVALID_ARG;
-    if (dims->T == 0) return MOE_OK;
     if (!act_ok_or_null(y) || !act_ok(residual) || !act_ok_or_null(w_post) || !act_ok_or_null(w_pre) ||
         !act_ok_or_null(x) || (y && !act_ok(residual_out)) ||
         (gate && !(dims->gate == MOE_GATE_TOKEN ? aligned4(gate) : act_ok(gate))))
@@ -182,12 +182,14 @@ moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N
     if (T == 0) return MOE_OK;
     if (!rows_ok(x, ldx, T, K) || !act_ok(w.q) || !act_ok(w.b) || !aligned4(w.s) || !act_ok(out))
         return MOE_ERR_INVALID_ARG;
+    if (gemv_fp4_takes(T, K))
+        return map_err(launch_gemv_fp4(x, ldx, w, T, N, K, out, static_cast<cudaStream_t>(stream)));
     uint8_t* base = static_cast<uint8_t*>(ws);
     const Fp4Rows xq{base + at.q, base + at.b, reinterpret_cast<float*>(base + at.s)};
     const cudaStream_t stm = static_cast<cudaStream_t>(stream);
     const cudaError_t err = launch_quant_fp4(x, true, ldx, T, K, xq, stm);
     if (err != cudaSuccess) return map_err(err);
-    return map_err(launch_linear_fp4(moe_fp4_t{xq.q, xq.b, xq.s}, w, T, N, K, out, ws, at, stm));
+    return map_err(launch_linear_fp4(moe_fp4_t{xq.q, xq.b, xq.s}, w, T, N, K, out, ws, stm));
 }
 
 }  // extern "C"

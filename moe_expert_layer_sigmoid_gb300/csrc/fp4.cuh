@@ -17,23 +17,13 @@ __host__ __device__ inline int64_t fp4_scale_at(int64_t r, int j, int K) {
     return ((r / kFp4TileRows) * (K / 64) + j / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4;
 }
 
-constexpr int kFp4Units = 152;  // parts of tiles at most where K is cut: one per SM
-
-// Tokens of a tile of moe_linear_fp4.
-int fp4_tile_tokens(int64_t T);
-
-// The workspace of moe_linear_fp4: the header, arrival counters of the tiles at a place that no size moves, the
-// parts' sums, the quantised activations.
+// Where moe_linear_fp4 keeps the quantised activations, behind the header.
 struct Fp4Ws {
-    size_t counters, parts, q, b, s, bytes;
+    size_t q, b, s, bytes;
 };
 inline Fp4Ws fp4_ws(int64_t T, int64_t K) {
     Fp4Ws w{};
     size_t off = sizeof(WsHeader);
-    w.counters = off;
-    off += align256(sizeof(int32_t) * kFp4Units);
-    w.parts = off;
-    off += align256(sizeof(float) * (size_t)kFp4Units * 128 * fp4_tile_tokens(T));
     w.q = off;
     off += align256((size_t)(T * (K / 2)));
     w.b = off;
@@ -53,7 +43,12 @@ struct Fp4Rows {
 cudaError_t launch_quant_fp4(const void* src, bool bf16, int64_t ld, int64_t rows, int64_t K, Fp4Rows out,
                              cudaStream_t st);
 cudaError_t launch_unpack_fp4(moe_fp4_t w, int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
+// The projection of few tokens, quantisation included.
+constexpr int kGemvFp4Tokens = 1;
+bool gemv_fp4_takes(int T, int K);
+cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, int N, int K, uint16_t* out,
+                            cudaStream_t st);
 cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws,
-                              const Fp4Ws& at, cudaStream_t st);
+                              cudaStream_t st);
 
 }  // namespace moe

@@ -5,12 +5,15 @@
 // Code products and block scales meet inside the product, so codes go from memory to the tensor core as they are
 // stored; the two row scales are applied once, to the finished sum.
 //
-// A tile is M = 128 weight rows by NT tokens, K in stages of 256 elements: 128 bytes of codes per row (TMA, 128-byte
-// swizzle) and, for each 128 rows and 64 elements, 512 bytes of scales, which lie in memory in the order
-// that tcgen05.cp spreads over TMEM (lane r % 32 and column r / 32 hold row r's four scales).  Four products of
-// K = 64 per stage.  NT is the smallest of 16, 32, 64, 128 that holds the tokens, so that few tokens do not pay for
-// many; what bounds few tokens is the weights' bytes.  They are spread over all SMs by cutting K, and the cuts' sums are
-// joined in a fixed order by the last CTA of a tile to arrive.
+// A tile has M = 128 rows of one operand and NT of the other, K in stages of 256 elements: 128 bytes of codes per
+// row (TMA, 128-byte swizzle) and, for each 128 rows and 64 elements, 512 bytes of scales, which lie in memory
+// in the order that tcgen05.cp spreads over TMEM (lane r % 32 and column r / 32 hold row r's four scales).  Four
+// products of K = 64 per stage.  Two forms:
+//  - narrow, for few tokens: M are weight rows, NT the smallest of 16, 32, 64 that holds the tokens.  What bounds it is
+//    the weights' bytes and the time until the first of them arrive; one tile per CTA, two CTAs on an SM.
+//  - wide: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row; CTAs walk the tiles.
+// Where the tiles are too few for the SMs, K is cut among the CTAs of a cluster, which add their sums in
+// the order of K through each other's shared memory.
 //
 // Warps: 0 copies, 1 allocates TMEM and issues the products, 2-9 the epilogue, two per quarter of TMEM's
 // lanes.  The scales of a stage have TMEM columns of their own, which are free when the stage's shared memory is.
@@ -21,41 +24,50 @@
 namespace moe {
 namespace {
 
-constexpr int kEpiWarps = 8, kEpiWarp0 = 2;
+constexpr int kEpiWarps = 8, kEpiWarp0 = 2, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kStageK = 256;           // elements of K per stage
 constexpr int kRowBytes = kStageK / 2;  // codes of a row per stage
 constexpr int kAtom = 512;             // scales of 128 rows and 64 elements
-constexpr int kTmemCols = 512;
+constexpr int kMaxSplits = 8;          // CTAs of a cluster
 
-template <int NT>
+template <int NT, bool WIDE>
 struct Shape {
-    static constexpr int kBlocks = (NT + 127) / 128;  // scale tiles of the tokens
+    static constexpr int kBlocks = (NT + 127) / 128;  // scale tiles of the NT rows
     static constexpr int kA = 128 * kRowBytes, kB = NT * kRowBytes;
     static constexpr int kSfA = 4 * kAtom, kSfB = 4 * kAtom * kBlocks;
     static constexpr int kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kStages = 216 * 1024 / kStage < 8 ? 216 * 1024 / kStage : 8;
-    static constexpr int kAcc = NT <= 128 ? 2 : 1;             // accumulators
-    static constexpr int kSfCols = 16 + 16 * kBlocks;          // TMEM columns of a stage's scales
+    static constexpr int kBudget = (WIDE ? 216 : 108) * 1024;
+    static constexpr int kStages = kBudget / kStage < 6 ? kBudget / kStage : 6;
+    static constexpr int kAcc = WIDE && NT <= 128 ? 2 : 1;  // accumulators
+    static constexpr int kSfCols = 16 + 16 * kBlocks;       // TMEM columns of a stage's scales
     static constexpr int kSfCol0 = kAcc * NT;
+    static constexpr int kTmemCols = WIDE ? 512 : 256;
     // FULL[stages], EMPTY[stages], AFULL[acc], AEMPTY[acc], TD (the products in flight at the end)
     static constexpr int kFull = 0, kEmpty = kStages, kAFull = 2 * kStages, kAEmpty = kAFull + kAcc, kTd = kAEmpty + kAcc;
     static constexpr int kBarAt = kStages * kStage;
     static constexpr int kMisc = kBarAt + 8 * (kTd + 1);
-    static constexpr int kSmem = kMisc + 16 + 1024;  // + alignment slack
-    static_assert(kSmem <= 227 * 1024 && kSfCol0 + kStages * kSfCols <= kTmemCols && kStage % 1024 == 0, "");
+    static constexpr int kScales = (kMisc + 16 + 15) / 16 * 16;  // row scales of the NT rows, two tiles' (wide)
+    static constexpr int kSmem = kScales + (WIDE ? 2 * NT * 4 : 0) + 1024;  // + alignment slack
+    static_assert(kSmem <= (WIDE ? 227 : 113) * 1024 && kSfCol0 + kStages * kSfCols <= kTmemCols && kStage % 1024 == 0,
+                  "");
+    static_assert(NT * 128 * 4 <= kStages * kStage, "a tile's sums fit where the stages were");
+};
+
+// One operand: rows of codes and their scales.
+struct Side {
+    CUtensorMap map;
+    const uint8_t* b;
+    const float* s;
+    int rows, tiles;  // tiles of 128 (M) or NT rows
 };
 
 struct LinearParams {
-    CUtensorMap tm_w, tm_x;
-    const uint8_t *wb, *xb;  // block scales
-    const float *ws, *xs;    // row scales
+    Side m, n;
     uint16_t* out;
     WsHeader* hdr;
-    int32_t* counters;  // arrivals per tile, 0 between calls
-    float* parts;       // sums of a unit's part of K, [unit][NT][128]
-    int T, N, K;
-    int m_tiles, tiles, splits;
+    int64_t ld;  // output channels, N of the call
+    int K, splits;
 };
 
 // Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, unsigned E4M3 scales, fp32 D, both K-major.
@@ -85,24 +97,66 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 }
 
 struct Unit {
-    int m, n;      // tile of weight rows, of tokens
-    int k0, k1;    // stages
+    int m, n;    // tiles of either side
+    int k0, k1;  // stages
 };
 __device__ __forceinline__ Unit unit_of(const LinearParams& p, int u) {
     const int tile = u / p.splits, s = u - tile * p.splits, all = (p.K + kStageK - 1) / kStageK;
     Unit r;
-    r.n = tile / p.m_tiles;
-    r.m = tile - r.n * p.m_tiles;
+    r.n = tile / p.m.tiles;
+    r.m = tile - r.n * p.m.tiles;
     r.k0 = (int)((int64_t)all * s / p.splits);
     r.k1 = (int)((int64_t)all * (s + 1) / p.splits);
     return r;
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of one's own shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
-    using S = Shape<NT>;
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One step of a transposition among lanes: with the lane whose number differs in bit BIT, a's half from the lane with
+// the bit clear stays or goes to the other's b.
+template <int BIT>
+__device__ __forceinline__ void trade(uint4& a, uint4& b, int lane) {
+    const bool up = lane & BIT;
+    const uint4 send = up ? a : b, keep = up ? b : a;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xFFFFFFFFu, send.x, BIT);
+    got.y = __shfl_xor_sync(0xFFFFFFFFu, send.y, BIT);
+    got.z = __shfl_xor_sync(0xFFFFFFFFu, send.z, BIT);
+    got.w = __shfl_xor_sync(0xFFFFFFFFu, send.w, BIT);
+    a = up ? got : keep;
+    b = up ? keep : got;
+}
+
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __grid_constant__ LinearParams p) {
+    using S = Shape<NT, WIDE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -111,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     auto bar = [&](int i) { return sbase + S::kBarAt + 8 * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
-    volatile int* last_here = reinterpret_cast<volatile int*>(smem + S::kMisc + 8);
+    float* scales = reinterpret_cast<float*>(smem + S::kScales);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -125,12 +179,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         mbar_init(bar(S::kTd), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_tmap(&p.tm_w);
-        prefetch_tmap(&p.tm_x);
+        prefetch_tmap(&p.m.map);
+        prefetch_tmap(&p.n.map);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols)
+                     "r"(S::kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -138,9 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int units = p.tiles * p.splits, grid = gridDim.x;
-    const int atoms = p.K / 64;                      // scale atoms of a row tile
-    const int x_blocks = (p.T + 127) / 128;          // row tiles of the tokens' scales
+    const int units = p.m.tiles * p.n.tiles * p.splits, grid = gridDim.x;
+    const int atoms = p.K / 64;                                    // scale atoms of a row tile
+    const int n_blocks = (p.n.rows + 127) / 128;                   // row tiles of the n side's scales
+    const bool once = !WIDE || p.splits > 1;                       // one unit per CTA: its sums go through shared memory
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
@@ -148,29 +203,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             const uint32_t withheld = withheld_stage(p.hdr);
             uint32_t it = 0;
             bool ok = true;
-            auto weights = [&](uint32_t i, const Unit& u, int ks) {
+            auto load_m = [&](uint32_t i, const Unit& u, int ks) {
                 const uint32_t at = sbase + (i % S::kStages) * S::kStage, full = bar(S::kFull + i % S::kStages);
                 const int nk = min(4, atoms - 4 * ks);
-                const int blocks = min(S::kBlocks, x_blocks - u.n * NT / 128);
-                mbar_expect_tx(full, S::kA + S::kB + nk * kAtom * (1 + blocks));
-                tma_load_2d(at, &p.tm_w, ks * kRowBytes, u.m * 128, full);
-                bulk_load(at + S::kA + S::kB, p.wb + ((int64_t)u.m * atoms + 4 * ks) * kAtom, nk * kAtom, full);
+                tma_load_2d(at, &p.m.map, ks * kRowBytes, u.m * 128, full);
+                bulk_load(at + S::kA + S::kB, p.m.b + ((int64_t)u.m * atoms + 4 * ks) * kAtom, nk * kAtom, full);
             };
-            auto tokens = [&](uint32_t i, const Unit& u, int ks) {
+            auto load_n = [&](uint32_t i, const Unit& u, int ks) {
                 const uint32_t at = sbase + (i % S::kStages) * S::kStage, full = bar(S::kFull + i % S::kStages);
                 const int nk = min(4, atoms - 4 * ks), first = u.n * NT / 128;
-                tma_load_2d(at + S::kA, &p.tm_x, ks * kRowBytes, u.n * NT, full);
-                for (int b = 0; b < min(S::kBlocks, x_blocks - first); ++b)
+                tma_load_2d(at + S::kA, &p.n.map, ks * kRowBytes, u.n * NT, full);
+                for (int b = 0; b < min(S::kBlocks, n_blocks - first); ++b)
                     bulk_load(at + S::kA + S::kB + S::kSfA + b * 4 * kAtom,
-                              p.xb + ((int64_t)(first + b) * atoms + 4 * ks) * kAtom, nk * kAtom, full);
+                              p.n.b + ((int64_t)(first + b) * atoms + 4 * ks) * kAtom, nk * kAtom, full);
+            };
+            auto expect = [&](uint32_t i, const Unit& u, int ks) {
+                const int nk = min(4, atoms - 4 * ks), blocks = min(S::kBlocks, n_blocks - u.n * NT / 128);
+                mbar_expect_tx(bar(S::kFull + i % S::kStages), S::kA + S::kB + nk * kAtom * (1 + blocks));
             };
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
             uint32_t ahead = 0;
             if ((int)blockIdx.x < units) {
                 const Unit u = unit_of(p, blockIdx.x);
                 ahead = min(S::kStages, u.k1 - u.k0);
-                for (uint32_t i = 0; i < ahead; ++i)
-                    if (i + 1 != withheld) weights(i, u, u.k0 + i);
+                for (uint32_t i = 0; i < ahead; ++i) {
+                    if (i + 1 == withheld) continue;
+                    expect(i, u, u.k0 + i);
+                    if (WIDE) load_n(i, u, u.k0 + i);
+                    else load_m(i, u, u.k0 + i);
+                }
             }
             pdl_wait();
             for (int n = blockIdx.x; n < units && ok; n += grid) {
@@ -182,8 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                         break;
                     }
                     if (it + 1 == withheld) continue;  // its FULL phase never completes
-                    if (it >= ahead) weights(it, u, ks);
-                    tokens(it, u, ks);
+                    if (it >= ahead) expect(it, u, ks);
+                    if (it >= ahead || WIDE) load_m(it, u, ks);
+                    if (it >= ahead || !WIDE) load_n(it, u, ks);
                 }
             }
             // do not leave with copies in flight (without an abort their phases are complete)
@@ -199,10 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         for (int n = blockIdx.x; n < units && ok; n += grid) {
             const Unit u = unit_of(p, n);
             const int b = tc % S::kAcc;
-            if (!warp_wait(bar(S::kAEmpty + b), ((tc / S::kAcc) & 1) ^ 1, abort_flag, p.hdr)) {
-                ok = false;
-                break;
-            }
+            if (!warp_wait(bar(S::kAEmpty + b), ((tc / S::kAcc) & 1) ^ 1, abort_flag, p.hdr)) break;
             tc_fence_after();
             const uint32_t d = tmem + b * NT;
             for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
@@ -245,33 +304,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         // After a failed wait every warp keeps walking the units without the work, so that none waits
         // at a barrier that the others left.
         constexpr int kChunk = NT < 32 ? NT : 32;
-        const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;
-        const int m = q * 32 + lane;
+        const int q = warp & 3, part = (warp - kEpiWarp0) >> 2, me = threadIdx.x - 32 * kEpiWarp0;
+        const int r = q * 32 + lane;  // row of the tile, TMEM lane
         bool ok = true;
         uint32_t tc = 0;
         pdl_wait();
         for (int n = blockIdx.x; n < units; n += grid, ++tc) {
             const Unit u = unit_of(p, n);
-            const int b = tc % S::kAcc, t0 = u.n * NT;
-            const int64_t row = (int64_t)u.m * 128 + m;  // output channel
-            const int cols = min(NT, p.T - t0);
-            if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
+            const int b = tc % S::kAcc;
+            const int64_t row = (int64_t)u.m * 128 + r, col0 = (int64_t)u.n * NT;
+            const int cols = (int)min((int64_t)NT, p.n.rows - col0);
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * NT;
-            const float sw = row < p.N ? __ldg(p.ws + row) : 0.0f;
-            auto finish = [&](const float (&v)[kChunk], int c0) {
-                const float mine = c0 + lane < cols && lane < kChunk ? __ldg(p.xs + t0 + c0 + lane) : 0.0f;
-                // Two tokens at a time: even lanes store the first one's pair of channels, odd lanes the second one's.
-#pragma unroll
-                for (int j = 0; j < kChunk; j += 2) {
-                    const float a = v[j] * __shfl_sync(0xFFFFFFFFu, mine, j) * sw;
-                    const float c = v[j + 1] * __shfl_sync(0xFFFFFFFFu, mine, j + 1) * sw;
-                    const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? a : c, 1);
-                    const __nv_bfloat162 o = lane & 1 ? __floats2bfloat162_rn(other, c) : __floats2bfloat162_rn(a, other);
-                    const int t = c0 + j + (lane & 1);
-                    if (t < cols && row < p.N)
-                        *reinterpret_cast<__nv_bfloat162*>(p.out + (int64_t)(t0 + t) * p.N + (row & ~1ll)) = o;
-                }
-            };
+            float* cs = scales + (tc & 1) * NT;
+            float rs = 0.0f;
+            if (!once) {
+                if (me < cols) cs[me] = __ldg(p.n.s + col0 + me);
+                if (row < p.m.rows) rs = __ldg(p.m.s + row);
+                epi_sync();
+            }
+            if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
             if (ok) {
                 tc_fence_after();
                 for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
@@ -283,57 +334,87 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                         tmem_ld_x32(acc + c0, v);
                         tmem_wait_ld32(v);
                     }
-                    float f[kChunk];
+                    if (once) {
+                        float* to = reinterpret_cast<float*>(smem) + c0 * 128 + r;
 #pragma unroll
-                    for (int j = 0; j < kChunk; ++j) f[j] = __uint_as_float(v[j]);
-                    if (p.splits == 1) {
-                        finish(f, c0);
-                    } else {
-                        float* to = p.parts + ((int64_t)n * NT + c0) * 128 + m;
+                        for (int j = 0; j < kChunk; ++j) to[j * 128] = __uint_as_float(v[j]);
+                    } else if constexpr (kChunk == 32) {
+                        // 64 bytes of a row each: four lanes trade pieces of 16, so that a store writes whole
+                        // sectors (a lane's own 16 bytes at a time cost twice the writes in L2)
+                        uint4 x[4];
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j)
-                            if (c0 + j < cols) to[j * 128] = f[j];
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 a = *reinterpret_cast<const float4*>(cs + c0 + 8 * j);
+                            const float4 c = *reinterpret_cast<const float4*>(cs + c0 + 8 * j + 4);
+                            auto f = [&](int i) { return __uint_as_float(v[8 * j + i]) * rs; };
+                            x[j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
+                                              pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
+                        }
+                        trade<1>(x[0], x[1], lane);
+                        trade<1>(x[2], x[3], lane);
+                        trade<2>(x[0], x[2], lane);
+                        trade<2>(x[1], x[3], lane);
+                        // x[i] is now piece lane % 4 of row lane / 4 * 4 + i
+                        const int c = c0 + 8 * (lane & 3);
+                        const int64_t first = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (first + i < p.m.rows && c < cols)
+                                *reinterpret_cast<uint4*>(p.out + (first + i) * p.ld + col0 + c) = x[i];
                     }
                 }
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
-            if (p.splits == 1) continue;
-            // the last CTA of the tile to arrive adds the parts, in the order of K
-            __threadfence();
-            epi_sync();
-            const int tile = n / p.splits;
-            if (threadIdx.x == 32 * kEpiWarp0) {
-                const int before = atomicAdd(p.counters + tile, 1);
-                *last_here = before == p.splits - 1;
-                if (*last_here) p.counters[tile] = 0;
-                __threadfence();
-            }
-            epi_sync();
-            if (*last_here) {
-                for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
-                    float f[kChunk];
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) f[j] = 0.0f;
-                    for (int s = 0; s < p.splits; ++s) {
-                        const float* from = p.parts + ((int64_t)(tile * p.splits + s) * NT + c0) * 128 + m;
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j)
-                            if (c0 + j < cols) f[j] += __ldcg(from + j * 128);
-                    }
-                    finish(f, c0);
-                }
-            }
-            epi_sync();  // (last_here has been read)
         }
     }
 
     tc_fence_before();
+    if (once) {
+        // Every warp's sums lie in shared memory as [NT][128]; the CTAs of a cluster share the adding and the stores.
+        if (p.splits > 1) cluster_sync();
+        else __syncthreads();
+        if (warp >= kEpiWarp0) {
+            const Unit u = unit_of(p, blockIdx.x);
+            const int64_t row0 = (int64_t)u.m * 128, col0 = (int64_t)u.n * NT;
+            const int rows = (int)min((int64_t)128, p.m.rows - row0), cols = (int)min((int64_t)NT, p.n.rows - col0);
+            const int rank = blockIdx.x % p.splits, me = threadIdx.x - 32 * kEpiWarp0;
+            // a thread takes 8 outputs that lie together: 8 rows of a column (narrow), 8 columns of a row (wide)
+            const int items = WIDE ? 128 * ((cols + 7) / 8) : 16 * cols;
+            for (int i = rank * kEpiThreads + me; i < items; i += p.splits * kEpiThreads) {
+                const int r = WIDE ? i % 128 : 8 * (i % 16), c = WIDE ? 8 * (i / 128) : i / 16;
+                if (r >= rows) continue;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                for (int s = 0; s < p.splits; ++s) {
+                    const uint32_t from = p.splits > 1 ? peer_addr(sbase, s) : sbase;
+                    if (WIDE) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += load_peer(from + 4 * ((c + j) * 128 + r));
+                    } else {
+                        const float4 a = load_peer4(from + 4 * (c * 128 + r)), b = load_peer4(from + 4 * (c * 128 + r) + 16);
+                        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                    }
+                }
+                const float own = __ldg(WIDE ? p.m.s + row0 + r : p.n.s + col0 + c);
+                const float* others = WIDE ? p.n.s + col0 + c : p.m.s + row0 + r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * own * __ldg(others + j);
+                uint16_t* to = p.out + (WIDE ? (row0 + r) * p.ld + col0 + c : (col0 + c) * p.ld + row0 + r);
+                *reinterpret_cast<uint4*>(to) =
+                    make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+            }
+        }
+        __syncwarp();
+        if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its sums
+    }
     __syncthreads();
     tc_fence_after();
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmemCols) : "memory");
 }
 
 bool codes_map(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t K, int box_rows) {
@@ -343,57 +424,64 @@ bool codes_map(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t K, int bo
     return make_map_nd(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NT>
-cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, cudaStream_t st) {
-    using S = Shape<NT>;
-    if (!codes_map(&p.tm_w, w.q, p.N, p.K, 128) || !codes_map(&p.tm_x, x.q, p.T, p.K, NT)) return cudaErrorInvalidValue;
-    cudaError_t err = ensure_dynamic_smem((const void*)linear_kernel<NT>, S::kSmem);
+bool make_side(Side& s, const moe_fp4_t& v, int rows, int K, int tile) {
+    s.b = v.b;
+    s.s = v.s;
+    s.rows = rows;
+    s.tiles = (rows + tile - 1) / tile;
+    return codes_map(&s.map, v.q, rows, K, tile);
+}
+
+template <int NT, bool WIDE>
+cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, int T, int N, cudaStream_t st) {
+    using S = Shape<NT, WIDE>;
+    if (!make_side(p.m, WIDE ? x : w, WIDE ? T : N, p.K, 128) || !make_side(p.n, WIDE ? w : x, WIDE ? N : T, p.K, NT))
+        return cudaErrorInvalidValue;
+    cudaError_t err = ensure_dynamic_smem((const void*)linear_kernel<NT, WIDE>, S::kSmem);
     if (err != cudaSuccess) return err;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    p.tiles = p.m_tiles * ((p.T + NT - 1) / NT);
-    const int stages = (p.K + kStageK - 1) / kStageK;
-    p.splits = std::max(1, std::min({kFp4Units / p.tiles, stages / 2, 16}));
+    const int tiles = p.m.tiles * p.n.tiles, stages = (p.K + kStageK - 1) / kStageK;
+    if (WIDE) {
+        p.splits = 1;
+        for (int s = 2; s <= kMaxSplits; s *= 2)
+            if (tiles * s <= (s == 2 ? sms : sms * 7 / 8) && stages >= 2 * s) p.splits = s;
+    } else {
+        p.splits = std::max(1, std::min({sms / tiles, stages / 2, kMaxSplits}));
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(std::min(p.tiles * p.splits, sms));
+    cfg.gridDim = dim3(WIDE && p.splits == 1 ? std::min(tiles, sms) : tiles * p.splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<NT>, p);
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<NT, WIDE>, p);
 }
 
 }  // namespace
 
-int fp4_tile_tokens(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256; }
-
-cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws, const Fp4Ws& at,
+cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws,
                               cudaStream_t st) {
-    uint8_t* base = static_cast<uint8_t*>(ws);
     LinearParams p{};
-    p.wb = w.b;
-    p.xb = x.b;
-    p.ws = w.s;
-    p.xs = x.s;
     p.out = out;
     p.hdr = static_cast<WsHeader*>(ws);
-    p.counters = reinterpret_cast<int32_t*>(base + at.counters);
-    p.parts = reinterpret_cast<float*>(base + at.parts);
-    p.T = T;
-    p.N = N;
+    p.ld = N;
     p.K = K;
-    p.m_tiles = (N + 127) / 128;
-    switch (fp4_tile_tokens(T)) {
-        case 16: return launch<16>(p, x, w, st);
-        case 32: return launch<32>(p, x, w, st);
-        case 64: return launch<64>(p, x, w, st);
-        case 128: return launch<128>(p, x, w, st);
-        default: return launch<256>(p, x, w, st);
-    }
+    if (T <= 16) return launch<16, false>(p, x, w, T, N, st);
+    if (T <= 32) return launch<32, false>(p, x, w, T, N, st);
+    if (T <= 64) return launch<64, false>(p, x, w, T, N, st);
+    const int m = (T + 127) / 128, sms = sm_count();
+    // the larger tile moves fewer bytes per product; the smaller one where the larger would leave SMs idle
+    const int64_t t128 = (int64_t)m * ((N + 127) / 128), t256 = (int64_t)m * ((N + 255) / 256);
+    const bool large = sms > 0 && (t256 + sms - 1) / sms * 12 <= (t128 + sms - 1) / sms * 8;
+    return large ? launch<256, true>(p, x, w, T, N, st) : launch<128, true>(p, x, w, T, N, st);
 }
 
 }  // namespace moe

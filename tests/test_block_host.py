@@ -209,7 +209,7 @@ def _linear(L, x=OK, ldx=128, T=4, N=256, K=128, q=OK, b=OK, s=OK, out=OK, ws=1 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(K=-64), INV), (dict(K=96), UNS), (dict(K=65600), UNS),
-    (dict(N=252), UNS), (dict(N=1 << 24), UNS), (dict(T=1 << 24), UNS), (dict(x=None), INV), (dict(x=BAD), INV),
+    (dict(N=252), UNS), (dict(N=1 << 24), UNS), (dict(T=1 << 24), UNS), (dict(T=1 << 20, N=1 << 20), UNS), (dict(x=None), INV), (dict(x=BAD), INV),
     (dict(ldx=120), INV), (dict(ldx=132), INV), (dict(q=None), INV), (dict(q=BAD), INV), (dict(b=BAD), INV),
     (dict(s=ODD), INV), (dict(s=None), INV), (dict(out=None), INV), (dict(out=BAD), INV), (dict(T=0, x=None, out=None), OK_),
 ])

@@ -323,50 +323,69 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 epi_sync();
             }
             if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
-            if (ok) {
-                tc_fence_after();
-                for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
-                    uint32_t v[kChunk];
-                    if constexpr (kChunk == 16) {
-                        tmem_ld_x16(acc + c0, v);
-                        tmem_wait_ld16(v);
-                    } else {
-                        tmem_ld_x32(acc + c0, v);
-                        tmem_wait_ld32(v);
-                    }
-                    if (once) {
+            if (once) {
+                if (ok) {
+                    tc_fence_after();
+                    for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
+                        uint32_t v[kChunk];
+                        if constexpr (kChunk == 16) {
+                            tmem_ld_x16(acc + c0, v);
+                            tmem_wait_ld16(v);
+                        } else {
+                            tmem_ld_x32(acc + c0, v);
+                            tmem_wait_ld32(v);
+                        }
                         float* to = reinterpret_cast<float*>(smem) + c0 * 128 + r;
 #pragma unroll
                         for (int j = 0; j < kChunk; ++j) to[j * 128] = __uint_as_float(v[j]);
-                    } else if constexpr (kChunk == 32) {
-                        // 64 bytes of a row each: four lanes trade pieces of 16, so that a store writes whole
-                        // sectors (a lane's own 16 bytes at a time cost twice the writes in L2)
-                        uint4 x[4];
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
+            } else if constexpr (WIDE) {
+                // All of a lane's outputs are packed first, so that the accumulator is free for the next tile's products while they
+                // are stored.  64 bytes of a row each: four lanes trade pieces of 16, so that a store writes whole sectors (a
+                // lane's own 16 bytes at a time cost twice the writes in L2).
+                constexpr int kRuns = NT / 64;
+                uint4 x[kRuns][4];
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k) {
+                        const int c0 = 32 * (2 * k + part);
+                        uint32_t v[32];
+                        tmem_ld_x32(acc + c0, v);
+                        tmem_wait_ld32(v);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float4 a = *reinterpret_cast<const float4*>(cs + c0 + 8 * j);
                             const float4 c = *reinterpret_cast<const float4*>(cs + c0 + 8 * j + 4);
                             auto f = [&](int i) { return __uint_as_float(v[8 * j + i]) * rs; };
-                            x[j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
-                                              pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
+                            x[k][j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
+                                                 pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
                         }
-                        trade<1>(x[0], x[1], lane);
-                        trade<1>(x[2], x[3], lane);
-                        trade<2>(x[0], x[2], lane);
-                        trade<2>(x[1], x[3], lane);
-                        // x[i] is now piece lane % 4 of row lane / 4 * 4 + i
-                        const int c = c0 + 8 * (lane & 3);
-                        const int64_t first = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (first + i < p.m.rows && c < cols)
-                                *reinterpret_cast<uint4*>(p.out + (first + i) * p.ld + col0 + c) = x[i];
                     }
+                    tc_fence_before();
                 }
-                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
+                if (!ok) continue;
+                const int64_t first = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k) {
+                    trade<1>(x[k][0], x[k][1], lane);
+                    trade<1>(x[k][2], x[k][3], lane);
+                    trade<2>(x[k][0], x[k][2], lane);
+                    trade<2>(x[k][1], x[k][3], lane);
+                    // x[k][i] is now piece lane % 4 of row lane / 4 * 4 + i
+                    const int c = 32 * (2 * k + part) + 8 * (lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (first + i < p.m.rows && c < cols)
+                            *reinterpret_cast<uint4*>(p.out + (first + i) * p.ld + col0 + c) = x[k][i];
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
         }
     }
 

@@ -182,7 +182,7 @@ moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N
     if (T == 0) return MOE_OK;
     if (!rows_ok(x, ldx, T, K) || !act_ok(w.q) || !act_ok(w.b) || !aligned4(w.s) || !act_ok(out))
         return MOE_ERR_INVALID_ARG;
-    if (gemv_fp4_takes(T, K))
+    if (gemv_fp4_takes(T, N, K))
         return map_err(launch_gemv_fp4(x, ldx, w, T, N, K, out, static_cast<cudaStream_t>(stream)));
     uint8_t* base = static_cast<uint8_t*>(ws);
     const Fp4Rows xq{base + at.q, base + at.b, reinterpret_cast<float*>(base + at.s)};

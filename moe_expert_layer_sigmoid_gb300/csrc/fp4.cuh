@@ -44,8 +44,7 @@ cudaError_t launch_quant_fp4(const void* src, bool bf16, int64_t ld, int64_t row
                              cudaStream_t st);
 cudaError_t launch_unpack_fp4(moe_fp4_t w, int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
 // The projection of few tokens, quantisation included.
-constexpr int kGemvFp4Tokens = 1;
-bool gemv_fp4_takes(int T, int K);
+bool gemv_fp4_takes(int T, int N, int K);
 cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, int N, int K, uint16_t* out,
                             cudaStream_t st);
 cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws,

@@ -1,14 +1,13 @@
-// Projections of one or a few tokens in microscaled 4-bit floats, on the CUDA cores: one launch, which quantises
-// the tokens too.
+// Projections of few tokens in microscaled 4-bit floats, on the CUDA cores: one launch, which quantises the tokens too.
 //
 // A warp takes the four weight rows whose block scales lie together (rows r, r + 32, r + 64, r + 96 of a scale tile:
 // 16 bytes hold their scales of 64 elements), a lane 64 elements of each at a time: 32 bytes of codes per row and those 16.
-// The weights are read once and wait for nothing; meanwhile every CTA quantises the tokens for itself, a block
-// of 16 to a thread, and keeps them as f16 values in shared memory.  Products of two codes are multiples of 1/4 of at most 36,
+// The weights are read once, a step ahead, the first without waiting for anything; meanwhile every CTA quantises the tokens for
+// itself, a block of 16 to a thread, and keeps them as f16 values in shared memory.  Products of two codes are multiples of 1/4 of at most 36,
 // so eight of them add up exactly in f16; a block's sum and its two scales meet in fp32.
 //
-// What bounds a call is the weights' bytes and the time until the first arrive: with four rows to a warp, all of a decode
-// step's projection is in flight at once.
+// What bounds a call is the weights' bytes and the time until the first arrive: with four rows to a warp and two steps on the
+// way, all of a decode step's projection is in flight at once.
 #include "fp4_dev.cuh"
 
 namespace moe {
@@ -22,13 +21,34 @@ struct GemvParams {
     int64_t ldx;
     moe_fp4_t w;
     uint16_t* out;
-    int N, K, parts;  // parts: warps that share four rows, each a part of K
+    int N, K;
+    int parts;  // warps that share four rows, each a part of K; above 1 only where a CTA's warps have one turn each
 };
 
-// Two codes as f16 values.  (By conversion: putting the bits in place by hand takes four operations and was 5% slower.)
-__device__ __forceinline__ __half2 code_pair(uint32_t byte) {
-    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)byte, __NV_E2M1);
-    return *reinterpret_cast<const __half2*>(&hr);
+// Eight codes as f16 values.  (By conversion: putting the bits in place by hand takes four operations for two codes and
+// was 5% slower.)
+__device__ __forceinline__ void values_of_8(uint32_t c, __half2 (&v)[4]) {
+    uint32_t u[4];
+    asm("{\n .reg .b8 p, q, r, s;\n mov.b32 {p, q, r, s}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, p;\n cvt.rn.f16x2.e2m1x2 %1, q;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, r;\n cvt.rn.f16x2.e2m1x2 %3, s;\n}"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const __half2*>(&u[i]);
+}
+// Four E4M3 scales as fp32.
+__device__ __forceinline__ void scales_of_4(uint32_t b, float (&f)[4]) {
+    uint32_t u[2];
+    asm("{\n .reg .b16 p, q;\n mov.b32 {p, q}, %2;\n cvt.rn.f16x2.e4m3x2 %0, p;\n cvt.rn.f16x2.e4m3x2 %1, q;\n}"
+        : "=r"(u[0]), "=r"(u[1])
+        : "r"(b));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
 }
 
 // A lane's weights of one step: 64 elements of four rows and their block scales.
@@ -42,34 +62,34 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const GemvParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part_max[T][kWarps], sums[T][4][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int atoms = p.K / 64;
+    const int atoms = p.K / 64, blocks = p.K / 16;
     float* bx = reinterpret_cast<float*>(smem + T * atoms * kAtomBytes);  // [T][K / 16] the tokens' block scales
-    // the warp's rows
-    const int64_t group = ((int64_t)blockIdx.x * kWarps + warp) / p.parts;
-    const int64_t tile = group / 32, r0 = tile * 128 + group % 32;
-    const int part = warp % p.parts;
-    auto load = [&](int a) {
+    // Turns: four rows (of which `parts` warps take a part of K each), 32 lanes' atoms at a time.  CTAs take neighbouring turns,
+    // so that every SM gets as many.
+    const int part = warp % p.parts, teams = kWarps / p.parts;
+    const int groups = (p.N + 127) / 128 * 32, stride = gridDim.x * teams;
+    int group = warp / p.parts * gridDim.x + blockIdx.x, a = part * 32 + lane;
+    auto load = [&](int group, int a) {
         Step s;
+        const int tile = group >> 5, r0 = tile * 128 + (group & 31);
+        const uint8_t* q = p.w.q + (int64_t)r0 * (p.K / 2) + 32 * a;
+        const bool live = group < groups && a < atoms;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + 32 * i;
-            const uint4* q = reinterpret_cast<const uint4*>(p.w.q + r * (p.K / 2) + 32 * a);
             s.q[i][0] = s.q[i][1] = make_uint4(0, 0, 0, 0);
-            if (r < p.N) {
-                s.q[i][0] = __ldg(q);
-                s.q[i][1] = __ldg(q + 1);
+            if (live && r0 + 32 * i < p.N) {
+                const uint4* from = reinterpret_cast<const uint4*>(q + (int64_t)i * 16 * p.K);
+                s.q[i][0] = __ldg(from);
+                s.q[i][1] = __ldg(from + 1);
             }
         }
-        s.b = __ldg(reinterpret_cast<const uint4*>(p.w.b + (tile * atoms + a) * 512 + group % 32 * 16));
+        s.b = make_uint4(0, 0, 0, 0);
+        if (live) s.b = __ldg(reinterpret_cast<const uint4*>(p.w.b + ((int64_t)tile * atoms + a) * 512 + (group & 31) * 16));
         return s;
     };
-    int a = part * 32 + lane;
-    const bool live = r0 < p.N;
-    Step now;
-    if (live && a < atoms) now = load(a);
+    Step now = load(group, a);
 
-    // the tokens: largest magnitudes first, then codes as the values they stand for
-    const int blocks = p.K / 16;
+    // the tokens: their largest magnitudes first, then codes as the values they stand for
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         float m = 0.0f;
@@ -87,9 +107,9 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const GemvParams p) {
     float sx[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        float m = 0.0f;
+        float m = part_max[t][0];
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) m = fmaxf(m, part_max[t][i]);
+        for (int i = 1; i < kWarps; ++i) m = fmaxf(m, part_max[t][i]);
         const RowScale row = row_scale(m);
         sx[t] = row.s;
         for (int j = threadIdx.x; j < blocks; j += kThreads) {
@@ -101,104 +121,116 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const GemvParams p) {
             uint2 c;
             const uint32_t b = quant_block<true>(f, top, row, c);
             bx[t * blocks + j] = e4m3_value(b);
-            __half2 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = code_pair((i < 4 ? c.x : c.y) >> (8 * (i & 3)) & 0xFFu);
+            __half2 v[2][4];
+            values_of_8(c.x, v[0]);
+            values_of_8(c.y, v[1]);
             uint4* to = reinterpret_cast<uint4*>(smem + (t * atoms + j / 4) * kAtomBytes + 32 * (j & 3));
-            to[0] = reinterpret_cast<const uint4*>(v)[0];
-            to[1] = reinterpret_cast<const uint4*>(v)[1];
+            to[0] = *reinterpret_cast<const uint4*>(v[0]);
+            to[1] = *reinterpret_cast<const uint4*>(v[1]);
         }
     }
     __syncthreads();
 
     float acc[T][4] = {};
-    while (live && a < atoms) {
-        const int next = a + 32 * p.parts;
-        Step then;
-        if (next < atoms) then = load(next);
+    while (group < groups) {
+        // the next step's weights are on the way while this one's are used
+        const int step = 32 * p.parts, last = a - lane + step >= atoms;  // (the same for the warp)
+        const int next_group = last ? group + stride : group, next_a = last ? part * 32 + lane : a + step;
+        const Step next = load(next_group, next_a);
+        if (a < atoms) {
+            float bw[4][4];
+            scales_of_4(now.b.x, bw[0]);
+            scales_of_4(now.b.y, bw[1]);
+            scales_of_4(now.b.z, bw[2]);
+            scales_of_4(now.b.w, bw[3]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // blocks of 16
-            __half2 w[4][8];
-            float bw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 q = now.q[i][j / 2];
-                const uint32_t lo = j & 1 ? q.z : q.x, hi = j & 1 ? q.w : q.y;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) w[i][n] = code_pair((n < 4 ? lo : hi) >> (8 * (n & 3)) & 0xFFu);
-                bw[i] = e4m3_value((i == 0 ? now.b.x : i == 1 ? now.b.y : i == 2 ? now.b.z : now.b.w) >> (8 * j) & 0xFFu);
-            }
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const uint4* from = reinterpret_cast<const uint4*>(smem + (t * atoms + a) * kAtomBytes + 32 * j);
-                const uint4 u[2] = {from[0], from[1]};
-                const __half2* v = reinterpret_cast<const __half2*>(u);
-                const float b = bx[t * blocks + 4 * a + j];
+            for (int j = 0; j < 4; ++j) {  // blocks of 16
+                __half2 w[4][2][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    __half2 s = __hmul2(w[i][0], v[0]);
+                    const uint4 q = now.q[i][j / 2];
+                    values_of_8(j & 1 ? q.z : q.x, w[i][0]);
+                    values_of_8(j & 1 ? q.w : q.y, w[i][1]);
+                }
 #pragma unroll
-                    for (int n = 1; n < 8; ++n) s = __hfma2(w[i][n], v[n], s);
-                    const float2 f = __half22float2(s);
-                    acc[t][i] += (f.x + f.y) * (b * bw[i]);
+                for (int t = 0; t < T; ++t) {
+                    const uint4* from = reinterpret_cast<const uint4*>(smem + (t * atoms + a) * kAtomBytes + 32 * j);
+                    const uint4 u[2] = {from[0], from[1]};
+                    const __half2* v = reinterpret_cast<const __half2*>(u);
+                    const float b = bx[t * blocks + 4 * a + j];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        __half2 s = __hmul2(w[i][0][0], v[0]);
+#pragma unroll
+                        for (int n = 1; n < 8; ++n) s = __hfma2(w[i][n / 4][n % 4], v[n], s);
+                        const float2 f = __half22float2(s);
+                        acc[t][i] += (f.x + f.y) * (b * bw[i][j]);
+                    }
                 }
             }
         }
-        now = then;
-        a = next;
-    }
+        if (last) {
+            const int64_t r = group / 32 * 128 + group % 32 + 32 * (lane & 3);
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+            for (int t = 0; t < T; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) acc[t][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[t][i], o);
-            if (lane == 0) sums[t][i][warp] = acc[t][i];
+                    for (int o = 16; o > 0; o >>= 1) acc[t][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[t][i], o);
+                const float v = lane == 0 ? acc[t][0] : lane == 1 ? acc[t][1] : lane == 2 ? acc[t][2] : acc[t][3];
+                if (p.parts > 1) {
+                    if (lane < 4) sums[t][lane][warp] = v;
+                } else if (lane < 4 && r < p.N) {
+                    p.out[(int64_t)t * p.N + r] = float_to_bf16_bits(v * sx[t] * __ldg(p.w.s + r));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+            }
         }
+        now = next;
+        group = next_group;
+        a = next_a;
+    }
+    if (p.parts == 1) return;
+    // the parts of K in order
     __syncthreads();
-    // one thread per output: warps' parts in order
-    const int per = kWarps / p.parts;  // groups of the CTA
-    if ((int)threadIdx.x < per * 4 * T) {
-        const int g = threadIdx.x % per, i = threadIdx.x / per % 4, t = threadIdx.x / (per * 4);
-        const int64_t gg = (int64_t)blockIdx.x * per + g, r = gg / 32 * 128 + gg % 32 + 32 * i;
-        if (r < p.N) {
-            float v = 0.0f;
-            for (int k = 0; k < p.parts; ++k) v += sums[t][i][g * p.parts + k];
-            float scale = sx[0];
+    const int team = threadIdx.x / 4, i = threadIdx.x % 4, mine = team * gridDim.x + blockIdx.x;
+    if (team < teams && mine < groups) {
+        const int64_t r = mine / 32 * 128 + mine % 32 + 32 * i;
 #pragma unroll
-            for (int n = 1; n < T; ++n) scale = t == n ? sx[n] : scale;
-            p.out[(int64_t)t * p.N + r] = float_to_bf16_bits(v * scale * __ldg(p.w.s + r));
+        for (int t = 0; t < T; ++t) {
+            float v = 0.0f;
+            for (int k = 0; k < p.parts; ++k) v += sums[t][i][team * p.parts + k];
+            if (r < p.N) p.out[(int64_t)t * p.N + r] = float_to_bf16_bits(v * sx[t] * __ldg(p.w.s + r));
         }
     }
 }
 
 template <int T>
-cudaError_t launch(const GemvParams& p, cudaStream_t st) {
+cudaError_t launch(GemvParams p, cudaStream_t st) {
     const size_t smem = (size_t)T * (p.K / 64 * kAtomBytes + p.K / 16 * 4);
-    cudaError_t err = ensure_dynamic_smem((const void*)gemv_kernel<T>, smem);
+    cudaError_t err = ensure_dynamic_smem((const void*)gemv_kernel<T>, smem + 1024);
     if (err != cudaSuccess) return err;
-    const int64_t groups = (int64_t)((p.N + 127) / 128) * 32;
-    gemv_kernel<T><<<(unsigned)((groups * p.parts + kWarps - 1) / kWarps), kThreads, smem, st>>>(p);
+    // Where the rows leave warps idle, several share one's K, as long as each has a step of 32 lanes.
+    const int groups = (p.N + 127) / 128 * 32, warps = sm_count() * 2 * kWarps;
+    while (p.parts < kWarps && groups * p.parts * 2 <= warps && p.K / 64 >= 64 * p.parts) p.parts *= 2;
+    gemv_kernel<T><<<std::min(groups, sm_count() * 2), kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// One token (2: 10.4 us against 9.0 for the tensor cores at N = 6144, K = 4096), and a row that fits shared memory as f16.
-bool gemv_fp4_takes(int T, int K) { return T <= kGemvFp4Tokens && T * K <= 16384; }
+// One token, or two on a weight of at most 2^25 elements, whose rows fit shared memory as f16.  Here and by the tensor cores,
+// quantisation included, us: one token, N = 6144, K = 4096 5.6, 8.5; N = 16384 9.4, 12.0; two tokens 8.6, 9.1 and 14.3, 12.0; three
+// at N = 6144 12.4, 9.1.
+bool gemv_fp4_takes(int T, int N, int K) {
+    return T <= 2 && T * K <= 32768 && (T == 1 || (int64_t)N * K <= 1 << 25);
+}
 
 cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, int N, int K, uint16_t* out,
                             cudaStream_t st) {
-    GemvParams p{x, ldx, w, out, N, K, 1};
-    // warps for every SM: rows that are too few are shared, as long as each warp has a step of 32 lanes
-    const int64_t groups = (int64_t)((N + 127) / 128) * 32;
-    while (p.parts < kWarps && groups * p.parts < (int64_t)sm_count() * kWarps && K / 64 >= 64 * p.parts) p.parts *= 2;
-    switch (T) {
-        case 1: return launch<1>(p, st);
-        case 2: return launch<2>(p, st);
-        case 3: return launch<3>(p, st);
-        default: return launch<4>(p, st);
-    }
+    const GemvParams p{x, ldx, w, out, N, K, 1};
+    return T == 1 ? launch<1>(p, st) : launch<2>(p, st);
 }
 
 }  // namespace moe

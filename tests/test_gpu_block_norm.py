@@ -120,6 +120,29 @@ def test_same_bits_every_time_and_beside_other_rows():
     assert torch.equal(r1[0], r[17]) and torch.equal(x1[0], x[17])
 
 
+def test_no_rows():
+    dims = moe.NormDims(T=0, d=256, gate=1, flags=0, eps=EPS, scale=1.0)
+    e = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, device="cuda")
+    moe.moe_block_norm(e, e, torch.empty(0, device="cuda"), w, w, dims, e, e)
+
+
+def test_captured_on_another_stream():
+    args = inputs(50, 4096, 2, True, True, False)
+    dims = moe.NormDims(T=50, d=4096, gate=2, flags=0, eps=EPS, scale=1.0)
+    r, x = run(args, dims)
+    r2, x2 = torch.zeros_like(r), torch.zeros_like(x)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        moe.moe_block_norm(*args, dims, r2, x2)
+    for _ in range(2):
+        r2.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r, r2) and torch.equal(x, x2)
+
+
 def test_the_binding_refuses():
     y, res, gate, w_post, w_pre = inputs(4, 256, 0, True, True, False)
     dims = moe.NormDims(T=4, d=256, gate=0, flags=0, eps=EPS, scale=1.0)

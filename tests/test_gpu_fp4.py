@@ -143,7 +143,7 @@ def check(out, x, w32):
 
 
 @pytest.mark.parametrize("T,N,K", [
-    (1, 8, 64), (1, 256, 128), (2, 136, 192), (3, 1000, 448), (7, 128, 4096), (15, 520, 1024), (16, 256, 2048), (17, 264, 320), (31, 136, 576),
+    (1, 8, 64), (1, 256, 128), (2, 136, 192), (2, 8200, 4160), (2, 6144, 4096), (1, 4104, 16448), (2, 72, 16448), (3, 1000, 448), (7, 128, 4096), (15, 520, 1024), (16, 256, 2048), (17, 264, 320), (31, 136, 576),
     (33, 384, 256), (64, 6144, 512), (100, 72, 1088), (127, 640, 640), (128, 128, 256), (129, 136, 64), (191, 1032, 832), (193, 256, 4160),
     (255, 504, 128), (257, 2048, 384), (500, 4096, 1024), (1000, 264, 8192), (2049, 1000, 320), (1, 40000, 64), (3, 8, 65536), (300, 8, 16448),
 ])
@@ -230,6 +230,32 @@ def test_captured_calls_and_two_streams(T):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 512, 4096), (20, 8192, 1024), (300, 512, 4096), (3000, 2048, 1024), (600, 4096, 512)])
+@pytest.mark.parametrize("stage", [1, 2])   # (a CTA of eight that share 16 stages has two)
+def test_a_wait_that_runs_out(T, N, K, stage):
+    """CTA 0 skips the copies of one stage: the call ends with the status, and the workspace serves the next call."""
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    w = moe.fp4(*moe.moe_pack_fp4(torch.randn(N, K, generator=torch.Generator().manual_seed(2)).cuda()))
+    ws = moe.workspace(moe.moe_linear_fp4_workspace_bytes(T, N, K))
+    out, want = (torch.zeros(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    moe.moe_linear_fp4(x, w, want, ws)
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK
+    moe.moe_debug_set_waits(ws, 1_000_000, stage)     # 1 ms: every other wait of these launches takes microseconds
+    moe.moe_linear_fp4(x, w, out, ws)
+    assert moe.moe_check_device_status(ws) == moe.MOE_ERR_DEVICE_CHECK
+    moe.moe_debug_set_waits(ws, 0, 0)
+    moe.moe_linear_fp4(x, w, out, ws)
+    assert moe.moe_check_device_status(ws) == moe.MOE_OK and torch.equal(out, want)
+
+
+def test_empty_calls():
+    w = moe.fp4(*moe.moe_pack_fp4(torch.randn(64, 128, device="cuda")))
+    x, out = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    moe.moe_linear_fp4(x, w, out, moe.workspace(256))
+    q, b, s = moe.moe_quant_rows_fp4(x)
+    assert q.shape == (0, 64) and b.numel() == 0 and s.numel() == 0
 
 
 def test_the_binding_refuses():

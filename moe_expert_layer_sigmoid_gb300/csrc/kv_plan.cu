@@ -2,9 +2,9 @@
 //
 // Three exclusive sums over the batch (pages given back, then tokens and pages of the
 // sequences that can be served) place everything; what follows is a copy of ids, and a
-// search in the sums for each token.  The bytes are few (8 per token): a call is a launch,
-// the sums' latency and, with many tokens, their search.  So it is one launch, of one CTA or of
-// one cluster whose CTAs all make the same sums (the batch's lengths are a few KB) and share
+// search in the sums for each token.  The bytes are few (8 per token): a call is a launch, the state's
+// latency and the sums' (3.5 us for 32 sequences and a token each).  So it is one launch, of one CTA or, where tokens are many,
+// of one cluster whose CTAs all make the same sums (the batch's lengths are a few KB) and share
 // the copies and the tokens: nothing is handed from one CTA to another but the state itself, behind
 // two cluster barriers.  No result depends on timing.
 #include "kv.cuh"
@@ -12,8 +12,8 @@
 namespace moe {
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 1024;  // of a CTA, at most
+constexpr int kRun = 4;            // neighbouring tokens of a thread
 
 struct PlanParams {
     const int32_t* new_len;
@@ -92,7 +92,7 @@ __device__ __forceinline__ Sums scan(Sums v, Sums* part, Sums& total) {
     __syncthreads();
     Sums before{0, 0, 0};
     total = before;
-    for (int w = 0; w < kPlanWarps; ++w) {
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
         const Sums t = part[w];
         if (w < warp) {
             before.a += t.a;
@@ -124,16 +124,22 @@ __device__ __forceinline__ void cluster_barrier() {
 
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams p) {
     extern __shared__ int32_t smem[];
-    __shared__ Sums part[kPlanWarps];
+    __shared__ Sums part[kPlanThreads / 32];
     int32_t* after = smem;             // [B] tokens before the new ones
-    int32_t* q_off = after + p.B;      // [B] first row (while summing: tokens asked for)
+    int32_t* held = after + p.B;       // [B] the first page held from now on
+    int32_t* q_off = held + p.B;       // [B] first row (while summing: tokens asked for)
     int32_t* given = q_off + p.B;      // [B] first of the new pages in the order of taking (pages asked for)
     int32_t* back = given + p.B;       // [B] first of the returned pages in their list
     int32_t* lo = back + p.B;          // [B] entry of that page
-    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
-    const bool chief = blockIdx.x == 0;
+    const int kept = p.st.n_free[0];
     int errors = 0;
+    // all CTAs' writes to the state visible to each other
+    auto barrier = [&]() {
+        __syncthreads();
+        if (gridDim.x > 1) cluster_barrier();
+    };
 
     Sums mine{0, 0, 0}, all;
     for (int b = b0; b < b1; ++b) {
@@ -141,6 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         const Step s = step_of(p, b, bad);
         if (bad) errors |= kErrBadSeq;
         after[b] = s.after;
+        held[b] = s.first;
         q_off[b] = s.want;
         given[b] = s.need;
         back[b] = s.hi - s.lo;
@@ -150,31 +157,34 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         mine.c += s.hi - s.lo;
     }
     Sums at = scan(mine, part, all);
-    const int kept = p.st.n_free[0];
     const int had = min(max(kept, 0), p.n_pages);
     const int returned = (int)min(all.c, (int64_t)(1 << 30));  // (of a state that is whole: at most n_pages)
     const int total = (int)min((int64_t)had + returned, (int64_t)p.n_pages);
     if (had != kept || had + (int64_t)returned > p.n_pages) errors |= kErrBadPage;
-    mine = Sums{0, 0, 0};
+    int64_t gone = at.c;
     for (int b = b0; b < b1; ++b) {
-        const int want = q_off[b], need = given[b], gone = back[b];
-        at.a += want;
-        at.b += need;
-        const bool fits = at.a <= p.T && (need == 0 || at.b <= total);
-        if (!fits) {
-            if (want) errors |= kErrNoRoom;
-            q_off[b] = given[b] = 0;
-        } else {
-            mine.a += want;
-            mine.b += need;
-        }
-        back[b] = (int)min(at.c, (int64_t)(1 << 30));
-        at.c += gone;
+        const int n = back[b];
+        back[b] = (int)min(gone, (int64_t)(1 << 30));
+        gone += n;
     }
-    at = scan(mine, part, all);
+    if (all.a > p.T || all.b > total) {
+        // not all can be served: those that can are summed anew
+        mine = Sums{0, 0, 0};
+        for (int b = b0; b < b1; ++b) {
+            const int want = q_off[b], need = given[b];
+            at.a += want;
+            at.b += need;
+            if (at.a <= p.T && (need == 0 || at.b <= total)) {
+                mine.a += want;
+                mine.b += need;
+            } else {
+                if (want) errors |= kErrNoRoom;
+                q_off[b] = given[b] = 0;
+            }
+        }
+        at = scan(mine, part, all);
+    }
     const int tokens = (int)all.a, taken = (int)all.b;
-    // Every CTA has read the state; now it changes.  (Entries that go back are read behind the barrier too, but
-    // each by the one thread that then clears it.)
     for (int b = b0; b < b1; ++b) {
         const int want = q_off[b], need = given[b];
         q_off[b] = (int)at.a;
@@ -182,10 +192,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         at.a += want;
         at.b += need;
     }
-    __syncthreads();
-    cluster_barrier();
+    // Every CTA has read the state; now it changes.  (Entries that go back are read behind the barrier too, but
+    // each by the one thread that then clears it.)
+    barrier();
 
-    const int threads = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + threadIdx.x;
+    const int threads = gridDim.x * blockDim.x, me = blockIdx.x * blockDim.x + threadIdx.x;
     for (int r = me; r < returned; r += threads) {
         const int b = find(back, p.B, r);
         int32_t* e = p.st.pages + (int64_t)b * p.max_pages + lo[b] + (r - back[b]);
@@ -193,14 +204,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         if (to < p.n_pages) p.st.free_pages[to] = *e;
         *e = -1;
     }
-    if (chief) {
-        for (int b = b0; b < b1; ++b) {
-            bool bad = false;
-            const Step s = step_of(p, b, bad);
-            const int next = b + 1 < p.B ? q_off[b + 1] : tokens;
-            p.q_off[b] = q_off[b];
-            p.st.kv_len[b] = s.after + (next - q_off[b]);
-            p.st.first[b] = s.first;
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const int row = q_off[b], next = b + 1 < p.B ? q_off[b + 1] : tokens;
+            p.q_off[b] = row;
+            p.st.kv_len[b] = after[b] + (next - row);
+            p.st.first[b] = held[b];
         }
         if (threadIdx.x == 0) {
             p.q_off[p.B] = tokens;
@@ -208,29 +217,54 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         }
         if (errors) record_error(p.hdr, errors);
     }
-    if (returned > 0) {
-        __syncthreads();
-        cluster_barrier();
-    }
+    if (returned > 0) barrier();
     for (int r = me; r < taken; r += threads) {
         const int b = find(given, p.B, r);
         p.st.pages[(int64_t)b * p.max_pages + pages_of(after[b], p.page_log2) + (r - given[b])] =
             p.st.free_pages[total - 1 - r];
     }
+    // Rows of tokens, a run of neighbours to a thread: one search, then along the sequences; ids are fetched together.
     const int mask = (1 << p.page_log2) - 1;
-    for (int t = me; t < p.T; t += threads) {
-        int pos = -1, slot = -1;
-        if (t < tokens) {
-            const int b = find(q_off, p.B, t);
-            pos = after[b] + (t - q_off[b]);
-            const int i = pos >> p.page_log2, fresh = i - pages_of(after[b], p.page_log2);
-            const int id = fresh < 0 ? p.st.pages[(int64_t)b * p.max_pages + i]
-                                     : p.st.free_pages[total - 1 - (given[b] + fresh)];
-            if ((unsigned)id < (unsigned)p.n_pages) slot = (id << p.page_log2) + (pos & mask);
-            else record_error(p.hdr, kErrBadPage);
+    const bool wide = (reinterpret_cast<uintptr_t>(p.pos) | reinterpret_cast<uintptr_t>(p.slots)) % 16 == 0;
+    for (int64_t t0 = (int64_t)me * kRun; t0 < p.T; t0 += (int64_t)threads * kRun) {
+        int pos[kRun], id[kRun], slot[kRun];
+        const int t = (int)t0;
+        int b = t < tokens ? find(q_off, p.B, t) : p.B, end = t < tokens ? (b + 1 < p.B ? q_off[b + 1] : tokens) : 0;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            pos[i] = -1;
+            const int32_t* from = p.st.n_free;  // (read for nothing where there is no token)
+            if (t + i < tokens) {
+                while (t + i >= end) {
+                    ++b;
+                    end = b + 1 < p.B ? q_off[b + 1] : tokens;
+                }
+                pos[i] = after[b] + (t + i - q_off[b]);
+                const int entry = pos[i] >> p.page_log2, fresh = entry - pages_of(after[b], p.page_log2);
+                from = fresh < 0 ? p.st.pages + (int64_t)b * p.max_pages + entry
+                                 : p.st.free_pages + (total - 1 - (given[b] + fresh));
+            }
+            id[i] = *from;
         }
-        p.pos[t] = pos;
-        p.slots[t] = slot;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            slot[i] = -1;
+            if (pos[i] >= 0) {
+                if ((unsigned)id[i] < (unsigned)p.n_pages) slot[i] = (id[i] << p.page_log2) + (pos[i] & mask);
+                else record_error(p.hdr, kErrBadPage);
+            }
+        }
+        if (wide && t0 + kRun <= p.T) {
+            *reinterpret_cast<int4*>(p.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i)
+                if (t0 + i < p.T) {
+                    p.pos[t0 + i] = pos[i];
+                    p.slots[t0 + i] = slot[i];
+                }
+        }
     }
 }
 
@@ -240,12 +274,15 @@ cudaError_t launch_kv_plan(const int32_t* new_len, const moe_kv_dims_t& d, const
                            int32_t* q_off, int32_t* pos, int32_t* slots, WsHeader* hdr, cudaStream_t stream) {
     const PlanParams p{new_len, st, q_off, pos, slots, hdr, d.T, d.B, __builtin_ctz(d.page), d.n_pages,
                        d.max_pages, d.window};
-    const size_t smem = 5 * sizeof(int32_t) * (size_t)d.B;
-    cudaError_t err = ensure_dynamic_smem((const void*)kv_plan_kernel, smem);
+    const size_t smem = 6 * sizeof(int32_t) * (size_t)d.B;
+    cudaError_t err = ensure_dynamic_smem((const void*)kv_plan_kernel, smem + 1024);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(d.T > 2 * kPlanThreads ? 8 : 1);
-    cfg.blockDim = dim3(kPlanThreads);
+    // One CTA, as large as the batch, or a cluster of eight where tokens are many (1 and 8 CTAs, us for two calls: 1600
+    // tokens of 8 sequences 8.6, 10.1; 4000 of 20 12.1, 10.4; 35000 of 60 56, 17.6).
+    const int rows = (d.T + kRun - 1) / kRun;
+    cfg.gridDim = dim3(rows > 512 ? 8 : 1);
+    cfg.blockDim = dim3(std::max(d.B, rows) <= 128 ? 128 : std::max(d.B, rows) <= 2048 ? 512 : kPlanThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at{};

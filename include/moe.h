@@ -702,7 +702,8 @@ moe_status_t moe_rope_table(const moe_rope_config_t* config, int32_t pos0, int32
 
 /* How rows are turned.  rot: multiple of 16, at most D.  q_norm, k_norm (fp32 [D],
    16-byte aligned, or NULL): each head x becomes x / sqrt(mean(x^2) + eps) * norm first,
-   in fp32; eps >= 0. */
+   in fp32; eps >= 0 (with 0, a head of zeros becomes NaN).  Heads whose squares add up
+   past the range of fp32 are outside what the norms are for. */
 typedef struct {
     const float* table;
     const float* q_norm;
@@ -782,8 +783,10 @@ typedef struct {
  *   w_pre        (device) fp32 [d] or NULL
  *   residual_out (device) out: like residual; may be residual itself
  *   x            (device) out: bf16 [T][d]; may be y itself; NULL exactly when w_pre is
- * All contiguous and 16-byte aligned (a MOE_GATE_TOKEN gate 4-byte).  Values whose
- * squares add up past the range of fp32 are outside what the norms are for. */
+ * All contiguous and 16-byte aligned (a MOE_GATE_TOKEN gate 4-byte); but for what is
+ * said above, outputs do not overlap inputs or each other.  With eps = 0 a row of
+ * zeros becomes NaN; values whose squares add up past the range of fp32 are outside
+ * what the norms are for. */
 moe_status_t moe_block_norm(const uint16_t* y, const void* residual, const void* gate,
                             const float* w_post, const float* w_pre, const moe_norm_dims_t* dims,
                             void* residual_out, uint16_t* x, void* stream);
@@ -837,10 +840,11 @@ size_t moe_linear_fp4_workspace_bytes(int32_t T, int32_t N, int32_t K);
  *   x    (device) bf16 [T][K], token t at x + t * ldx elements; 16-byte aligned,
  *        ldx a multiple of 8, at least K when T > 1
  *   w    weights of moe_pack_fp4, N rows
- *   out  (device) out: bf16 [T][N], contiguous, 16-byte aligned
+ *   out  (device) out: bf16 [T][N], contiguous, 16-byte aligned, apart from x
  *   ws   moe_linear_fp4_workspace_bytes(T, N, K), zero-filled before its first
- *        use; calls of any sizes that fit leave it ready for the next.  Not one
- *        that other calls use.
+ *        use; calls of any sizes that fit leave it ready for the next.  It holds the
+ *        tokens' codes, so calls that may overlap (two streams, two captured graphs)
+ *        take one each, and it is not one that other calls use
  * N a multiple of 8, N < 2^24, T < 2^24, T * N < 2^40. */
 moe_status_t moe_linear_fp4(const uint16_t* x, int64_t ldx, int32_t T, int32_t N, int32_t K,
                             moe_fp4_t w, uint16_t* out, void* ws, size_t ws_bytes, void* stream);

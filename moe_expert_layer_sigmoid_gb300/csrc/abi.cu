@@ -4,6 +4,7 @@
 // (moe_check_device_status excepted).
 #include <atomic>
 #include <mutex>
+#include <vector>
 
 #include "common.cuh"
 
@@ -89,25 +90,31 @@ int sm_count() {
 
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes) {
     if (bytes <= 48 * 1024) return cudaSuccess;
-    // per (kernel, device) once; a small table is enough for the handful of kernels
+    // per (kernel, device) its highest limit so far: a limit never goes down, so calls of several threads do not
+    // take it from each other
+    struct Entry {
+        const void* kernel;
+        int dev;
+        size_t bytes;
+    };
     static std::mutex mu;
-    static const void* seen_k[64];
-    static int seen_dev[64];
-    static size_t seen_bytes[64];
-    static int n_seen = 0;
+    static std::vector<Entry> seen;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n_seen; ++i)
-        if (seen_k[i] == kernel && seen_dev[i] == dev && seen_bytes[i] >= bytes) return cudaSuccess;
+    Entry* mine = nullptr;
+    for (Entry& e : seen)
+        if (e.kernel == kernel && e.dev == dev) mine = &e;
+    if (mine && mine->bytes >= bytes) return cudaSuccess;
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (err != cudaSuccess) return err;
-    if (n_seen < 64) {
-        seen_k[n_seen] = kernel;
-        seen_dev[n_seen] = dev;
-        seen_bytes[n_seen] = bytes;
-        ++n_seen;
+    if (mine) mine->bytes = bytes;
+    else {
+        try {
+            seen.push_back(Entry{kernel, dev, bytes});
+        } catch (...) {  // (no room to remember it: the next call sets it again)
+        }
     }
     return cudaSuccess;
 }

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(MAX) block_norm_kernel(const NormParams p, boo
     constexpr int E = 16 / sizeof(Res), GROUPS = ELEMS / E;
     using S = Slot<Res, GATE, GROUPS>;
     using Half = typename Bits<E>::T;
-    constexpr bool kKeep = RING && MAX <= 512 && ELEMS <= 16;  // the norms' weights stay in registers
+    constexpr bool kKeep = RING && MAX <= 640 && ELEMS <= 16;  // the norms' weights stay in registers
     extern __shared__ __align__(16) uint8_t ring[];            // [p.ahead + 1][parts][threads of the CTA]
     __shared__ float part[2][2][32];                           // by row, by norm
     const int threads = CTA ? blockDim.x : 32, me = CTA ? threadIdx.x : threadIdx.x & 31;
@@ -244,7 +244,9 @@ cudaError_t launch_gate(const NormParams& p, bool sigmoid, cudaStream_t st) {
     auto threads = [&](int elems) { return (p.d + 32 * elems - 1) / (32 * elems) * 32; };
     if (p.d <= 512) return launch_kernel<Res, GATE, false, 16, 256, true>(p, sigmoid, 256, st);
     if (p.d <= kWarpRow) return launch_kernel<Res, GATE, false, 32, 256, true>(p, sigmoid, 256, st);
-    if (p.d <= 8192) return launch_kernel<Res, GATE, true, 16, 512, true>(p, sigmoid, threads(16), st);
+    // (bounds for 640 threads: at most 102 registers, so that two CTAs of up to 320 threads fit an SM; with 106, 257 rows
+    // of 5000 took 5.9 us, with 102 4.3)
+    if (p.d <= 8192) return launch_kernel<Res, GATE, true, 16, 640, true>(p, sigmoid, threads(16), st);
     if (p.d <= 16384) {
         // (two rows of all there is in fp32 do not fit shared memory)
         constexpr bool kFits = 2 * Slot<Res, GATE, (int)sizeof(Res)>::kBytes * 1024 <= kRing;

@@ -220,11 +220,11 @@ cudaError_t launch(GemvParams p, cudaStream_t st) {
 
 }  // namespace
 
-// One token, or two on a weight of at most 2^25 elements, whose rows fit shared memory as f16.  Here and by the tensor cores,
-// quantisation included, us: one token, N = 6144, K = 4096 5.6, 8.5; N = 16384 9.4, 12.0; two tokens 8.6, 9.1 and 14.3, 12.0; three
-// at N = 6144 12.4, 9.1.
+// One token, or two on a weight of at most 2^24 elements, whose rows fit shared memory as f16.  Here and by the tensor cores,
+// quantisation included, us: one token, N = 6144, K = 4096 5.6, 8.2; N = 16384 9.4, 10.1; two tokens, N = 4096 7.3, 8.1; N = 6144
+// 8.6, 8.2; three at N = 6144 12.4, 8.2.
 bool gemv_fp4_takes(int T, int N, int K) {
-    return T <= 2 && T * K <= 32768 && (T == 1 || (int64_t)N * K <= 1 << 25);
+    return T <= 2 && T * K <= 32768 && (T == 1 || (int64_t)N * K <= 1 << 24);
 }
 
 cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, int N, int K, uint16_t* out,

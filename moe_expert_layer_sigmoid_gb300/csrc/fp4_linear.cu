@@ -461,13 +461,14 @@ cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, int 
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int tiles = p.m.tiles * p.n.tiles, stages = (p.K + kStageK - 1) / kStageK;
-    if (WIDE) {
-        p.splits = 1;
-        for (int s = 2; s <= kMaxSplits; s *= 2)
-            if (tiles * s <= (s == 2 ? sms : sms * 7 / 8) && stages >= 2 * s) p.splits = s;
-    } else {
-        p.splits = std::max(1, std::min({sms / tiles, stages / 2, kMaxSplits}));
-    }
+    // K is cut while CTAs find an SM: in pairs all of them do, in fours 144 of 152, in eights 120 (each GPC holds whole
+    // clusters; 16 of eight took twice the time of 8).  Narrow tiles are light enough for more CTAs than SMs, in fours at most, since joining costs more the more
+    // tokens there are (cuts of 1, 2, 3, 4 and 6, us: 16 tokens, N = 6144, K = 4096 11.7, 9.7, 9.5, 9.6, 15.9; N = 16384 12.3, 10.8, 17.6,
+    // 18.3, 26.7; 64 tokens, N = 6144 13.4, 10.8, 11.8, 11.8, 20.4).
+    p.splits = 1;
+    const int most = WIDE ? kMaxSplits : NT <= 32 ? 4 : 2;
+    for (int s = 2; s <= most; s *= 2)
+        if (tiles * s <= (!WIDE ? sms * 7 / 4 : s == 2 ? sms : s == 4 ? sms * 7 / 8 : sms * 3 / 4) && stages >= 2 * s) p.splits = s;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(WIDE && p.splits == 1 ? std::min(tiles, sms) : tiles * p.splits);
     cfg.blockDim = dim3(kThreads);

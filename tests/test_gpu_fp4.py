@@ -143,7 +143,7 @@ def check(out, x, w32):
 
 
 @pytest.mark.parametrize("T,N,K", [
-    (1, 8, 64), (1, 256, 128), (2, 136, 192), (2, 8200, 4160), (2, 6144, 4096), (1, 4104, 16448), (2, 72, 16448), (3, 1000, 448), (7, 128, 4096), (15, 520, 1024), (16, 256, 2048), (17, 264, 320), (31, 136, 576),
+    (1, 8, 64), (1, 256, 128), (2, 136, 192), (2, 8200, 4160), (2, 4096, 4096), (2, 6144, 4096), (256, 1024, 4096), (16, 16384, 1024), (1, 4104, 16448), (2, 72, 16448), (3, 1000, 448), (7, 128, 4096), (15, 520, 1024), (16, 256, 2048), (17, 264, 320), (31, 136, 576),
     (33, 384, 256), (64, 6144, 512), (100, 72, 1088), (127, 640, 640), (128, 128, 256), (129, 136, 64), (191, 1032, 832), (193, 256, 4160),
     (255, 504, 128), (257, 2048, 384), (500, 4096, 1024), (1000, 264, 8192), (2049, 1000, 320), (1, 40000, 64), (3, 8, 65536), (300, 8, 16448),
 ])

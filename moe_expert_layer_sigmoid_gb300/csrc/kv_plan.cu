@@ -73,10 +73,9 @@ struct Sums {
     int64_t a, b, c;
 };
 
-// Exclusive sums over the CTA's threads; `total` gets the sums of all.
-__device__ __forceinline__ Sums scan(Sums v, Sums* part, Sums& total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Sums x = v;
+// Inclusive sums over the warp's lanes.
+__device__ __forceinline__ Sums warp_sums(Sums x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t a = __shfl_up_sync(0xFFFFFFFFu, x.a, o), b = __shfl_up_sync(0xFFFFFFFFu, x.b, o),
@@ -87,23 +86,31 @@ __device__ __forceinline__ Sums scan(Sums v, Sums* part, Sums& total) {
             x.c += c;
         }
     }
+    return x;
+}
+__device__ __forceinline__ Sums of_lane(Sums x, int lane) {
+    return Sums{__shfl_sync(0xFFFFFFFFu, x.a, lane), __shfl_sync(0xFFFFFFFFu, x.b, lane),
+                __shfl_sync(0xFFFFFFFFu, x.c, lane)};
+}
+
+// Exclusive sums over the CTA's threads; `total` gets the sums of all.  (Each warp sums the warps' sums again, by lanes: one by
+// one they were half of a call for 500 sequences.)
+__device__ __forceinline__ Sums scan(Sums v, Sums* part, Sums& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const Sums x = warp_sums(v);
     __syncthreads();  // (the sums of an earlier scan have been read)
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    Sums before{0, 0, 0};
-    total = before;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-        const Sums t = part[w];
-        if (w < warp) {
-            before.a += t.a;
-            before.b += t.b;
-            before.c += t.c;
-        }
-        total.a += t.a;
-        total.b += t.b;
-        total.c += t.c;
+    const Sums all = warp_sums(lane < warps ? part[lane] : Sums{0, 0, 0});
+    total = of_lane(all, 31);
+    const Sums before = of_lane(all, max(warp - 1, 0));
+    Sums r{x.a - v.a, x.b - v.b, x.c - v.c};
+    if (warp > 0) {
+        r.a += before.a;
+        r.b += before.b;
+        r.c += before.c;
     }
-    return Sums{before.a + x.a - v.a, before.b + x.b - v.b, before.c + x.c - v.c};
+    return r;
 }
 
 // The last b of [0, B) with off[b] <= i, off ascending from 0.
@@ -279,7 +286,7 @@ cudaError_t launch_kv_plan(const int32_t* new_len, const moe_kv_dims_t& d, const
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
     // One CTA, as large as the batch, or a cluster of eight where tokens are many (1 and 8 CTAs, us for two calls: 1600
-    // tokens of 8 sequences 8.6, 10.1; 4000 of 20 12.1, 10.4; 35000 of 60 56, 17.6).
+    // tokens of 8 sequences 8.6, 10.1; 4000 of 20 12.1, 10.4; 35000 of 60 56, 15.5).
     const int rows = (d.T + kRun - 1) / kRun;
     cfg.gridDim = dim3(rows > 512 ? 8 : 1);
     cfg.blockDim = dim3(std::max(d.B, rows) <= 128 ? 128 : std::max(d.B, rows) <= 2048 ? 512 : kPlanThreads);

@@ -352,21 +352,27 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 // lane's own 16 bytes at a time cost twice the writes in L2).
                 constexpr int kRuns = NT / 64;
                 uint4 x[kRuns][4];
+                uint32_t v[2][32];
+                auto pack_run = [&](int k) {
+                    const int c0 = 32 * (2 * k + part);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 a = *reinterpret_cast<const float4*>(cs + c0 + 8 * j);
+                        const float4 c = *reinterpret_cast<const float4*>(cs + c0 + 8 * j + 4);
+                        auto f = [&](int i) { return __uint_as_float(v[k & 1][8 * j + i]) * rs; };
+                        x[k][j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
+                                             pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
+                    }
+                };
                 if (ok) {
                     tc_fence_after();
+                    tmem_ld_x32(acc + 32 * part, v[0]);
 #pragma unroll
                     for (int k = 0; k < kRuns; ++k) {
-                        const int c0 = 32 * (2 * k + part);
-                        uint32_t v[32];
-                        tmem_ld_x32(acc + c0, v);
-                        tmem_wait_ld32(v);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 a = *reinterpret_cast<const float4*>(cs + c0 + 8 * j);
-                            const float4 c = *reinterpret_cast<const float4*>(cs + c0 + 8 * j + 4);
-                            auto f = [&](int i) { return __uint_as_float(v[8 * j + i]) * rs; };
-                            x[k][j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
-                                                 pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
+                        tmem_wait_ld32(v[k & 1]);
+                        if (k + 1 < kRuns) {
+                            tmem_ld_x32(acc + 32 * (2 * k + 2 + part), v[(k + 1) & 1]);
+                            pack_run(k);
                         }
                     }
                     tc_fence_before();
@@ -374,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
                 if (!ok) continue;
+                pack_run(kRuns - 1);
                 const int64_t first = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
 #pragma unroll
                 for (int k = 0; k < kRuns; ++k) {

@@ -91,11 +91,14 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// 32 rows of 16 bytes of shared memory to four TMEM columns, in each quarter of the lanes.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 |
-                          (uint64_t)(128 >> 4) << 32 |  // 8 rows of 16 bytes to the next 8
-                          (uint64_t)1 << 46;            // version; no swizzle
+// Scales in shared memory: 32 rows of 16 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 |
+           (uint64_t)(128 >> 4) << 32 |  // 8 rows of 16 bytes to the next 8
+           (uint64_t)1 << 46;            // version; no swizzle
+}
+// They go to four TMEM columns, in each quarter of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
@@ -203,52 +206,79 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
+            // (One thread issues every copy of a stage: what it works out for each of them bounds the loop, so addresses are
+            // counted up.)
             const uint32_t withheld = withheld_stage(p.hdr);
+            const int last = (atoms + 3) / 4 - 1;  // the last stage of K, and its bytes of scales per 128 rows
+            const uint32_t last_bytes = (atoms - 4 * last) * kAtom;
             uint32_t it = 0;
             bool ok = true;
-            auto load_m = [&](uint32_t i, const Unit& u, int ks) {
-                const uint32_t at = sbase + (i % S::kStages) * S::kStage, full = bar(S::kFull + i % S::kStages);
-                const int nk = min(4, atoms - 4 * ks);
-                tma_load_2d(at, &p.m.map, ks * kRowBytes, u.m * 128, full);
-                bulk_load(at + S::kA + S::kB, p.m.b + ((int64_t)u.m * atoms + 4 * ks) * kAtom, nk * kAtom, full);
+            // where the unit's rows and scales are, and the copies of its stage ks
+            int y_m = 0, y_n = 0, blocks = 0;
+            const uint8_t *sf_m = nullptr, *sf_n = nullptr;
+            auto aim = [&](const Unit& u) {
+                const int first = u.n * NT / 128;
+                y_m = u.m * 128;
+                y_n = u.n * NT;
+                blocks = min(S::kBlocks, n_blocks - first);
+                sf_m = p.m.b + ((int64_t)u.m * atoms + 4 * u.k0) * kAtom;
+                sf_n = p.n.b + ((int64_t)first * atoms + 4 * u.k0) * kAtom;
             };
-            auto load_n = [&](uint32_t i, const Unit& u, int ks) {
-                const uint32_t at = sbase + (i % S::kStages) * S::kStage, full = bar(S::kFull + i % S::kStages);
-                const int nk = min(4, atoms - 4 * ks), first = u.n * NT / 128;
-                tma_load_2d(at + S::kA, &p.n.map, ks * kRowBytes, u.n * NT, full);
-                for (int b = 0; b < min(S::kBlocks, n_blocks - first); ++b)
-                    bulk_load(at + S::kA + S::kB + S::kSfA + b * 4 * kAtom,
-                              p.n.b + ((int64_t)(first + b) * atoms + 4 * ks) * kAtom, nk * kAtom, full);
+            const int64_t next_block = (int64_t)atoms * kAtom;
+            auto load_m = [&](uint32_t at, uint32_t full, int x, uint32_t bytes, const uint8_t* sf) {
+                tma_load_2d(at, &p.m.map, x, y_m, full);
+                bulk_load(at + S::kA + S::kB, sf, bytes, full);
             };
-            auto expect = [&](uint32_t i, const Unit& u, int ks) {
-                const int nk = min(4, atoms - 4 * ks), blocks = min(S::kBlocks, n_blocks - u.n * NT / 128);
-                mbar_expect_tx(bar(S::kFull + i % S::kStages), S::kA + S::kB + nk * kAtom * (1 + blocks));
+            auto load_n = [&](uint32_t at, uint32_t full, int x, uint32_t bytes, const uint8_t* sf) {
+                tma_load_2d(at + S::kA, &p.n.map, x, y_n, full);
+                bulk_load(at + S::kA + S::kB + S::kSfA, sf, bytes, full);
+                if (S::kBlocks == 2 && blocks == 2)
+                    bulk_load(at + S::kA + S::kB + S::kSfA + 4 * kAtom, sf + next_block, bytes, full);
             };
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
             uint32_t ahead = 0;
             if ((int)blockIdx.x < units) {
                 const Unit u = unit_of(p, blockIdx.x);
+                aim(u);
                 ahead = min(S::kStages, u.k1 - u.k0);
                 for (uint32_t i = 0; i < ahead; ++i) {
                     if (i + 1 == withheld) continue;
-                    expect(i, u, u.k0 + i);
-                    if (WIDE) load_n(i, u, u.k0 + i);
-                    else load_m(i, u, u.k0 + i);
+                    const uint32_t at = sbase + i * S::kStage, full = bar(S::kFull + i);
+                    const int ks = u.k0 + i;
+                    const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
+                    mbar_expect_tx(full, S::kA + S::kB + bytes * (1 + blocks));
+                    if (WIDE) load_n(at, full, ks * kRowBytes, bytes, sf_n + i * 4 * kAtom);
+                    else load_m(at, full, ks * kRowBytes, bytes, sf_m + i * 4 * kAtom);
                 }
             }
             pdl_wait();
+            uint32_t s = 0, parity = 1, at = sbase, full = bar(S::kFull);
             for (int n = blockIdx.x; n < units && ok; n += grid) {
                 const Unit u = unit_of(p, n);
+                aim(u);
+                int x = u.k0 * kRowBytes;
                 for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
-                    if (it >= ahead &&
-                        !mbar_wait(bar(S::kEmpty + it % S::kStages), ((it / S::kStages) & 1) ^ 1, abort_flag, p.hdr)) {
+                    if (it >= ahead && !mbar_wait(full + 8 * S::kStages, parity, abort_flag, p.hdr)) {  // (EMPTY)
                         ok = false;
                         break;
                     }
-                    if (it + 1 == withheld) continue;  // its FULL phase never completes
-                    if (it >= ahead) expect(it, u, ks);
-                    if (it >= ahead || WIDE) load_m(it, u, ks);
-                    if (it >= ahead || !WIDE) load_n(it, u, ks);
+                    if (it + 1 != withheld) {  // (else its FULL phase never completes)
+                        const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
+                        if (it >= ahead) mbar_expect_tx(full, S::kA + S::kB + bytes * (1 + blocks));
+                        if (it >= ahead || WIDE) load_m(at, full, x, bytes, sf_m);
+                        if (it >= ahead || !WIDE) load_n(at, full, x, bytes, sf_n);
+                    }
+                    x += kRowBytes;
+                    sf_m += 4 * kAtom;
+                    sf_n += 4 * kAtom;
+                    at += S::kStage;
+                    full += 8;
+                    if (++s == S::kStages) {
+                        s = 0;
+                        parity ^= 1;
+                        at = sbase;
+                        full = bar(S::kFull);
+                    }
                 }
             }
             // do not leave with copies in flight (without an abort their phases are complete)
@@ -259,7 +289,9 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         const uint32_t idesc = idesc_fp4(128, NT);
-        uint32_t it = 0, tc = 0;
+        const uint64_t ad0 = smem_desc_sw128(sbase), bd0 = smem_desc_sw128(sbase + S::kA);
+        const uint64_t sd0 = scale_desc(sbase + S::kA + S::kB);
+        uint32_t s = 0, parity = 0, tc = 0;
         bool ok = true;
         for (int n = blockIdx.x; n < units && ok; n += grid) {
             const Unit u = unit_of(p, n);
@@ -267,30 +299,38 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             if (!warp_wait(bar(S::kAEmpty + b), ((tc / S::kAcc) & 1) ^ 1, abort_flag, p.hdr)) break;
             tc_fence_after();
             const uint32_t d = tmem + b * NT;
-            for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
-                const int s = it % S::kStages;
-                if (!warp_wait(bar(S::kFull + s), (it / S::kStages) & 1, abort_flag, p.hdr)) {
+            for (int ks = u.k0; ks < u.k1; ++ks) {
+                if (!warp_wait(bar(S::kFull + s), parity, abort_flag, p.hdr)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t at = sbase + s * S::kStage, sf = at + S::kA + S::kB;
+                    // (the lower 14 bits of a descriptor count 16 bytes, and a CTA's shared memory does not pass them)
+                    const uint64_t off = s * (S::kStage / 16), ad = ad0 + off, bd = bd0 + off, sd = sd0 + off;
                     const uint32_t sfa = tmem + S::kSfCol0 + s * S::kSfCols, sfb = sfa + 16;
                     const int nk = min(4, atoms - 4 * ks);
-                    const uint64_t ad = smem_desc_sw128(at), bd = smem_desc_sw128(at + S::kA);
-                    for (int kk = 0; kk < nk; ++kk) {
-                        copy_scales(sfa + 4 * kk, sf + kk * kAtom);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk >= nk) break;
+                        copy_scales(sfa + 4 * kk, sd + kk * (kAtom / 16));
 #pragma unroll
                         for (int r = 0; r < S::kBlocks; ++r)
-                            copy_scales(sfb + 4 * (S::kBlocks * kk + r), sf + S::kSfA + (4 * r + kk) * kAtom);
+                            copy_scales(sfb + 4 * (S::kBlocks * kk + r), sd + (S::kSfA + (4 * r + kk) * kAtom) / 16);
                     }
-                    for (int kk = 0; kk < nk; ++kk)  // 32 bytes = 2 address units per step
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {  // 32 bytes = 2 address units per step
+                        if (kk >= nk) break;
                         mma_fp4(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * S::kBlocks * kk,
                                 ks > u.k0 || kk > 0);
+                    }
                     mma_commit(bar(S::kEmpty + s));
                 }
                 __syncwarp();
+                if (++s == S::kStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
             }
             if (!ok) break;
             if (elect_one()) mma_commit(bar(S::kAFull + b));

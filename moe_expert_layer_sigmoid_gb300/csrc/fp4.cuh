@@ -49,5 +49,6 @@ cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, 
                             cudaStream_t st);
 cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws,
                               cudaStream_t st);
+cudaError_t launch_pair_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uint16_t* out, void* ws, cudaStream_t st);
 
 }  // namespace moe

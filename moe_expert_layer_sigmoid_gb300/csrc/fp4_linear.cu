@@ -20,18 +20,13 @@
 //
 // Warps: 0 copies, 1 allocates TMEM and issues the products, 2-9 the epilogue, two per quarter of TMEM's
 // lanes.  The scales of a stage have TMEM columns of their own, which are free when the stage's shared memory is.
-#include "fp4.cuh"
-#include "tma.cuh"
-#include "umma.cuh"
+#include "fp4_mma.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kEpiWarps = 8, kEpiWarp0 = 2, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kStageK = 256;           // elements of K per stage
-constexpr int kRowBytes = kStageK / 2;  // codes of a row per stage
-constexpr int kAtom = 512;             // scales of 128 rows and 64 elements
 constexpr int kMaxSplits = 8;          // CTAs of a cluster
 
 template <int NT, bool WIDE>
@@ -57,14 +52,6 @@ struct Shape {
     static_assert(NT * 128 * 4 <= kStages * kStage, "a tile's sums fit where the stages were");
 };
 
-// One operand: rows of codes and their scales.
-struct Side {
-    CUtensorMap map;
-    const uint8_t* b;
-    const float* s;
-    int rows, tiles;  // tiles of 128 (M) or NT rows
-};
-
 struct LinearParams {
     Side m, n;
     uint16_t* out;
@@ -72,35 +59,6 @@ struct LinearParams {
     int64_t ld;  // output channels, N of the call
     int K, splits;
 };
-
-// Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, unsigned E4M3 scales, fp32 D, both K-major.
-__device__ __forceinline__ uint32_t idesc_fp4(int M, int N) {
-    return (1u << 7)                      // A format: E2M1
-           | (1u << 10)                   // B format: E2M1
-           | ((uint32_t)(N >> 3) << 17)   // N / 8
-           | ((uint32_t)(M >> 7) << 27);  // M / 128
-}
-
-// D (TMEM) (+)= A (shared memory) x B (shared memory) with scales in TMEM, K = 64.
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
-// Scales in shared memory: 32 rows of 16 bytes.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 |
-           (uint64_t)(128 >> 4) << 32 |  // 8 rows of 16 bytes to the next 8
-           (uint64_t)1 << 46;            // version; no swizzle
-}
-// They go to four TMEM columns, in each quarter of the lanes.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
 
 struct Unit {
     int m, n;    // tiles of either side
@@ -117,15 +75,6 @@ __device__ __forceinline__ Unit unit_of(const LinearParams& p, int u) {
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of one's own shared memory in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 __device__ __forceinline__ float4 load_peer4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -138,26 +87,6 @@ __device__ __forceinline__ float load_peer(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// One step of a transposition among lanes: with the lane whose number differs in bit BIT, a's half from the lane with
-// the bit clear stays or goes to the other's b.
-template <int BIT>
-__device__ __forceinline__ void trade(uint4& a, uint4& b, int lane) {
-    const bool up = lane & BIT;
-    const uint4 send = up ? a : b, keep = up ? b : a;
-    uint4 got;
-    got.x = __shfl_xor_sync(0xFFFFFFFFu, send.x, BIT);
-    got.y = __shfl_xor_sync(0xFFFFFFFFu, send.y, BIT);
-    got.z = __shfl_xor_sync(0xFFFFFFFFu, send.z, BIT);
-    got.w = __shfl_xor_sync(0xFFFFFFFFu, send.w, BIT);
-    a = up ? got : keep;
-    b = up ? keep : got;
 }
 
 template <int NT, bool WIDE>
@@ -313,15 +242,15 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= nk) break;
-                        copy_scales(sfa + 4 * kk, sd + kk * (kAtom / 16));
+                        copy_scales<1>(sfa + 4 * kk, sd + kk * (kAtom / 16));
 #pragma unroll
                         for (int r = 0; r < S::kBlocks; ++r)
-                            copy_scales(sfb + 4 * (S::kBlocks * kk + r), sd + (S::kSfA + (4 * r + kk) * kAtom) / 16);
+                            copy_scales<1>(sfb + 4 * (S::kBlocks * kk + r), sd + (S::kSfA + (4 * r + kk) * kAtom) / 16);
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {  // 32 bytes = 2 address units per step
                         if (kk >= nk) break;
-                        mma_fp4(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * S::kBlocks * kk,
+                        mma_fp4<1>(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * S::kBlocks * kk,
                                 ks > u.k0 || kk > 0);
                     }
                     mma_commit(bar(S::kEmpty + s));
@@ -363,9 +292,15 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             if (!once) {
                 if (me < cols) cs[me] = __ldg(p.n.s + col0 + me);
                 if (row < p.m.rows) rs = __ldg(p.m.s + row);
-                epi_sync();
             }
-            if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
+            // (one warp waits for all: waiting warps take turns of the shared memory that copies and products use)
+            if (warp == kEpiWarp0) {
+                if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
+                tc_fence_after();
+                tc_fence_before();
+            }
+            epi_sync();
+            if (ok) ok = !__any_sync(0xFFFFFFFFu, *abort_flag);
             if (once) {
                 if (ok) {
                     tc_fence_after();
@@ -421,20 +356,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
                 if (!ok) continue;
                 pack_run(kRuns - 1);
-                const int64_t first = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
-#pragma unroll
-                for (int k = 0; k < kRuns; ++k) {
-                    trade<1>(x[k][0], x[k][1], lane);
-                    trade<1>(x[k][2], x[k][3], lane);
-                    trade<2>(x[k][0], x[k][2], lane);
-                    trade<2>(x[k][1], x[k][3], lane);
-                    // x[k][i] is now piece lane % 4 of row lane / 4 * 4 + i
-                    const int c = 32 * (2 * k + part) + 8 * (lane & 3);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (first + i < p.m.rows && c < cols)
-                            *reinterpret_cast<uint4*>(p.out + (first + i) * p.ld + col0 + c) = x[k][i];
-                }
+                store_runs<kRuns>(x, p.out, p.ld, (int64_t)u.m * 128 + q * 32, p.m.rows, col0, cols, part, lane);
             }
         }
     }
@@ -484,21 +406,6 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmemCols) : "memory");
-}
-
-bool codes_map(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t K, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};
-    return make_map_nd(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-bool make_side(Side& s, const moe_fp4_t& v, int rows, int K, int tile) {
-    s.b = v.b;
-    s.s = v.s;
-    s.rows = rows;
-    s.tiles = (rows + tile - 1) / tile;
-    return codes_map(&s.map, v.q, rows, K, tile);
 }
 
 template <int NT, bool WIDE>
@@ -551,7 +458,8 @@ cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uin
     // the larger tile moves fewer bytes per product; the smaller one where the larger would leave SMs idle
     const int64_t t128 = (int64_t)m * ((N + 127) / 128), t256 = (int64_t)m * ((N + 255) / 256);
     const bool large = sms > 0 && (t256 + sms - 1) / sms * 12 <= (t128 + sms - 1) / sms * 8;
-    return large ? launch<256, true>(p, x, w, T, N, st) : launch<128, true>(p, x, w, T, N, st);
+    if (large) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
+    return launch<128, true>(p, x, w, T, N, st);
 }
 
 }  // namespace moe

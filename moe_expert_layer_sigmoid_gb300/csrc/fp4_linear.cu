@@ -12,9 +12,8 @@
 //  - narrow, for few tokens: M are weight rows, NT the smallest of 16, 32, 64 that holds the tokens; one tile per CTA.  What
 //    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 9.5 us with the
 //    quantisation's 1.9; the weights are 2.1 us of DRAM time).
-//  - wide: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row; CTAs walk the tiles.  What bounds
-//    it is what an SM takes in: a stage of 54 KB (NT = 256) takes 0.45 us, 0.41 without any product, the products
-//    themselves 0.2 (2048 tokens, N = 6144, K = 4096: 29.5 us and 5.4 for the quantisation, 2.9 PFLOP/s; K = N = 8192 3.6).
+//  - wide, NT = 128: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row; CTAs walk the tiles.
+// More tokens than wide tiles suit go to pairs of CTAs (launch_pair_fp4).
 // Where the tiles are too few for the SMs, K is cut among the CTAs of a cluster, which add their sums in
 // the order of K through each other's shared memory.
 //
@@ -31,14 +30,13 @@ constexpr int kMaxSplits = 8;          // CTAs of a cluster
 
 template <int NT, bool WIDE>
 struct Shape {
-    static constexpr int kBlocks = (NT + 127) / 128;  // scale tiles of the NT rows
     static constexpr int kA = 128 * kRowBytes, kB = NT * kRowBytes;
-    static constexpr int kSfA = 4 * kAtom, kSfB = 4 * kAtom * kBlocks;
+    static constexpr int kSfA = 4 * kAtom, kSfB = 4 * kAtom;
     static constexpr int kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kBudget = (WIDE ? 216 : 108) * 1024;
-    static constexpr int kStages = kBudget / kStage < 6 ? kBudget / kStage : 6;
-    static constexpr int kAcc = WIDE && NT <= 128 ? 2 : 1;  // accumulators
-    static constexpr int kSfCols = 16 + 16 * kBlocks;       // TMEM columns of a stage's scales
+    static constexpr int kRoom = (WIDE ? 216 : 108) * 1024;
+    static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
+    static constexpr int kAcc = WIDE ? 2 : 1;  // accumulators
+    static constexpr int kSfCols = 32;         // TMEM columns of a stage's scales
     static constexpr int kSfCol0 = kAcc * NT;
     static constexpr int kTmemCols = WIDE ? 512 : 256;
     // FULL[stages], EMPTY[stages], AFULL[acc], AEMPTY[acc], TD (the products in flight at the end)
@@ -129,7 +127,6 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     const uint32_t tmem = *tmem_slot;
     const int units = p.m.tiles * p.n.tiles * p.splits, grid = gridDim.x;
     const int atoms = p.K / 64;                                    // scale atoms of a row tile
-    const int n_blocks = (p.n.rows + 127) / 128;                   // row tiles of the n side's scales
     const bool once = !WIDE || p.splits > 1;                       // one unit per CTA: its sums go through shared memory
 
     if (warp == 0) {
@@ -143,17 +140,14 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             uint32_t it = 0;
             bool ok = true;
             // where the unit's rows and scales are, and the copies of its stage ks
-            int y_m = 0, y_n = 0, blocks = 0;
+            int y_m = 0, y_n = 0;
             const uint8_t *sf_m = nullptr, *sf_n = nullptr;
             auto aim = [&](const Unit& u) {
-                const int first = u.n * NT / 128;
                 y_m = u.m * 128;
                 y_n = u.n * NT;
-                blocks = min(S::kBlocks, n_blocks - first);
                 sf_m = p.m.b + ((int64_t)u.m * atoms + 4 * u.k0) * kAtom;
-                sf_n = p.n.b + ((int64_t)first * atoms + 4 * u.k0) * kAtom;
+                sf_n = p.n.b + ((int64_t)(y_n / 128) * atoms + 4 * u.k0) * kAtom;
             };
-            const int64_t next_block = (int64_t)atoms * kAtom;
             auto load_m = [&](uint32_t at, uint32_t full, int x, uint32_t bytes, const uint8_t* sf) {
                 tma_load_2d(at, &p.m.map, x, y_m, full);
                 bulk_load(at + S::kA + S::kB, sf, bytes, full);
@@ -161,8 +155,6 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             auto load_n = [&](uint32_t at, uint32_t full, int x, uint32_t bytes, const uint8_t* sf) {
                 tma_load_2d(at + S::kA, &p.n.map, x, y_n, full);
                 bulk_load(at + S::kA + S::kB + S::kSfA, sf, bytes, full);
-                if (S::kBlocks == 2 && blocks == 2)
-                    bulk_load(at + S::kA + S::kB + S::kSfA + 4 * kAtom, sf + next_block, bytes, full);
             };
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
             uint32_t ahead = 0;
@@ -175,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                     const uint32_t at = sbase + i * S::kStage, full = bar(S::kFull + i);
                     const int ks = u.k0 + i;
                     const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
-                    mbar_expect_tx(full, S::kA + S::kB + bytes * (1 + blocks));
+                    mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
                     if (WIDE) load_n(at, full, ks * kRowBytes, bytes, sf_n + i * 4 * kAtom);
                     else load_m(at, full, ks * kRowBytes, bytes, sf_m + i * 4 * kAtom);
                 }
@@ -193,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                     }
                     if (it + 1 != withheld) {  // (else its FULL phase never completes)
                         const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
-                        if (it >= ahead) mbar_expect_tx(full, S::kA + S::kB + bytes * (1 + blocks));
+                        if (it >= ahead) mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
                         if (it >= ahead || WIDE) load_m(at, full, x, bytes, sf_m);
                         if (it >= ahead || !WIDE) load_n(at, full, x, bytes, sf_n);
                     }
@@ -243,14 +235,12 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= nk) break;
                         copy_scales<1>(sfa + 4 * kk, sd + kk * (kAtom / 16));
-#pragma unroll
-                        for (int r = 0; r < S::kBlocks; ++r)
-                            copy_scales<1>(sfb + 4 * (S::kBlocks * kk + r), sd + (S::kSfA + (4 * r + kk) * kAtom) / 16);
+                        copy_scales<1>(sfb + 4 * kk, sd + (S::kSfA + kk * kAtom) / 16);
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {  // 32 bytes = 2 address units per step
                         if (kk >= nk) break;
-                        mma_fp4<1>(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * S::kBlocks * kk,
+                        mma_fp4<1>(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * kk,
                                 ks > u.k0 || kk > 0);
                     }
                     mma_commit(bar(S::kEmpty + s));
@@ -454,11 +444,11 @@ cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uin
     if (T <= 16) return launch<16, false>(p, x, w, T, N, st);
     if (T <= 32) return launch<32, false>(p, x, w, T, N, st);
     if (T <= 64) return launch<64, false>(p, x, w, T, N, st);
-    const int m = (T + 127) / 128, sms = sm_count();
-    // the larger tile moves fewer bytes per product; the smaller one where the larger would leave SMs idle
-    const int64_t t128 = (int64_t)m * ((N + 127) / 128), t256 = (int64_t)m * ((N + 255) / 256);
-    const bool large = sms > 0 && (t256 + sms - 1) / sms * 12 <= (t128 + sms - 1) / sms * 8;
-    if (large) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
+    // Wide tiles that find an SM each (or share K) are done soonest; where there are more of them, and K is long enough to pay for
+    // a pair's longer way in and out, the pairs' larger tiles move fewer bytes.  Wide, pairs, us without the quantisation: 256 tokens, N =
+    // 8192, K = 2048 7.2, 8.2; N = 16384, K = 512 6.2, 6.4; K = 1024 8.0, 7.3; K = 2048 10.5, 8.6; 2048 tokens, N = 6144, K = 4096 34, 25.
+    const int64_t tiles = (int64_t)((T + 127) / 128) * ((N + 127) / 128);
+    if (tiles > sm_count() && K >= 1024) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
     return launch<128, true>(p, x, w, T, N, st);
 }
 

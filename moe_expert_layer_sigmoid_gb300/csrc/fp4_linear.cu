@@ -312,41 +312,36 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
             } else if constexpr (WIDE) {
-                // All of a lane's outputs are packed first, so that the accumulator is free for the next tile's products while they
-                // are stored.  64 bytes of a row each: four lanes trade pieces of 16, so that a store writes whole sectors (a
-                // lane's own 16 bytes at a time cost twice the writes in L2).
+                // All of a lane's sums leave TMEM before they are packed and stored, so that the accumulator is free soonest.
                 constexpr int kRuns = NT / 64;
-                uint4 x[kRuns][4];
-                uint32_t v[2][32];
-                auto pack_run = [&](int k) {
-                    const int c0 = 32 * (2 * k + part);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 a = *reinterpret_cast<const float4*>(cs + c0 + 8 * j);
-                        const float4 c = *reinterpret_cast<const float4*>(cs + c0 + 8 * j + 4);
-                        auto f = [&](int i) { return __uint_as_float(v[k & 1][8 * j + i]) * rs; };
-                        x[k][j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
-                                             pack2(f(4) * c.x, f(5) * c.y), pack2(f(6) * c.z, f(7) * c.w));
-                    }
-                };
+                uint32_t v[kRuns][32];
                 if (ok) {
                     tc_fence_after();
-                    tmem_ld_x32(acc + 32 * part, v[0]);
 #pragma unroll
-                    for (int k = 0; k < kRuns; ++k) {
-                        tmem_wait_ld32(v[k & 1]);
-                        if (k + 1 < kRuns) {
-                            tmem_ld_x32(acc + 32 * (2 * k + 2 + part), v[(k + 1) & 1]);
-                            pack_run(k);
-                        }
-                    }
+                    for (int k = 0; k < kRuns; ++k) tmem_ld_x32(acc + 32 * (2 * k + part), v[k]);
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k) tmem_wait_ld32(v[k]);
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
                 if (!ok) continue;
-                pack_run(kRuns - 1);
-                store_runs<kRuns>(x, p.out, p.ld, (int64_t)u.m * 128 + q * 32, p.m.rows, col0, cols, part, lane);
+                const int64_t at = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
+                const int rows = (int)min((int64_t)4, p.m.rows - at), left = cols - 32 * part - 8 * (lane & 3);
+                uint16_t* to = p.out + at * p.ld + col0 + 32 * part + 8 * (lane & 3);
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k) {
+                    const float4* c = reinterpret_cast<const float4*>(cs + 32 * (2 * k + part));
+                    uint4 x[4];  // 32 outputs, packed
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 a = c[2 * j], e = c[2 * j + 1];
+                        auto f = [&](int i) { return __uint_as_float(v[k][8 * j + i]) * rs; };
+                        x[j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
+                                          pack2(f(4) * e.x, f(5) * e.y), pack2(f(6) * e.z, f(7) * e.w));
+                    }
+                    store_run(x, to + 64 * k, p.ld, rows, left - 64 * k, lane);
+                }
             }
         }
     }

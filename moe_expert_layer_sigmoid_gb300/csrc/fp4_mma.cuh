@@ -91,24 +91,18 @@ __device__ __forceinline__ void trade(uint4& a, uint4& b, int lane) {
     b = up ? keep : got;
 }
 
-// A warp's 32 rows from row0 on, lane by lane RUNS runs of 32 packed outputs, to columns 32 (2 k + part) of col0's tile.
-// Four lanes trade pieces of 16 bytes, so that a store writes whole sectors.
-template <int RUNS>
-__device__ __forceinline__ void store_runs(uint4 (&x)[RUNS][4], uint16_t* out, int64_t ld, int64_t row0, int64_t rows,
-                                           int64_t col0, int cols, int part, int lane) {
-    const int64_t first = row0 + (lane & ~3);
+// A lane's 32 packed outputs of its row, the warp's 32 rows below each other: four lanes trade pieces of 16 bytes, so that a store
+// writes whole sectors (a lane's own 16 bytes at a time cost twice the writes in L2).  `to`: where piece
+// lane % 4 of row lane / 4 * 4 belongs; from there on `rows` rows and `cols` columns are inside.
+__device__ __forceinline__ void store_run(uint4 (&x)[4], uint16_t* to, int64_t ld, int rows, int cols, int lane) {
+    trade<1>(x[0], x[1], lane);
+    trade<1>(x[2], x[3], lane);
+    trade<2>(x[0], x[2], lane);
+    trade<2>(x[1], x[3], lane);
+    // x[i] is now piece lane % 4 of row lane / 4 * 4 + i
 #pragma unroll
-    for (int k = 0; k < RUNS; ++k) {
-        trade<1>(x[k][0], x[k][1], lane);
-        trade<1>(x[k][2], x[k][3], lane);
-        trade<2>(x[k][0], x[k][2], lane);
-        trade<2>(x[k][1], x[k][3], lane);
-        // x[k][i] is now piece lane % 4 of row lane / 4 * 4 + i
-        const int c = 32 * (2 * k + part) + 8 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (first + i < rows && c < cols) *reinterpret_cast<uint4*>(out + (first + i) * ld + col0 + c) = x[k][i];
-    }
+    for (int i = 0; i < 4; ++i)
+        if (i < rows && cols > 0) *reinterpret_cast<uint4*>(to + i * ld) = x[i];
 }
 
 inline bool codes_map(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t K, int box_rows) {

@@ -253,36 +253,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             }
             asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
             if (ok) ok = !__any_sync(0xFFFFFFFFu, *abort_flag);
-            uint4 x[4][4];  // four runs of 32 outputs, packed
-            uint32_t v[2][32];
+            // Nearly all of a lane's sums leave TMEM before they are packed, so that the next tile's products wait the least; the
+            // last come while the first are packed, since registers hold no more.
+            uint32_t v[4][32];
+            uint4 x[4];  // 32 outputs, packed
             auto pack_run = [&](int k) {
                 const float4* c = reinterpret_cast<const float4*>(cs + 32 * (2 * k + part));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 a = c[2 * j], b = c[2 * j + 1];
-                    auto f = [&](int i) { return __uint_as_float(v[k & 1][8 * j + i]) * rs; };
-                    x[k][j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
-                                         pack2(f(4) * b.x, f(5) * b.y), pack2(f(6) * b.z, f(7) * b.w));
+                    auto f = [&](int i) { return __uint_as_float(v[k][8 * j + i]) * rs; };
+                    x[j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
+                                      pack2(f(4) * b.x, f(5) * b.y), pack2(f(6) * b.z, f(7) * b.w));
                 }
             };
             if (ok) {
                 tc_fence_after();
-                tmem_ld_x32(acc, v[0]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    tmem_wait_ld32(v[k & 1]);
-                    if (k < 3) {
-                        tmem_ld_x32(acc + 64 * (k + 1), v[(k + 1) & 1]);
-                        pack_run(k);
-                    }
-                }
+                for (int k = 0; k < 3; ++k) tmem_ld_x32(acc + 64 * k, v[k]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) tmem_wait_ld32(v[k]);
+                tmem_ld_x32(acc + 64 * 3, v[3]);
+                pack_run(0);
+                tmem_wait_ld32(v[3]);
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0) arrive_at(aempty);
             if (!ok) continue;
-            pack_run(3);
-            store_runs<4>(x, p.out, p.ld, row0, p.x.rows, col0, cols, part, lane);
+            const int64_t at = row0 + (lane & ~3);
+            const int rows = (int)min((int64_t)4, p.x.rows - at), left = cols - 32 * part - 8 * (lane & 3);
+            uint16_t* to = p.out + at * p.ld + col0 + 32 * part + 8 * (lane & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k > 0) pack_run(k);
+                store_run(x, to + 64 * k, p.ld, rows, left - 64 * k, lane);
+            }
         }
     }
 

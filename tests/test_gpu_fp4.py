@@ -154,6 +154,44 @@ def test_projection(T, N, K):
     check(project(x.cuda(), w, T, N, K), x, w)
 
 
+# More wide tiles (128 tokens by 128 rows) than SMs, and K from 1024 on: pairs of CTAs.  Halves of a tile without tokens or
+# weight rows, K that ends inside a stage, one and several tiles to a pair.
+@pytest.mark.parametrize("T,N,K", [
+    (2049, 1400, 1088), (257, 10248, 1024), (300, 8200, 1984), (1100, 2568, 1344), (385, 16392, 4160), (2000, 1416, 1152), (20000, 136, 1024), (129, 20000, 1216),
+])
+def test_projection_by_pairs(T, N, K):
+    g = torch.Generator().manual_seed(T + N + K)
+    x = rows_of(T, K, "outliers", seed=T).to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g) / math.sqrt(K)
+    buf = torch.full((T + 130, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    check(project(x.cuda(), w, T, N, K, out=buf[:T]), x, w)
+    assert (buf[T:] == 7).all()
+
+
+def test_pairs_captured_and_on_two_streams():
+    T, N, K = 1300, 2056, 1088
+    g = torch.Generator().manual_seed(8)
+    xs = [torch.randn(T, K + 8, generator=g).to(torch.bfloat16).cuda()[:, :K] for _ in range(2)]
+    w = torch.randn(N, K, generator=g)
+    handle = moe.fp4(*moe.moe_pack_fp4(w.cuda()))
+    want = [project(x, w, T, N, K) for x in xs]
+    assert all(torch.equal(a, project(x.contiguous(), w, T, N, K)) for a, x in zip(want, xs))
+    graphs = []
+    for x in xs:
+        graph, s, out = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        ws = moe.workspace(moe.moe_linear_fp4_workspace_bytes(T, N, K))
+        with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+            moe.moe_linear_fp4(x, handle, out, ws)
+        graphs.append((graph, s, out, ws))
+    for _ in range(10):
+        for graph, s, _, _ in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, _, out, ws), a in zip(graphs, want):
+        assert torch.equal(out, a) and moe.moe_check_device_status(ws) == moe.MOE_OK
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_projection_of_any_rows(T, kind):

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kEpiWarps = 8, kEpiWarp0 = 2, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kMaxSplits = 8;          // CTAs of a cluster
+constexpr int kMaxSplits = 8, kMaxNarrow = 4;  // CTAs of a cluster
 
 template <int NT, bool WIDE>
 struct Shape {
@@ -73,13 +73,11 @@ __device__ __forceinline__ Unit unit_of(const LinearParams& p, int u) {
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
-__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
-    float4 v;
+__device__ __forceinline__ void load_peer4(uint32_t addr, float* v) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                  : "r"(addr)
                  : "memory");
-    return v;
 }
 __device__ __forceinline__ float load_peer(uint32_t addr) {
     float v;
@@ -362,17 +360,32 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 const int r = WIDE ? i % 128 : 8 * (i % 16), c = WIDE ? 8 * (i / 128) : i / 16;
                 if (r >= rows) continue;
                 float v[8];
+                if constexpr (WIDE) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-                for (int s = 0; s < p.splits; ++s) {
-                    const uint32_t from = p.splits > 1 ? peer_addr(sbase, s) : sbase;
-                    if (WIDE) {
+                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                    for (int s = 0; s < p.splits; ++s) {
+                        const uint32_t from = p.splits > 1 ? peer_addr(sbase, s) : sbase;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] += load_peer(from + 4 * ((c + j) * 128 + r));
-                    } else {
-                        const float4 a = load_peer4(from + 4 * (c * 128 + r)), b = load_peer4(from + 4 * (c * 128 + r) + 16);
-                        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                    }
+                } else {
+                    // (every CTA's part is on the way before the first is added: 64 tokens, N = 6144, K = 4096 8.3 to 8.0 us; with
+                    // eight loads of the wide form for each it took longer)
+                    float part[kMaxNarrow][8];
+#pragma unroll
+                    for (int s = 0; s < kMaxNarrow; ++s) {
+                        if (s >= p.splits) break;
+                        const uint32_t from = (p.splits > 1 ? peer_addr(sbase, s) : sbase) + 4 * (c * 128 + r);
+                        load_peer4(from, part[s]);
+                        load_peer4(from + 16, part[s] + 4);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = part[0][j];
+#pragma unroll
+                    for (int s = 1; s < kMaxNarrow; ++s) {
+                        if (s >= p.splits) break;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += part[s][j];
                     }
                 }
                 const float own = __ldg(WIDE ? p.m.s + row0 + r : p.n.s + col0 + c);
@@ -408,7 +421,7 @@ cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, int 
     // tokens there are (cuts of 1, 2, 3, 4 and 6, us: 16 tokens, N = 6144, K = 4096 11.7, 9.7, 9.5, 9.6, 15.9; N = 16384 12.3, 10.8, 17.6,
     // 18.3, 26.7; 64 tokens, N = 6144 13.4, 10.8, 11.8, 11.8, 20.4).
     p.splits = 1;
-    const int most = WIDE ? kMaxSplits : NT <= 32 ? 4 : 2;
+    const int most = WIDE ? kMaxSplits : NT <= 32 ? kMaxNarrow : 2;
     for (int s = 2; s <= most; s *= 2)
         if (tiles * s <= (!WIDE ? sms * 7 / 4 : s == 2 ? sms : s == 4 ? sms * 7 / 8 : sms * 3 / 4) && stages >= 2 * s) p.splits = s;
     cudaLaunchConfig_t cfg{};

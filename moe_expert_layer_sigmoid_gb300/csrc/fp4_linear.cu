@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             }
         }
         __syncwarp();
-        if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its sums
+        if (p.splits > 1) cluster_meet();  // no CTA leaves while another reads its sums
     }
     __syncthreads();
     tc_fence_after();

@@ -64,6 +64,11 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without handing anything over: before a cluster's barriers are used, and before its CTAs leave.  (With release it
+// waits for the outputs' stores.)
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
 // The address of one's own shared memory in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;

@@ -103,7 +103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_meet();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int units = p.x.tiles * p.w.tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -311,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
     __syncthreads();
     if (threadIdx.x == 0) mbar_drain(bar(kTd), 0, p.hdr);
     __syncthreads();
-    cluster_sync();
+    cluster_meet();
     tc_fence_after();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

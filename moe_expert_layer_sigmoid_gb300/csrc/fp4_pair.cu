@@ -10,7 +10,7 @@
 // All of a stage's copies, of either CTA, are counted on one barrier of the leader (rank 0), which issues the products; their
 // completion frees the stage in both.
 //
-// Warps of each CTA: 0 copies codes, 10 scales; 1 allocates TMEM and, in the leader, issues the products; 2-9 the epilogue, two per quarter of
+// Warps of each CTA: 0, 10 and 11 copy; 1 allocates TMEM and, in the leader, issues the products; 2-9 the epilogue, two per quarter of
 // TMEM's lanes.
 #include "fp4_mma.cuh"
 
@@ -18,7 +18,8 @@ namespace moe {
 namespace {
 
 constexpr int kEpiWarps = 8, kEpiWarp0 = 2;
-constexpr int kScaleWarp = kEpiWarp0 + kEpiWarps, kThreads = 32 * (kScaleWarp + 1);
+constexpr int kCopyWarps = 3, kCopyWarp1 = kEpiWarp0 + kEpiWarps;  // warp 0 and those from kCopyWarp1 on
+constexpr int kThreads = 32 * (kCopyWarp1 + kCopyWarps - 1);
 constexpr int kTile = 256;                                 // tokens, and weight rows, of a pair's tile
 constexpr int kA = 128 * kRowBytes, kB = 128 * kRowBytes;  // a CTA's halves of a stage
 constexpr int kSfA = 4 * kAtom, kSfB = 8 * kAtom;          // scales of its tokens, of all weight rows
@@ -74,7 +75,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that a warp has one number: copies of three roles took 10% longer without)
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = blockIdx.x & 1;
     auto bar = [&](int i) { return sbase + kBarAt + 8 * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMisc);
@@ -82,7 +84,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bar(kFull + s), 2);
+            mbar_init(bar(kFull + s), kCopyWarps);
             mbar_init(bar(kEmpty + s), 1);
         }
         mbar_init(bar(kAFull), 1);
@@ -109,11 +111,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
     const int units = p.x.tiles * p.w.tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int atoms = p.K / 64, stages = (p.K + kStageK - 1) / kStageK;
 
-    if (warp == 0 || warp == kScaleWarp) {
+    if (warp == 0 || warp >= kCopyWarp1) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
-            // One thread copies codes, one scales: issuing a copy takes a thread some 60 ns, and four of them bounded the loop.
-            const bool codes = warp == 0;
+            // One thread copies the weight rows' codes, one the tokens', one the scales: issuing a copy takes a thread some 60 ns,
+            // and all four of a stage by one thread bounded the loop.
+            enum { kWeights, kTokens, kScaleTiles };
+            const int role = warp == 0 ? kWeights : warp == kCopyWarp1 ? kTokens : kScaleTiles;
             const uint32_t withheld = withheld_stage(p.hdr);
             const uint32_t full0 = peer_addr(bar(kFull), 0);  // in the leader
             uint32_t it = 0;
@@ -121,15 +125,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             int m = 0, n = 0;
             // K's last stage is filled up with zeros where K ends inside it, and rows past the last are zeros
             auto expect = [&](uint32_t i) {
-                if (rank == 0) mbar_expect_tx(bar(kFull) + 8 * i, codes ? 2 * (kA + kB) : 2 * (kSfA + kSfB));
+                if (rank == 0) mbar_expect_tx(bar(kFull) + 8 * i, role == kWeights ? 2 * kB : role == kTokens ? 2 * kA : 2 * (kSfA + kSfB));
             };
             auto weights = [&](uint32_t at, uint32_t full, int ks) {
-                if (codes) tma_load_2d_pair(at + kA, &p.w.codes, ks * kRowBytes, n * kTile + rank * 128, full);
-                else tma_load_2d_pair(at + kA + kB + kSfA, &p.w.scales, ks * (4 * kAtom / 8), 2 * n, full);
+                if (role == kWeights) tma_load_2d_pair(at + kA, &p.w.codes, ks * kRowBytes, n * kTile + rank * 128, full);
+                if (role == kScaleTiles)
+                    tma_load_2d_pair(at + kA + kB + kSfA, &p.w.scales, ks * (4 * kAtom / 8), 2 * n, full);
             };
             auto tokens = [&](uint32_t at, uint32_t full, int ks) {
-                if (codes) tma_load_2d_pair(at, &p.x.codes, ks * kRowBytes, m * kTile + rank * 128, full);
-                else tma_load_2d_pair(at + kA + kB, &p.x.scales, ks * (4 * kAtom / 8), 2 * m + rank, full);
+                if (role == kTokens) tma_load_2d_pair(at, &p.x.codes, ks * kRowBytes, m * kTile + rank * 128, full);
+                if (role == kScaleTiles)
+                    tma_load_2d_pair(at + kA + kB, &p.x.scales, ks * (4 * kAtom / 8), 2 * m + rank, full);
             };
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
             uint32_t ahead = 0;

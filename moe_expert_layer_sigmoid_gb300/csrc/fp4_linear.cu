@@ -12,8 +12,8 @@
 //  - narrow, for few tokens: M are weight rows, NT the smallest of 16, 32, 64 that holds the tokens; one tile per CTA.  What
 //    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 9.5 us with the
 //    quantisation's 1.9; the weights are 2.1 us of DRAM time).
-//  - wide, NT = 128: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row; CTAs walk the tiles.
-// More tokens than wide tiles suit go to pairs of CTAs (launch_pair_fp4).
+//  - wide, NT = 128: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row.
+// A CTA has one tile.  Where wide tiles are more than SMs, pairs of CTAs take over (launch_pair_fp4).
 // Where the tiles are too few for the SMs, K is cut among the CTAs of a cluster, which add their sums in
 // the order of K through each other's shared memory.
 //
@@ -35,16 +35,15 @@ struct Shape {
     static constexpr int kStage = kA + kB + kSfA + kSfB;
     static constexpr int kRoom = (WIDE ? 216 : 108) * 1024;
     static constexpr int kStages = kRoom / kStage < 6 ? kRoom / kStage : 6;
-    static constexpr int kAcc = WIDE ? 2 : 1;  // accumulators
-    static constexpr int kSfCols = 32;         // TMEM columns of a stage's scales
-    static constexpr int kSfCol0 = kAcc * NT;
+    static constexpr int kSfCols = 32;  // TMEM columns of a stage's scales
+    static constexpr int kSfCol0 = NT;
     static constexpr int kTmemCols = WIDE ? 512 : 256;
-    // FULL[stages], EMPTY[stages], AFULL[acc], AEMPTY[acc], TD (the products in flight at the end)
-    static constexpr int kFull = 0, kEmpty = kStages, kAFull = 2 * kStages, kAEmpty = kAFull + kAcc, kTd = kAEmpty + kAcc;
+    // FULL[stages], EMPTY[stages], AFULL (the tile's products are done), TD (those in flight at the end are)
+    static constexpr int kFull = 0, kEmpty = kStages, kAFull = 2 * kStages, kTd = kAFull + 1;
     static constexpr int kBarAt = kStages * kStage;
     static constexpr int kMisc = kBarAt + 8 * (kTd + 1);
-    static constexpr int kScales = (kMisc + 16 + 15) / 16 * 16;  // row scales of the NT rows, two tiles' (wide)
-    static constexpr int kSmem = kScales + (WIDE ? 2 * NT * 4 : 0) + 1024;  // + alignment slack
+    static constexpr int kScales = (kMisc + 16 + 15) / 16 * 16;  // row scales of the NT rows (wide)
+    static constexpr int kSmem = kScales + (WIDE ? NT * 4 : 0) + 1024;  // + alignment slack
     static_assert(kSmem <= (WIDE ? 227 : 113) * 1024 && kSfCol0 + kStages * kSfCols <= kTmemCols && kStage % 1024 == 0,
                   "");
     static_assert(NT * 128 * 4 <= kStages * kStage, "a tile's sums fit where the stages were");
@@ -97,17 +96,13 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     auto bar = [&](int i) { return sbase + S::kBarAt + 8 * i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
-    float* scales = reinterpret_cast<float*>(smem + S::kScales);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(bar(S::kFull + s), 1);
             mbar_init(bar(S::kEmpty + s), 1);
         }
-        for (int b = 0; b < S::kAcc; ++b) {
-            mbar_init(bar(S::kAFull + b), 1);
-            mbar_init(bar(S::kAEmpty + b), kEpiWarps);
-        }
+        mbar_init(bar(S::kAFull), 1);
         mbar_init(bar(S::kTd), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -124,9 +119,9 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int units = p.m.tiles * p.n.tiles * p.splits, grid = gridDim.x;
-    const int atoms = p.K / 64;                                    // scale atoms of a row tile
-    const bool once = !WIDE || p.splits > 1;                       // one unit per CTA: its sums go through shared memory
+    const int atoms = p.K / 64;  // scale atoms of a row tile
+    const Unit u = unit_of(p, blockIdx.x);
+    const bool shared = !WIDE || p.splits > 1;  // sums go through shared memory
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
@@ -137,16 +132,10 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
             const int last = (atoms + 3) / 4 - 1;  // the last stage of K, and its bytes of scales per 128 rows
             const uint32_t last_bytes = (atoms - 4 * last) * kAtom;
             uint32_t it = 0;
-            bool ok = true;
-            // where the unit's rows and scales are, and the copies of its stage ks
-            int y_m = 0, y_n = 0;
-            const uint8_t *sf_m = nullptr, *sf_n = nullptr;
-            auto aim = [&](const Unit& u) {
-                y_m = u.m * 128;
-                y_n = u.n * NT;
-                sf_m = p.m.b + ((int64_t)u.m * atoms + 4 * u.k0) * kAtom;
-                sf_n = p.n.b + ((int64_t)(y_n / 128) * atoms + 4 * u.k0) * kAtom;
-            };
+            // where the tile's rows and scales are, and the copies of a stage
+            const int y_m = u.m * 128, y_n = u.n * NT;
+            const uint8_t* sf_m = p.m.b + ((int64_t)u.m * atoms + 4 * u.k0) * kAtom;
+            const uint8_t* sf_n = p.n.b + ((int64_t)(y_n / 128) * atoms + 4 * u.k0) * kAtom;
             auto load_m = [&](uint32_t at, uint32_t full, int x, uint32_t bytes, const uint8_t* sf) {
                 tma_load_2d(at, &p.m.map, x, y_m, full);
                 bulk_load(at + S::kA + S::kB, sf, bytes, full);
@@ -156,49 +145,37 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                 bulk_load(at + S::kA + S::kB + S::kSfA, sf, bytes, full);
             };
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
-            uint32_t ahead = 0;
-            if ((int)blockIdx.x < units) {
-                const Unit u = unit_of(p, blockIdx.x);
-                aim(u);
-                ahead = min(S::kStages, u.k1 - u.k0);
-                for (uint32_t i = 0; i < ahead; ++i) {
-                    if (i + 1 == withheld) continue;
-                    const uint32_t at = sbase + i * S::kStage, full = bar(S::kFull + i);
-                    const int ks = u.k0 + i;
-                    const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
-                    mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
-                    if (WIDE) load_n(at, full, ks * kRowBytes, bytes, sf_n + i * 4 * kAtom);
-                    else load_m(at, full, ks * kRowBytes, bytes, sf_m + i * 4 * kAtom);
-                }
+            const uint32_t ahead = min(S::kStages, u.k1 - u.k0);
+            for (uint32_t i = 0; i < ahead; ++i) {
+                if (i + 1 == withheld) continue;
+                const uint32_t at = sbase + i * S::kStage, full = bar(S::kFull + i);
+                const int ks = u.k0 + i;
+                const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
+                mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
+                if (WIDE) load_n(at, full, ks * kRowBytes, bytes, sf_n + i * 4 * kAtom);
+                else load_m(at, full, ks * kRowBytes, bytes, sf_m + i * 4 * kAtom);
             }
             pdl_wait();
             uint32_t s = 0, parity = 1, at = sbase, full = bar(S::kFull);
-            for (int n = blockIdx.x; n < units && ok; n += grid) {
-                const Unit u = unit_of(p, n);
-                aim(u);
-                int x = u.k0 * kRowBytes;
-                for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
-                    if (it >= ahead && !mbar_wait(full + 8 * S::kStages, parity, abort_flag, p.hdr)) {  // (EMPTY)
-                        ok = false;
-                        break;
-                    }
-                    if (it + 1 != withheld) {  // (else its FULL phase never completes)
-                        const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
-                        if (it >= ahead) mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
-                        if (it >= ahead || WIDE) load_m(at, full, x, bytes, sf_m);
-                        if (it >= ahead || !WIDE) load_n(at, full, x, bytes, sf_n);
-                    }
-                    x += kRowBytes;
-                    sf_m += 4 * kAtom;
-                    sf_n += 4 * kAtom;
-                    at += S::kStage;
-                    full += 8;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        parity ^= 1;
-                        at = sbase;
-                        full = bar(S::kFull);
-                    }
+            int x = u.k0 * kRowBytes;
+            for (int ks = u.k0; ks < u.k1; ++ks, ++it) {
+                if (it >= ahead && !mbar_wait(full + 8 * S::kStages, parity, abort_flag, p.hdr)) break;  // (EMPTY)
+                if (it + 1 != withheld) {  // (else its FULL phase never completes)
+                    const uint32_t bytes = ks == last ? last_bytes : 4 * kAtom;
+                    if (it >= ahead) mbar_expect_tx(full, S::kA + S::kB + 2 * bytes);
+                    if (it >= ahead || WIDE) load_m(at, full, x, bytes, sf_m);
+                    if (it >= ahead || !WIDE) load_n(at, full, x, bytes, sf_n);
+                }
+                x += kRowBytes;
+                sf_m += 4 * kAtom;
+                sf_n += 4 * kAtom;
+                at += S::kStage;
+                full += 8;
+                if (++s == S::kStages) {
+                    s = 0;
+                    parity ^= 1;
+                    at = sbase;
+                    full = bar(S::kFull);
                 }
             }
             // do not leave with copies in flight (without an abort their phases are complete)
@@ -211,50 +188,41 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
         const uint32_t idesc = idesc_fp4(128, NT);
         const uint64_t ad0 = smem_desc_sw128(sbase), bd0 = smem_desc_sw128(sbase + S::kA);
         const uint64_t sd0 = scale_desc(sbase + S::kA + S::kB);
-        uint32_t s = 0, parity = 0, tc = 0;
+        uint32_t s = 0, parity = 0;
         bool ok = true;
-        for (int n = blockIdx.x; n < units && ok; n += grid) {
-            const Unit u = unit_of(p, n);
-            const int b = tc % S::kAcc;
-            if (!warp_wait(bar(S::kAEmpty + b), ((tc / S::kAcc) & 1) ^ 1, abort_flag, p.hdr)) break;
-            tc_fence_after();
-            const uint32_t d = tmem + b * NT;
-            for (int ks = u.k0; ks < u.k1; ++ks) {
-                if (!warp_wait(bar(S::kFull + s), parity, abort_flag, p.hdr)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    // (the lower 14 bits of a descriptor count 16 bytes, and a CTA's shared memory does not pass them)
-                    const uint64_t off = s * (S::kStage / 16), ad = ad0 + off, bd = bd0 + off, sd = sd0 + off;
-                    const uint32_t sfa = tmem + S::kSfCol0 + s * S::kSfCols, sfb = sfa + 16;
-                    const int nk = min(4, atoms - 4 * ks);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= nk) break;
-                        copy_scales<1>(sfa + 4 * kk, sd + kk * (kAtom / 16));
-                        copy_scales<1>(sfb + 4 * kk, sd + (S::kSfA + kk * kAtom) / 16);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {  // 32 bytes = 2 address units per step
-                        if (kk >= nk) break;
-                        mma_fp4<1>(d, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * kk,
-                                ks > u.k0 || kk > 0);
-                    }
-                    mma_commit(bar(S::kEmpty + s));
-                }
-                __syncwarp();
-                if (++s == S::kStages) {
-                    s = 0;
-                    parity ^= 1;
-                }
+        for (int ks = u.k0; ks < u.k1; ++ks) {
+            if (!warp_wait(bar(S::kFull + s), parity, abort_flag, p.hdr)) {
+                ok = false;
+                break;
             }
-            if (!ok) break;
-            if (elect_one()) mma_commit(bar(S::kAFull + b));
+            tc_fence_after();
+            if (elect_one()) {
+                // (the lower 14 bits of a descriptor count 16 bytes, and a CTA's shared memory does not pass them)
+                const uint64_t off = s * (S::kStage / 16), ad = ad0 + off, bd = bd0 + off, sd = sd0 + off;
+                const uint32_t sfa = tmem + S::kSfCol0 + s * S::kSfCols, sfb = sfa + 16;
+                const int nk = min(4, atoms - 4 * ks);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (kk >= nk) break;
+                    copy_scales<1>(sfa + 4 * kk, sd + kk * (kAtom / 16));
+                    copy_scales<1>(sfb + 4 * kk, sd + (S::kSfA + kk * kAtom) / 16);
+                }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {  // 32 bytes = 2 address units per step
+                    if (kk >= nk) break;
+                    mma_fp4<1>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, sfa + 4 * kk, sfb + 4 * kk,
+                            ks > u.k0 || kk > 0);
+                }
+                mma_commit(bar(S::kEmpty + s));
+            }
             __syncwarp();
-            ++tc;
+            if (++s == S::kStages) {
+                s = 0;
+                parity ^= 1;
+            }
         }
+        if (ok && elect_one()) mma_commit(bar(S::kAFull));
+        __syncwarp();
         // the products are done before the CTA frees TMEM
         if (elect_one()) mma_commit(bar(S::kTd));
         __syncwarp();
@@ -262,80 +230,60 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
-        // After a failed wait every warp keeps walking the units without the work, so that none waits
-        // at a barrier that the others left.
-        constexpr int kChunk = NT < 32 ? NT : 32;
+        // (after a failed wait every warp goes on without the work, so that none waits at a barrier that the others left)
         const int q = warp & 3, part = (warp - kEpiWarp0) >> 2, me = threadIdx.x - 32 * kEpiWarp0;
         const int r = q * 32 + lane;  // row of the tile, TMEM lane
-        bool ok = true;
-        uint32_t tc = 0;
+        const int64_t row = (int64_t)u.m * 128 + r, col0 = (int64_t)u.n * NT;
+        const int cols = (int)min((int64_t)NT, p.n.rows - col0);
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
+        float* cs = reinterpret_cast<float*>(smem + S::kScales);
+        float rs = 0.0f;
         pdl_wait();
-        for (int n = blockIdx.x; n < units; n += grid, ++tc) {
-            const Unit u = unit_of(p, n);
-            const int b = tc % S::kAcc;
-            const int64_t row = (int64_t)u.m * 128 + r, col0 = (int64_t)u.n * NT;
-            const int cols = (int)min((int64_t)NT, p.n.rows - col0);
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * NT;
-            float* cs = scales + (tc & 1) * NT;
-            float rs = 0.0f;
-            if (!once) {
-                if (me < cols) cs[me] = __ldg(p.n.s + col0 + me);
-                if (row < p.m.rows) rs = __ldg(p.m.s + row);
-            }
-            // (one warp waits for all: waiting warps take turns of the shared memory that copies and products use)
-            if (warp == kEpiWarp0) {
-                if (ok) ok = warp_wait(bar(S::kAFull + b), (tc / S::kAcc) & 1, abort_flag, p.hdr);
-                tc_fence_after();
-                tc_fence_before();
-            }
-            epi_sync();
-            if (ok) ok = !__any_sync(0xFFFFFFFFu, *abort_flag);
-            if (once) {
-                if (ok) {
-                    tc_fence_after();
-                    for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
-                        uint32_t v[kChunk];
-                        if constexpr (kChunk == 16) {
-                            tmem_ld_x16(acc + c0, v);
-                            tmem_wait_ld16(v);
-                        } else {
-                            tmem_ld_x32(acc + c0, v);
-                            tmem_wait_ld32(v);
-                        }
-                        float* to = reinterpret_cast<float*>(smem) + c0 * 128 + r;
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) to[j * 128] = __uint_as_float(v[j]);
-                    }
-                    tc_fence_before();
+        if (!shared) {
+            if (me < cols) cs[me] = __ldg(p.n.s + col0 + me);
+            if (row < p.m.rows) rs = __ldg(p.m.s + row);
+        }
+        // (one warp waits for all: waiting warps take turns of the shared memory that copies and products use)
+        bool ok = true;
+        if (warp == kEpiWarp0) {
+            ok = warp_wait(bar(S::kAFull), 0, abort_flag, p.hdr);
+            tc_fence_after();
+            tc_fence_before();
+        }
+        epi_sync();
+        if (ok) ok = !__any_sync(0xFFFFFFFFu, *abort_flag);
+        tc_fence_after();
+        if (shared && ok) {
+            constexpr int kChunk = NT < 32 ? NT : 32;
+            for (int c0 = part * kChunk; c0 < cols; c0 += 2 * kChunk) {
+                uint32_t v[kChunk];
+                if constexpr (kChunk == 16) {
+                    tmem_ld_x16(acc + c0, v);
+                    tmem_wait_ld16(v);
+                } else {
+                    tmem_ld_x32(acc + c0, v);
+                    tmem_wait_ld32(v);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
-            } else if constexpr (WIDE) {
-                // All of a lane's sums leave TMEM before they are packed and stored, so that the accumulator is free soonest.
-                constexpr int kRuns = NT / 64;
-                uint32_t v[kRuns][32];
-                if (ok) {
-                    tc_fence_after();
+                float* to = reinterpret_cast<float*>(smem) + c0 * 128 + r;
 #pragma unroll
-                    for (int k = 0; k < kRuns; ++k) tmem_ld_x32(acc + 32 * (2 * k + part), v[k]);
-#pragma unroll
-                    for (int k = 0; k < kRuns; ++k) tmem_wait_ld32(v[k]);
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(S::kAEmpty + b));
-                if (!ok) continue;
+                for (int j = 0; j < kChunk; ++j) to[j * 128] = __uint_as_float(v[j]);
+            }
+        } else if constexpr (WIDE) {
+            if (ok) {
                 const int64_t at = (int64_t)u.m * 128 + q * 32 + (lane & ~3);
                 const int rows = (int)min((int64_t)4, p.m.rows - at), left = cols - 32 * part - 8 * (lane & 3);
                 uint16_t* to = p.out + at * p.ld + col0 + 32 * part + 8 * (lane & 3);
 #pragma unroll
-                for (int k = 0; k < kRuns; ++k) {
+                for (int k = 0; k < NT / 64; ++k) {
+                    uint32_t v[32];
+                    tmem_ld_x32(acc + 32 * (2 * k + part), v);
+                    tmem_wait_ld32(v);
                     const float4* c = reinterpret_cast<const float4*>(cs + 32 * (2 * k + part));
                     uint4 x[4];  // 32 outputs, packed
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float4 a = c[2 * j], e = c[2 * j + 1];
-                        auto f = [&](int i) { return __uint_as_float(v[k][8 * j + i]) * rs; };
+                        auto f = [&](int i) { return __uint_as_float(v[8 * j + i]) * rs; };
                         x[j] = make_uint4(pack2(f(0) * a.x, f(1) * a.y), pack2(f(2) * a.z, f(3) * a.w),
                                           pack2(f(4) * e.x, f(5) * e.y), pack2(f(6) * e.z, f(7) * e.w));
                     }
@@ -346,12 +294,11 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
     }
 
     tc_fence_before();
-    if (once) {
+    if (shared) {
         // Every warp's sums lie in shared memory as [NT][128]; the CTAs of a cluster share the adding and the stores.
         if (p.splits > 1) cluster_sync();
         else __syncthreads();
         if (warp >= kEpiWarp0) {
-            const Unit u = unit_of(p, blockIdx.x);
             const int64_t row0 = (int64_t)u.m * 128, col0 = (int64_t)u.n * NT;
             const int rows = (int)min((int64_t)128, p.m.rows - row0), cols = (int)min((int64_t)NT, p.n.rows - col0);
             const int rank = blockIdx.x % p.splits, me = threadIdx.x - 32 * kEpiWarp0;
@@ -426,7 +373,7 @@ cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, int 
     for (int s = 2; s <= most; s *= 2)
         if (tiles * s <= (!WIDE ? sms * 7 / 4 : s == 2 ? sms : s == 4 ? sms * 7 / 8 : sms * 3 / 4) && stages >= 2 * s) p.splits = s;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(WIDE && p.splits == 1 ? std::min(tiles, sms) : tiles * p.splits);
+    cfg.gridDim = dim3(tiles * p.splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = st;
@@ -453,11 +400,11 @@ cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uin
     if (T <= 16) return launch<16, false>(p, x, w, T, N, st);
     if (T <= 32) return launch<32, false>(p, x, w, T, N, st);
     if (T <= 64) return launch<64, false>(p, x, w, T, N, st);
-    // Wide tiles that find an SM each (or share K) are done soonest; where there are more of them, and K is long enough to pay for
-    // a pair's longer way in and out, the pairs' larger tiles move fewer bytes.  Wide, pairs, us without the quantisation: 256 tokens, N =
-    // 8192, K = 2048 7.2, 8.2; N = 16384, K = 512 6.2, 6.4; K = 1024 8.0, 7.3; K = 2048 10.5, 8.6; 2048 tokens, N = 6144, K = 4096 34, 25.
+    // Wide tiles that find an SM each (or share K) are done soonest; where there are more of them, the pairs' larger tiles move fewer
+    // bytes.  Wide, pairs, us without the quantisation: 256 tokens, N = 8192, K = 512 4.3, 5.2; K = 2048 7.0, 7.1; N = 16384,
+    // K = 512 6.3, 5.7; K = 2048 10.5, 7.7; 2048 tokens, N = 6144, K = 512 12.9, 10.3; K = 4096 36, 21.
     const int64_t tiles = (int64_t)((T + 127) / 128) * ((N + 127) / 128);
-    if (tiles > sm_count() && K >= 1024) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
+    if (tiles > sm_count()) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
     return launch<128, true>(p, x, w, T, N, st);
 }
 

@@ -154,10 +154,10 @@ def test_projection(T, N, K):
     check(project(x.cuda(), w, T, N, K), x, w)
 
 
-# More wide tiles (128 tokens by 128 rows) than SMs, and K from 1024 on: pairs of CTAs.  Halves of a tile without tokens or
+# More wide tiles (128 tokens by 128 rows) than SMs: pairs of CTAs.  Halves of a tile without tokens or
 # weight rows, K that ends inside a stage, one and several tiles to a pair.
 @pytest.mark.parametrize("T,N,K", [
-    (2049, 1400, 1088), (257, 10248, 1024), (300, 8200, 1984), (1100, 2568, 1344), (385, 16392, 4160), (2000, 1416, 1152), (20000, 136, 1024), (129, 20000, 1216),
+    (2049, 1400, 1088), (257, 10248, 1024), (300, 8200, 1984), (1100, 2568, 1344), (385, 16392, 4160), (2000, 1416, 1152), (20000, 136, 1024), (129, 20000, 1216), (2570, 1288, 64), (3000, 4104, 192),
 ])
 def test_projection_by_pairs(T, N, K):
     g = torch.Generator().manual_seed(T + N + K)

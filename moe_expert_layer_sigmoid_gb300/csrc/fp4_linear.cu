@@ -66,8 +66,8 @@ __device__ __forceinline__ Unit unit_of(const LinearParams& p, int u) {
     Unit r;
     r.n = tile / p.m.tiles;
     r.m = tile - r.n * p.m.tiles;
-    r.k0 = (int)((int64_t)all * s / p.splits);
-    r.k1 = (int)((int64_t)all * (s + 1) / p.splits);
+    r.k0 = all * s / p.splits;  // (at most 256 * 8)
+    r.k1 = all * (s + 1) / p.splits;
     return r;
 }
 

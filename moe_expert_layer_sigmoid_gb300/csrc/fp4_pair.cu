@@ -122,7 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             const uint32_t full0 = peer_addr(bar(kFull), 0);  // in the leader
             uint32_t it = 0;
             bool ok = true;
-            int m = 0, n = 0;
+            int n = first / p.x.tiles, m = first - n * p.x.tiles;
             // K's last stage is filled up with zeros where K ends inside it, and rows past the last are zeros
             auto expect = [&](uint32_t i) {
                 if (rank == 0) mbar_expect_tx(bar(kFull) + 8 * i, role == kWeights ? 2 * kB : role == kTokens ? 2 * kA : 2 * (kSfA + kSfB));
@@ -140,7 +140,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             // The weights of the first stages do not wait for the kernel before this one, which makes the tokens' codes.
             uint32_t ahead = 0;
             if (first < units) {
-                n = first / p.x.tiles;
                 ahead = min(kStages, stages);
                 for (uint32_t i = 0; i < ahead; ++i) {
                     if (i + 1 == withheld) continue;
@@ -151,8 +150,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
             pdl_wait();
             uint32_t s = 0, parity = 1, at = sbase, full = full0, empty = bar(kEmpty);
             for (int u = first; u < units && ok; u += step) {
-                n = u / p.x.tiles;
-                m = u - n * p.x.tiles;
+                if (u != first) {
+                    n = u / p.x.tiles;
+                    m = u - n * p.x.tiles;
+                }
                 for (int ks = 0; ks < stages; ++ks, ++it) {
                     if (it >= ahead && !mbar_wait(empty, parity, abort_flag, p.hdr)) {
                         ok = false;

@@ -409,7 +409,7 @@ moe_status_t moe_check_device_status(void* ws, size_t ws_bytes, void* stream);
  *                   default);
  *   withhold_stage  s > 0: in every later gate+up launch on the grouped path
  *                   (W4A16 and W8A8), every later attention launch and every later
- *                   moe_linear_fp4 launch that has stages (3 tokens and more), CTA 0
+ *                   moe_linear_fp4 launch that has stages (3 tokens and more, fewer on large weights), CTA 0
  *                   skips the copies of its s-th pipeline stage, so that
  *                   stage's consumers wait until the limit; 0: off.
  * No memory access changes.  A call with (0, 0) restores normal operation; the

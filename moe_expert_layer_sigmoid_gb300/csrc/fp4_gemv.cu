@@ -220,11 +220,12 @@ cudaError_t launch(GemvParams p, cudaStream_t st) {
 
 }  // namespace
 
-// One token, or two on a weight of at most 2^24 elements, whose rows fit shared memory as f16.  Here and by the tensor cores,
-// quantisation included, us: one token, N = 6144, K = 4096 5.6, 8.2; N = 16384 9.4, 10.1; two tokens, N = 4096 7.3, 8.1; N = 6144
-// 8.6, 8.2; three at N = 6144 12.4, 8.2.
+// One or two tokens whose rows fit shared memory as f16, on weights small enough; a row of weights costs as much as some 1024
+// more of K.  Here and by the tensor cores, quantisation included, us: one token, N = 1024, K = 4096 4.1, 6.7; N = 6144 6.0, 7.3; N = 8192
+// 6.4, 7.4; N = 6144, K = 8192 8.9, 8.5; N = 16384, K = 4096 9.5, 8.7; N = 32768, K = 512 8.6, 5.6; two tokens, N = 1024, K = 4096 5.8,
+// 6.8; N = 4096, K = 2048 5.4, 6.0; K = 4096 7.5, 6.8; N = 6144 8.9, 7.5; three at N = 6144 12.4, 7.4.
 bool gemv_fp4_takes(int T, int N, int K) {
-    return T <= 2 && T * K <= 32768 && (T == 1 || (int64_t)N * K <= 1 << 24);
+    return T <= 2 && T * K <= 32768 && (int64_t)N * (K + 1024) < (T == 1 ? 3 << 24 : 7 << 21);
 }
 
 cudaError_t launch_gemv_fp4(const uint16_t* x, int64_t ldx, moe_fp4_t w, int T, int N, int K, uint16_t* out,

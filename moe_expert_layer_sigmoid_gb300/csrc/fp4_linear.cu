@@ -10,8 +10,8 @@
 // in the order that tcgen05.cp spreads over TMEM (lane r % 32 and column r / 32 hold row r's four scales).  Four
 // products of K = 64 per stage.  Two forms:
 //  - narrow, for few tokens: M are weight rows, NT the smallest of 16, 32, 64 that holds the tokens; one tile per CTA.  What
-//    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 9.5 us with the
-//    quantisation's 1.9; the weights are 2.1 us of DRAM time).
+//    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 9.2 us with the
+//    quantisation's 2.1; the weights are 2.1 us of DRAM time).
 //  - wide, NT = 128: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row.
 // A CTA has one tile.  Where wide tiles are more than SMs, pairs of CTAs take over (launch_pair_fp4).
 // Where the tiles are too few for the SMs, K is cut among the CTAs of a cluster, which add their sums in
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, WIDE ? 1 : 2) linear_kernel(const __
                         for (int j = 0; j < 8; ++j) v[j] += load_peer(from + 4 * ((c + j) * 128 + r));
                     }
                 } else {
-                    // (every CTA's part is on the way before the first is added: 64 tokens, N = 6144, K = 4096 8.3 to 8.0 us; with
+                    // (every CTA's part is on the way before the first is added: 64 tokens, N = 6144, K = 4096 8.0 to 7.7 us; with
                     // eight loads of the wide form for each it took longer)
                     float part[kMaxNarrow][8];
 #pragma unroll

@@ -3,9 +3,9 @@
 // A tile of 256 tokens by 256 weight rows belongs to two CTAs of a cluster, whose tensor cores work as one (cta_group::2):
 // each holds half of the tokens and half of the weight rows of a stage, the scales of its tokens and of all weight rows, and
 // the sums of its tokens.  So a CTA takes in 38 KB per stage of K = 256, where a tile of 128 by 256 of its own would take 54, and its
-// tensor core reads 32 KB of codes instead of 48.  What bounds it is the stages' way round (0.33 us each, 0.31 without products, which
-// take 0.2; 0.36 with one stage less) and about 2 us from a tile to the next: 2048 tokens, N = 6144, K = 4096 25 us, 4.1 PFLOP/s;
-// 8192 tokens, N = K = 8192 180, 6.1 PFLOP/s.
+// tensor core reads 32 KB of codes instead of 48.  What bounds it is a stage's way round (0.32 us, 0.29
+// without products, which take 0.2; 0.25 without the scales too) and what lies between two tiles: 2048 tokens, N = 6144, K = 4096 20.5 us,
+// 5.0 PFLOP/s; 8192 tokens, N = K = 8192 152, 7.2 PFLOP/s.
 //
 // All of a stage's copies, of either CTA, are counted on one barrier of the leader (rank 0), which issues the products; their
 // completion frees the stage in both.
@@ -58,7 +58,7 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 // Relaxed: what it tells, that TMEM has been read, is over when it is issued, and it hands nothing in memory over.  (With release, and
-// a fence at the leader, it waited for the tile's stores before: 25.2 us instead of 22.2 in the case above.)
+// a fence at the leader, it waited for the tile's stores before: in the first case above 25.2 us instead of 22.2.)
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }

@@ -168,6 +168,18 @@ def test_projection_by_pairs(T, N, K):
     assert (buf[T:] == 7).all()
 
 
+# One and two tokens on either side of where the tensor cores take over.
+@pytest.mark.parametrize("T,N,K", [
+    (1, 9000, 4160), (1, 16384, 512), (1, 16392, 2048), (1, 33000, 448), (1, 8, 32768), (1, 8, 65536), (1, 6144, 8192), (2, 13000, 64), (2, 4104, 2048), (2, 1024, 8192),
+    (2, 8, 16384), (2, 8, 16448), (2, 6152, 1984), (2, 1032, 16384),
+])
+def test_projection_of_one_and_two(T, N, K):
+    g = torch.Generator().manual_seed(T + N + K)
+    x = rows_of(T, K, "outliers", seed=T).to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g) / math.sqrt(K)
+    check(project(x.cuda(), w, T, N, K), x, w)
+
+
 def test_pairs_captured_and_on_two_streams():
     T, N, K = 1300, 2056, 1088
     g = torch.Generator().manual_seed(8)

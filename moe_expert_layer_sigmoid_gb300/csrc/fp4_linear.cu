@@ -10,7 +10,7 @@
 // in the order that tcgen05.cp spreads over TMEM (lane r % 32 and column r / 32 hold row r's four scales).  Four
 // products of K = 64 per stage.  Two forms:
 //  - narrow, for few tokens: M are weight rows, NT the smallest of 16, 32, 64 that holds the tokens; one tile per CTA.  What
-//    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 9.2 us with the
+//    bounds it is the time until the first weights arrive and the joining (16 tokens, N = 6144, K = 4096: 8.5 us with the
 //    quantisation's 2.1; the weights are 2.1 us of DRAM time).
 //  - wide, NT = 128: M are tokens, so that a lane of the epilogue holds 32 neighbours of an output row.
 // A CTA has one tile.  Where wide tiles are more than SMs, pairs of CTAs take over (launch_pair_fp4).
@@ -365,13 +365,15 @@ cudaError_t launch(LinearParams& p, const moe_fp4_t& x, const moe_fp4_t& w, int 
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int tiles = p.m.tiles * p.n.tiles, stages = (p.K + kStageK - 1) / kStageK;
     // K is cut while CTAs find an SM: in pairs all of them do, in fours 144 of 152, in eights 120 (each GPC holds whole
-    // clusters; 16 of eight took twice the time of 8).  Narrow tiles are light enough for more CTAs than SMs, in fours at most, since joining costs more the more
-    // tokens there are (cuts of 1, 2, 3, 4 and 6, us: 16 tokens, N = 6144, K = 4096 11.7, 9.7, 9.5, 9.6, 15.9; N = 16384 12.3, 10.8, 17.6,
-    // 18.3, 26.7; 64 tokens, N = 6144 13.4, 10.8, 11.8, 11.8, 20.4).
+    // clusters; 16 of eight took twice the time of 8).  Narrow tiles are light enough for more CTAs than SMs, in pairs or where K is
+    // long; joining wide ones costs as much as some ten stages.  Cuts of 1, 2, 4, us without the quantisation: 16 tokens, N = 2048, K = 4096 7.6, 5.8, 5.0; N = 6144
+    // 7.8, 6.0, 6.6, K = 16384 20.6, 12.3, 9.6; N = 16384, K = 4096 7.8, 7.0, 13.2; 64 tokens, N = 4096 8.9, 6.9, 6.7; 128 tokens, N = 2048 7.8, 8.4, 7.2; K = 2048 5.6, 6.6, 6.0.
     p.splits = 1;
-    const int most = WIDE ? kMaxSplits : NT <= 32 ? kMaxNarrow : 2;
-    for (int s = 2; s <= most; s *= 2)
-        if (tiles * s <= (!WIDE ? sms * 7 / 4 : s == 2 ? sms : s == 4 ? sms * 7 / 8 : sms * 3 / 4) && stages >= 2 * s) p.splits = s;
+    for (int s = 2; s <= (WIDE ? kMaxSplits : kMaxNarrow); s *= 2) {
+        const bool many = !WIDE && (s == 2 || stages >= 48);
+        const int most = many ? sms * 7 / 4 : s == 2 ? sms : s == 4 ? sms * 7 / 8 : sms * 3 / 4;
+        if (tiles * s <= most && stages >= 2 * s && (!WIDE || stages * (s - 1) / s >= 12)) p.splits = s;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(tiles * p.splits);
     cfg.blockDim = dim3(kThreads);

@@ -180,12 +180,14 @@ cudaError_t launch_bf16(const uint16_t* x, int64_t ld, int64_t rows, int64_t K, 
 
 cudaError_t launch_quant_fp4(const void* src, bool bf16, int64_t ld, int64_t rows, int64_t K, Fp4Rows out,
                              cudaStream_t st) {
+    const int64_t sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     if (!bf16) return launch_any(static_cast<const float*>(src), ld, rows, K, out, st);
     const uint16_t* x = static_cast<const uint16_t*>(src);
     if (K > 16384) return launch_any(x, ld, rows, K, out, st);
     // Blocks to a thread, by how many blocks there are for a full house of threads (1024 on every SM).  1, 2 and 4 to a
     // thread, us: 128 rows of 4096 (0.2 full) 2.2, 2.3, 3.0; 2048 rows (3.4) 6.3, 5.5, 5.8; 8191 rows (13) 22.5, 19.2, 18.1
-    const int64_t blocks = K / 16, full = rows * blocks / ((int64_t)sm_count() * 1024);
+    const int64_t blocks = K / 16, full = rows * blocks / (sms * 1024);
     if (full >= 6 && blocks >= 128) return launch_bf16<4>(x, ld, rows, K, out, st);
     if (blocks > 512 || (full >= 1 && blocks >= 64)) return launch_bf16<2>(x, ld, rows, K, out, st);
     return launch_bf16<1>(x, ld, rows, K, out, st);

@@ -113,14 +113,14 @@ class Kv(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p),
                 ("vs", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
-    shape = None
+    shape = dev = None
 
 
 class KvPages(ctypes.Structure):
     """moe_kv_pages_t: the state of a pool's pages (device pointers).  kv_pages makes one and
     records its sizes for the calls' checks."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("kv_len", "first", "pages", "free_pages", "n_free")]
-    sizes = None
+    sizes = dev = None
 
 
 class RopeConfig(ctypes.Structure):
@@ -135,7 +135,7 @@ class Rope(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
                 ("n_pos", ctypes.c_int32), ("rot", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("eps", ctypes.c_float)]
-    D = None
+    D = dev = None
 
 
 class NormDims(ctypes.Structure):
@@ -148,7 +148,7 @@ class Fp4(ctypes.Structure):
     """moe_fp4_t: 4-bit codes, block scales and row scales (device pointers).  fp4 makes one and
     records its shape for the calls' checks."""
     _fields_ = [("q", ctypes.c_void_p), ("b", ctypes.c_void_p), ("s", ctypes.c_void_p)]
-    shape = None
+    shape = dev = None
 
 
 _lib = None
@@ -524,9 +524,11 @@ def kv_cache(k: torch.Tensor, v: torch.Tensor, ks: torch.Tensor | None = None,
     for t, n in ((ks, "ks"), (vs, "vs")):
         if t is not None and tuple(t.shape) != tuple(k.shape[:3]):
             raise ValueError(f"{n} must be [n_pages][H_kv][page]")
+    if any(t is not None and t.get_device() != k.get_device() for t in (v, ks, vs)):
+        raise ValueError("the cache's tensors must be on one device")
     c = Kv(k.data_ptr(), v.data_ptr(), _dev(ks, torch.float32, "ks") if quantised else None,
            _dev(vs, torch.float32, "vs") if quantised else None, *strides(k))
-    c.shape, c.dtype = tuple(k.shape), k.dtype
+    c.shape, c.dtype, c.dev = tuple(k.shape), k.dtype, k.get_device()
     return c
 
 
@@ -646,9 +648,16 @@ def _heads(t, shape, dev: int, name: str):
 
 
 def _space(ws, dev: int):
-    if ws.get_device() != dev:
-        raise ValueError("ws must be a CUDA tensor on the current device")
+    """Pointer and bytes of a workspace (of any type: its bytes count)."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor on the current device")
     return ws.data_ptr(), ws.nbytes
+
+
+def _here(handle, dev: int, name: str):
+    """A handle's tensors are on the current device, as the call's others (one made from raw pointers has no device)."""
+    if handle.dev != dev and handle.dev is not None:
+        raise ValueError(f"the tensors of {name} must be on the current device")
 
 
 def kv_pages(kv_len: torch.Tensor, first: torch.Tensor, pages: torch.Tensor, free_pages: torch.Tensor,
@@ -662,7 +671,7 @@ def kv_pages(kv_len: torch.Tensor, first: torch.Tensor, pages: torch.Tensor, fre
     st = KvPages(_flat(kv_len, B, _I32, dev, "kv_len"), _flat(first, B, _I32, dev, "first"),
                  _flat(pages, pages.numel(), _I32, dev, "pages"),
                  _flat(free_pages, free_pages.numel(), _I32, dev, "free_pages"), _flat(n_free, 1, _I32, dev, "n_free"))
-    st.sizes = (B, pages.shape[1], free_pages.numel())
+    st.sizes, st.dev = (B, pages.shape[1], free_pages.numel()), dev
     st.tensors = (kv_len, first, pages, free_pages, n_free)
     return st
 
@@ -676,6 +685,7 @@ def moe_kv_plan(new_len: torch.Tensor, dims: KvDims, state: KvPages, q_off: torc
     if state.sizes is not None and state.sizes != (B, dims.max_pages, dims.n_pages):
         raise ValueError("the state's sizes are not those of dims")
     dev = _current_device()
+    _here(state, dev, "state")
     status = (_lib or lib()).moe_kv_plan(
         _flat(new_len, B, _I32, dev, "new_len"), dims, state, _flat(q_off, B + 1, _I32, dev, "q_off"),
         _flat(pos, T, _I32, dev, "pos"), _flat(slots, T, _I32, dev, "slots"), *_space(ws, dev), _stream(stream))
@@ -706,12 +716,13 @@ def rope(table: torch.Tensor, flags: int = 0, q_norm: torch.Tensor | None = None
     D, dev = widths.pop() if widths else None, _current_device()
     r = Rope(_flat(table, table.numel(), _F32, dev, "table"), _flat(q_norm, D, _F32, dev, "q_norm"),
              _flat(k_norm, D, _F32, dev, "k_norm"), table.shape[0], table.shape[1], flags, eps)
-    r.D = D
+    r.D, r.dev = D, dev
     r.tensors = (table, q_norm, k_norm)
     return r
 
 
-def _rope_check(rope: Rope, D: int):
+def _rope_check(rope: Rope, D: int, dev: int):
+    _here(rope, dev, "rope")
     if rope.D is not None and rope.D != D:
         raise ValueError(f"the norms must be [D] with D = {D}")
 
@@ -722,8 +733,8 @@ def moe_rope_rows(x: torch.Tensor, pos: torch.Tensor, rope: Rope, out: torch.Ten
     if x.dim() != 3:
         raise ValueError("x must be [T][H][D]")
     T, H, D = x.shape
-    _rope_check(rope, D)
     dev = _current_device()
+    _rope_check(rope, D, dev)
     status = (_lib or lib()).moe_rope_rows(
         *_heads(x, (T, H, D), dev, "x"), _flat(pos, T, _I32, dev, "pos"), T, H, D, rope,
         *_heads(out, (T, H, D), dev, "out"), *_space(ws, dev), _stream(stream))
@@ -737,8 +748,9 @@ def moe_rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: to
     written into the cache's slots with the values (tokens of each may lie apart)."""
     T, H, D = dims.T, dims.H, dims.D
     _kv_check(dims, cache, dims.H_kv, D)
-    _rope_check(rope, D)
     dev, wide, narrow = _current_device(), (T, H, D), (T, dims.H_kv, D)
+    _here(cache, dev, "cache")
+    _rope_check(rope, D, dev)
     status = (_lib or lib()).moe_rope_kv_write(
         *_heads(q, wide, dev, "q"), *_heads(k, narrow, dev, "k"), *_heads(v, narrow, dev, "v"),
         _flat(pos, T, _I32, dev, "pos"), _flat(slots, T, _I32, dev, "slots"), rope, dims, cache,
@@ -777,7 +789,7 @@ def fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor) -> Fp4:
         raise ValueError("q must be [rows][K/2], s [rows] and b moe_fp4_scale_bytes(rows, K) bytes")
     dev = _current_device()
     w = Fp4(_flat(q, q.numel(), _U8, dev, "q"), _flat(b, b.numel(), _U8, dev, "b"), _flat(s, s.numel(), _F32, dev, "s"))
-    w.shape, w.tensors = (q.shape[0], 2 * q.shape[1]), (q, b, s)
+    w.shape, w.dev, w.tensors = (q.shape[0], 2 * q.shape[1]), dev, (q, b, s)
     return w
 
 
@@ -837,6 +849,7 @@ def moe_linear_fp4(x: torch.Tensor, w: Fp4, out: torch.Tensor, ws, stream=None):
         raise ValueError("w must come from fp4()")
     N, K = w.shape
     dev = _current_device()
+    _here(w, dev, "w")
     if x.dim() != 2 or x.get_device() != dev or x.dtype not in _BF16:
         raise ValueError("x must be a bf16 CUDA tensor [T][K] on the current device")
     (T, width), (ld, one) = x.shape, x.stride()

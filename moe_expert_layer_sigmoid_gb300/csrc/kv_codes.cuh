@@ -32,8 +32,9 @@ __device__ __forceinline__ float quotient(float f, float s, float r) {
     return __fmaf_rn(-__fmaf_rn(y, s, -f), r, y);
 }
 
-// The codes of eight quotients.  int4: no quotient by s rounds to more than 7 in magnitude, so the
-// recipe's clamp has nothing to do; adding 1.5 * 2^23 leaves the rounded number in the low bits.
+// The codes of eight quotients.  int4: they round to -8 .. 7, which those of bf16 rows do without the recipe's clamp (a seventh
+// of 2^-133 or more keeps 13 bits, so no quotient by it rounds to more than 7 in magnitude); fp32 rows are clamped by who
+// calls.  Adding 1.5 * 2^23 leaves the rounded number in the low bits.
 template <int FMT>
 __device__ __forceinline__ uint2 codes_of(const float (&f)[8]) {
     if (FMT == kKvE4m3) {

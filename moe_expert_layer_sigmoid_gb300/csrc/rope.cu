@@ -109,6 +109,12 @@ __device__ __forceinline__ void store_key(const float (&f)[2][8], uint8_t* row, 
         // (keys are a small share of the rows: a division each costs nothing that shows)
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = s > 0.0f ? __fdiv_rn(f[j][i], s) : 0.0f;
+        // The recipe's clamp: a turned key may be so small that its scale is a few units of 2^-149, rounded by up to half of
+        // one, and quotients reach 10.  (NaN stays; E4M3's conversion saturates by itself.)
+        if (FMT == kKvInt4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = y[i] > 7.0f ? 7.0f : y[i] < -8.0f ? -8.0f : y[i];
+        }
         const uint2 c = codes_of<FMT>(y);
         if (FMT == kKvE4m3) reinterpret_cast<uint2*>(row)[at[j]] = c;
         else reinterpret_cast<uint32_t*>(row)[at[j]] = c.x;

@@ -626,8 +626,9 @@ typedef struct {
  *     dims.window > 0 those of the others in which no token from position
  *     kv_len[b] on sees a key any more.  They are listed by sequence, then by
  *     index, and the stack gets the last of the list first, so dropping the
- *     tokens that the call before added restores the stack.  Their entries
- *     become -1.
+ *     tokens that the call before added restores the stack if that call gave
+ *     none back (what a window has given back stays on it, and first stays).
+ *     Their entries become -1.
  *  2. New pages come off the top of the stack, by sequence, then by index.  A
  *     sequence that grows is served if the tokens asked for by it and all before
  *     it are at most dims.T and, where it needs a page, the pages asked for by

@@ -179,14 +179,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
                 }
             }
             // Do not leave with copies in flight: without an abort their phases are complete, as every product has been
-            // waited for; after one the leader waits for its phases, and the other, which cannot, for longer than a copy takes.
+            // waited for; after one the leader waits for its phases, which count the other's copies too (for what that one copies
+            // past them see the end).
             if (rank == 0) {
                 for (uint32_t j = it >= kStages ? it - kStages : 0; j < it; ++j)
                     if (j + 1 != withheld) mbar_drain(bar(kFull + j % kStages), (j / kStages) & 1, p.hdr);
             }
-            if (!ok)
-                for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
-                }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -313,10 +311,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) pair_ke
         }
     }
 
-    // neither leaves while the other's arrivals or products may still come
+    // Neither leaves while the other's arrivals or products may still come.  After an abort the leader may have given up at an
+    // earlier stage than the other copied for, whose phases nobody can wait for then: its CTA stays for longer than a copy
+    // takes.  (Its own flag is set by then: products that the leader leaves out never reach its epilogue's or its copies' waits.)
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) mbar_drain(bar(kTd), 0, p.hdr);
+    if (threadIdx.x == 0) {
+        mbar_drain(bar(kTd), 0, p.hdr);
+        if (*abort_flag)
+            for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000;) {
+            }
+    }
     __syncthreads();
     cluster_meet();
     tc_fence_after();

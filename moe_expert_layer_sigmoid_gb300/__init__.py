@@ -614,6 +614,7 @@ def moe_attn_paged(q: torch.Tensor, q_off: torch.Tensor, kv_len: torch.Tensor, p
 # ------------------------------------- page planning, rotary positions, block norms, 4-bit floats
 
 _current_device = torch._C._cuda_getDevice
+_I32_END = 1 << 31
 _BF16, _F32, _I32, _U8 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,), (torch.uint8,)
 
 
@@ -697,6 +698,8 @@ def moe_rope_table(config: RopeConfig, pos0: int, table: torch.Tensor, stream=No
     """The rotary table fp32 [n_pos][rot] of positions pos0 on: cosines, then sines."""
     if table.dim() != 2 or table.shape[1] != config.rot:
         raise ValueError("table must be [n_pos][rot]")
+    if not -_I32_END <= pos0 < _I32_END:  # (it would be cut to another position)
+        raise ValueError(f"pos0 must be a position below 2^31, got {pos0}")
     status = (_lib or lib()).moe_rope_table(config, pos0, table.shape[0],
                                             _flat(table, table.numel(), _F32, _current_device(), "table"),
                                             _stream(stream))
@@ -779,6 +782,8 @@ def moe_block_norm(y: torch.Tensor | None, residual: torch.Tensor, gate: torch.T
 
 
 def moe_fp4_scale_bytes(rows: int, K: int) -> int:
+    if max(rows, K) >= _I32_END:
+        return 0
     return lib().moe_fp4_scale_bytes(rows, K)
 
 
@@ -839,6 +844,8 @@ def moe_unpack_fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor, out: torch
 
 
 def moe_linear_fp4_workspace_bytes(T: int, N: int, K: int) -> int:
+    if max(T, N, K) >= _I32_END:
+        return 0
     return lib().moe_linear_fp4_workspace_bytes(T, N, K)
 
 

@@ -287,7 +287,7 @@ cudaError_t launch_kv_plan(const int32_t* new_len, const moe_kv_dims_t& d, const
     cudaLaunchConfig_t cfg{};
     // One CTA, as large as the batch, or a cluster of eight where tokens are many (1 and 8 CTAs, us for two calls: 1600
     // tokens of 8 sequences 8.6, 10.1; 4000 of 20 12.1, 10.4; 35000 of 60 56, 15.5).
-    const int rows = (d.T + kRun - 1) / kRun;
+    const int rows = d.T / kRun + (d.T % kRun != 0);  // (T may be 2^31 - 1)
     cfg.gridDim = dim3(rows > 512 ? 8 : 1);
     cfg.blockDim = dim3(std::max(d.B, rows) <= 128 ? 128 : std::max(d.B, rows) <= 2048 ? 512 : kPlanThreads);
     cfg.dynamicSmemBytes = smem;

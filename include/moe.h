@@ -837,7 +837,8 @@ size_t moe_linear_fp4_workspace_bytes(int32_t T, int32_t N, int32_t K);
 /* moe_linear_fp4 -- a projection: x quantised as above, then
  *   out[t][n] = bf16( sum_j x^_tj w^_nj ),
  * x^ and w^ what the codes stand for: code products with their block scales
- * summed in fp32 over K, then the two row scales.
+ * summed in fp32 over K, then times the token's row scale and the weights', in fp32 (a
+ * product that passes its range on the way is lost).
  *   x    (device) bf16 [T][K], token t at x + t * ldx elements; 16-byte aligned,
  *        ldx a multiple of 8, at least K when T > 1
  *   w    weights of moe_pack_fp4, N rows

@@ -1,12 +1,18 @@
 // The norms between two blocks, fused with the gate, the scale and the residual
 // between them: one launch, one pass over memory.
 //
-// A row stays in the registers of its threads from the first load to the last store, so the two sums of
+// A row stays with its threads from the first load to the last store, so the two sums of
 // squares cost exchanges only; the bound is DRAM bandwidth, and for a few rows the launch and two exchanges.
 // Rows of at most kWarpRow elements take a warp each, longer ones a CTA.  Either walks rows, and copies the rows
 // to come into shared memory meanwhile, each thread what it will itself read, so that memory is busy while
-// sums are exchanged.  Sums are fp32, in an order that the row's length alone sets.  Measured: 8192 rows of 4096 with a
-// full gate 57 us, 5.9 TB/s (rows in registers only, a CTA each: 67); one row 2.5 us.
+// sums are exchanged.  Sums are fp32, in an order that the row's length and the residual's type set (a thread adds the groups of 8
+// or 4 elements that it loads).  Measured: 8192 rows of 4096 with a
+// full gate 57 us, 5.9 TB/s (rows in registers only, a CTA each: 67); one row 2.7 us.
+//
+// Rows past 16384 elements (and past 8192 with an fp32 residual and a full gate, whose copies do not fit) have no ring: a CTA
+// each, read in place.  Past 16384 a thread's 32 elements of residual and output do not fit the 64 registers of 1024 threads, and 132 to
+// 280 bytes of them go to local memory and back: 2048 rows of 24576, bf16 without a gate 136 us, 3.0 TB/s, with a full gate
+// 183, fp32 202 (16384 elements in registers and ring: 58 us, 4.6 TB/s).
 #include "block_norm.cuh"
 
 namespace moe {
@@ -188,7 +194,8 @@ __global__ void __launch_bounds__(MAX) block_norm_kernel(const NormParams p, boo
                                 : *reinterpret_cast<const Half*>(static_cast<const uint16_t*>(p.gate) + row + at(j)), g);
                 }
                 if (GATE != MOE_GATE_NONE) {
-                    // (the approximate quotient: two units of fp32, where the exponential has as many)
+                    // (the approximate quotient, two units of fp32; __expf has 2 + 1.2 |g|: for large |g| the gate is near 0, where
+                    // that is lost beside the residual, or near 1, where the exponential hardly counts)
 #pragma unroll
                     for (int i = 0; i < E; ++i) u[j][i] *= sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g[i])) : g[i];
                 }

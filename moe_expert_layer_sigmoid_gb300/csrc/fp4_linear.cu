@@ -404,7 +404,9 @@ cudaError_t launch_linear_fp4(moe_fp4_t x, moe_fp4_t w, int T, int N, int K, uin
     if (T <= 64) return launch<64, false>(p, x, w, T, N, st);
     // Wide tiles that find an SM each (or share K) are done soonest; where there are more of them, the pairs' larger tiles move fewer
     // bytes.  Wide, pairs, us without the quantisation: 256 tokens, N = 8192, K = 512 4.3, 5.2; K = 2048 7.0, 7.1; N = 16384,
-    // K = 512 6.3, 5.7; K = 2048 10.5, 7.7; 2048 tokens, N = 6144, K = 512 12.9, 10.3; K = 4096 36, 21.
+    // K = 512 6.3, 5.7; K = 2048 10.5, 7.7; 2048 tokens, N = 6144, K = 512 12.9, 10.3; K = 4096 36, 21.  The same for 65 to 128
+    // tokens, where half of a pair's tile is empty, with the quantisation: 128 tokens, N = 19584, K = 512 8.7, 9.3; K = 4096 20.1, 19.9;
+    // N = 32768 21.8, 21.8; N = 65536, K = 2048 28.2, 23.1; N = 152064, K = 4096 80, 67; 65 tokens, N = 32768 20.1, 20.4.
     const int64_t tiles = (int64_t)((T + 127) / 128) * ((N + 127) / 128);
     if (tiles > sm_count()) return launch_pair_fp4(x, w, T, N, K, out, ws, st);
     return launch<128, true>(p, x, w, T, N, st);

@@ -2,7 +2,11 @@
 //
 //   s = absmax(row) / 2688,  b = e4m3(absmax(block) / (6 s)),  code = e2m1(x / (b s))
 // A row is read once, into registers.  The way there is bound by instructions as much as by bytes (a quotient per element that
-// has to be the rounded one): 8191 bf16 rows of 4096 18.1 us, 4.8 TB/s.  The way back by bytes: 12.8 us, 6.7 TB/s.
+// has to be the rounded one): 8191 bf16 rows of 4096 18.1 us, 4.8 TB/s (18.8 with no row in L2).  The way back by bytes: 12.8 us
+// where L2 takes what is written, 16.3 with other rows each time, 5.3 TB/s.  Weights, fp32, once per load: 6144 rows of 4096
+// 27.6 us, 4.2 TB/s, 4096 of 16384 93, 3.3.
+// Rows past 16384 take four blocks of 16 fp32 values to a thread, which 64 registers do not hold (148 bytes to local memory
+// and 248 back, fp32 880 and 672): 2048 bf16 rows of 18432 37 us, 2.6 TB/s, of 28672 49, 3.1; fp32 4096 of 18432 192, 1.8.
 #include "fp4_dev.cuh"
 
 namespace moe {

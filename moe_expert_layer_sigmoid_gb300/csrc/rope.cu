@@ -304,8 +304,10 @@ __device__ __forceinline__ void sincos_pi(float x, float& s, float& c) {
 
 // Angles in turns, as 64-bit fractions: the product with a position drops whole turns by itself and
 // is off by position * 2^-65 of one.  What is left is taken to the nearest quarter turn, so that
-// the rest, at most an eighth, keeps 24 bits as a float.  A thread makes four cosines and four sines of a few rows
-// (131072 positions of 128 15.3 us, 4.4 TB/s of stores: its arithmetic and its stores take turns).
+// the rest, at most an eighth, keeps 24 bits as a float.  A thread makes four cosines and four sines of a few rows:
+// 131072 positions of 128 15.3 us, 4.4 TB/s of stores.  Neither the stores nor the arithmetic (issue 56%, ALU 52%) bound it, but the
+// pairs' turns, which each lane takes out of the parameters at a place of its own: the unit that serves such loads one address
+// after another is busy for 65% of the time, and most waits are for it.
 constexpr int kTableRows = 4;  // rows of a thread
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableParams p) {
     const int j = threadIdx.x * 4;

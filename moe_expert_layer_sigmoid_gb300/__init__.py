@@ -11,6 +11,7 @@ as their bit patterns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -252,6 +253,12 @@ def _stream(stream=None):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
+
+
+def _made_for(stream):
+    """Outputs that a call makes itself belong to its stream, as its kernel does: their memory is free there, and what fills
+    them comes first."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def w4(q: torch.Tensor, s: torch.Tensor) -> W4:
@@ -798,17 +805,19 @@ def fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor) -> Fp4:
     return w
 
 
-def _fp4_out(x: torch.Tensor, q, b, s):
+def _fp4_out(x: torch.Tensor, q, b, s, stream):
     if x.dim() != 2:
         raise ValueError("rows must be [rows][K]")
     rows, K = x.shape
     n = moe_fp4_scale_bytes(rows, K)
-    if q is None:
-        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-    if b is None:  # (zeros: the tiles' bytes past the last row are not written)
-        b = torch.zeros(n, dtype=torch.uint8, device=x.device)
-    if s is None:
-        s = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if q is None or b is None or s is None:
+        with _made_for(stream):
+            if q is None:
+                q = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+            if b is None:  # (zeros: the tiles' bytes past the last row are not written)
+                b = torch.zeros(n, dtype=torch.uint8, device=x.device)
+            if s is None:
+                s = torch.empty(rows, dtype=torch.float32, device=x.device)
     dev = _current_device()
     return rows, K, q, b, s, (_flat(q, rows * (K // 2), _U8, dev, "q"), _flat(b, n, _U8, dev, "b"),
                               _flat(s, rows, _F32, dev, "s"))
@@ -817,7 +826,7 @@ def _fp4_out(x: torch.Tensor, q, b, s):
 def moe_pack_fp4(w: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor | None = None,
                  s: torch.Tensor | None = None, stream=None):
     """fp32 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
-    rows, K, q, b, s, to = _fp4_out(w, q, b, s)
+    rows, K, q, b, s, to = _fp4_out(w, q, b, s, stream)
     _check((_lib or lib()).moe_pack_fp4(_flat(w, rows * K, _F32, _current_device(), "w"), rows, K, *to, _stream(stream)),
            "moe_pack_fp4")
     return q, b, s
@@ -826,7 +835,7 @@ def moe_pack_fp4(w: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor
 def moe_quant_rows_fp4(x: torch.Tensor, q: torch.Tensor | None = None, b: torch.Tensor | None = None,
                        s: torch.Tensor | None = None, stream=None):
     """bf16 [rows][K] -> (codes uint8 [rows][K/2], block scales uint8, row scales fp32 [rows])."""
-    rows, K, q, b, s, to = _fp4_out(x, q, b, s)
+    rows, K, q, b, s, to = _fp4_out(x, q, b, s, stream)
     _check((_lib or lib()).moe_quant_rows_fp4(_flat(x, rows * K, _BF16, _current_device(), "x"), rows, K, *to,
                                               _stream(stream)), "moe_quant_rows_fp4")
     return q, b, s
@@ -837,7 +846,8 @@ def moe_unpack_fp4(q: torch.Tensor, b: torch.Tensor, s: torch.Tensor, out: torch
     w = fp4(q, b, s)
     rows, K = w.shape
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.device)
+        with _made_for(stream):
+            out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.device)
     _check((_lib or lib()).moe_unpack_fp4(w, rows, K, _flat(out, rows * K, _BF16, _current_device(), "out"),
                                           _stream(stream)), "moe_unpack_fp4")
     return out

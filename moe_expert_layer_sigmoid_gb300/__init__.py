@@ -275,10 +275,11 @@ def moe_pack_w4(w: torch.Tensor, group: int, q: torch.Tensor | None = None,
                 s: torch.Tensor | None = None, stream=None):
     """fp32 [rows][K] -> (q uint8 [rows][K/2], s fp16 bits as int16 [rows][K/group])."""
     rows, K = w.shape
-    if q is None:
-        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=w.device)
-    if s is None:
-        s = torch.empty((rows, K // group), dtype=torch.int16, device=w.device)
+    with _made_for(stream):
+        if q is None:
+            q = torch.empty((rows, K // 2), dtype=torch.uint8, device=w.device)
+        if s is None:
+            s = torch.empty((rows, K // group), dtype=torch.int16, device=w.device)
     _check(lib().moe_pack_w4(_dev(w, torch.float32, "w"), rows, K, group,
                              _dev(q, torch.uint8, "q"), _dev(s, torch.int16, "s"),
                              _stream(stream)), "moe_pack_w4")
@@ -289,10 +290,11 @@ def moe_pack_w8(w: torch.Tensor, q: torch.Tensor | None = None, s: torch.Tensor 
                 stream=None):
     """fp32 [rows][K] -> (E4M3 codes uint8 [rows][K], fp32 row scales [rows])."""
     rows, K = w.shape
-    if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=w.device)
-    if s is None:
-        s = torch.empty(rows, dtype=torch.float32, device=w.device)
+    with _made_for(stream):
+        if q is None:
+            q = torch.empty((rows, K), dtype=torch.uint8, device=w.device)
+        if s is None:
+            s = torch.empty(rows, dtype=torch.float32, device=w.device)
     _check(lib().moe_pack_w8(_dev(w, torch.float32, "w"), rows, K, _dev(q, torch.uint8, "q"),
                              _dev(s, torch.float32, "s"), _stream(stream)), "moe_pack_w8")
     return q, s
@@ -302,10 +304,12 @@ def moe_quant_rows_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
                        a: torch.Tensor | None = None, stream=None):
     """bf16 rows (int16 bits) [rows][K] -> (E4M3 codes uint8 [rows][K], fp32 scales [rows])."""
     rows, K = x.shape
-    if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
-    if a is None:
-        a = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if q is None or a is None:
+        with _made_for(stream):
+            if q is None:
+                q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+            if a is None:
+                a = torch.empty(rows, dtype=torch.float32, device=x.device)
     _check(lib().moe_quant_rows_fp8(_dev(x, torch.int16, "x"), rows, K, _dev(q, torch.uint8, "q"),
                                     _dev(a, torch.float32, "a"), _stream(stream)),
            "moe_quant_rows_fp8")
@@ -351,12 +355,13 @@ def moe_import_q4_blocks(blocks: torch.Tensor, K: int, group: int, w_scratch=Non
     if blocks.dim() != 2 or blocks.shape[1] != (K // 32) * 18:
         raise ValueError("blocks must be [rows][K/32*18] bytes")
     dev = blocks.device
-    if w_scratch is None:
-        w_scratch = torch.empty((rows, K), dtype=torch.float32, device=dev)
-    if q is None:
-        q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
-    if s is None:
-        s = torch.empty((rows, K // group), dtype=torch.int16, device=dev)
+    with _made_for(stream):
+        if w_scratch is None:
+            w_scratch = torch.empty((rows, K), dtype=torch.float32, device=dev)
+        if q is None:
+            q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+        if s is None:
+            s = torch.empty((rows, K // group), dtype=torch.int16, device=dev)
     _check(lib().moe_import_q4_blocks(
         _dev(blocks, torch.uint8, "blocks"), rows, K, group,
         _dev(w_scratch, torch.float32, "w_scratch"), _dev(q, torch.uint8, "q"),

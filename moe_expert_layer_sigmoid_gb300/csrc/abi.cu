@@ -154,8 +154,6 @@ using namespace moe;
 
 namespace {
 
-moe_status_t map_err(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 __global__ void set_waits_kernel(WsHeader* hdr, unsigned long long wait_ns, int withhold_stage) {
     hdr->wait_ns = wait_ns;
     hdr->withhold_stage = withhold_stage;
@@ -280,36 +278,36 @@ moe_status_t layer_forward(const uint16_t* x, const float* W_r, const float* bia
             e = launch_router_decode(x, W_r, bias, d, topk_idx, topk_w, nullptr,
                                      ws_at<float>(ws, L.logits), L.router_ksplit, counts, offsets,
                                      perm, pos, sched, hdr, s);
-            if (e != cudaSuccess) return MOE_ERR_CUDA;
+            if (e != cudaSuccess) return map_err(e);
         } else {
             e = launch_router(x, W_r, bias, d, topk_idx, topk_w, nullptr,
                               ws_at<float>(ws, L.logits), L.router_ksplit, L.router_ksplit_large,
                               ws_at<uint16_t>(ws, L.wr_planes), hdr, s);
-            if (e != cudaSuccess) return MOE_ERR_CUDA;
+            if (e != cudaSuccess) return map_err(e);
             e = launch_descriptors(topk_idx, d, counts, offsets, perm, pos, sched, hdr,
                                    ws_at<int4>(ws, L.tiles), L.max_tiles,
                                    ws_at<int32_t>(ws, L.hist), s);
-            if (e != cudaSuccess) return MOE_ERR_CUDA;
+            if (e != cudaSuccess) return map_err(e);
         }
         if (tc_w && tc_decode_supported(d)) {
             e = launch_gateup_tc(x, d, offsets, sched, Wgu, Wgu_s, H, &hdr->n_active, hdr, true, s);
-            if (e != cudaSuccess) return MOE_ERR_CUDA;
+            if (e != cudaSuccess) return map_err(e);
             return map_err(launch_down_tc(H, d, offsets, sched, Wd, Wd_s, Y, &hdr->n_active,
                                           topk_w, pos, residual, out, true, s));
         }
         e = launch_gateup_gemv(x, d, offsets, perm, sched, Wgu, Wgu_s, H, &hdr->n_active, hdr,
                                true, s);
-        if (e != cudaSuccess) return MOE_ERR_CUDA;
+        if (e != cudaSuccess) return map_err(e);
         return map_err(launch_down_gemv(H, d, offsets, sched, Wd, Wd_s, Y, &hdr->n_active, topk_w,
                                         pos, residual, out, hdr, true, s));
     }
     e = launch_router(x, W_r, bias, d, topk_idx, topk_w, nullptr, ws_at<float>(ws, L.logits),
                       L.router_ksplit, L.router_ksplit_large, ws_at<uint16_t>(ws, L.wr_planes), hdr,
                       s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     e = launch_descriptors(topk_idx, d, counts, offsets, perm, pos, sched, hdr,
                            ws_at<int4>(ws, L.tiles), L.max_tiles, ws_at<int32_t>(ws, L.hist), s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     if ((st = gateup_impl(x, d, offsets, perm, sched, Wgu, Wgu_s, H, ws, s)) != MOE_OK) return st;
     if ((st = down_impl(H, d, offsets, sched, Wd, Wd_s, Y, ws, s)) != MOE_OK) return st;
     return map_err(launch_combine(Y, topk_w, pos, d, residual, out, s));
@@ -364,7 +362,8 @@ moe_status_t moe_import_q4_blocks(const uint8_t* blocks, int64_t rows, int64_t K
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (group <= 32)  // each group inside one block: s = d, q = n - 8, exact
         return map_err(launch_import_q4_direct(blocks, rows, K, group, w_scratch, q, s, st));
-    if (launch_decode_q4_blocks(blocks, rows, K, w_scratch, st) != cudaSuccess) return MOE_ERR_CUDA;
+    const cudaError_t e = launch_decode_q4_blocks(blocks, rows, K, w_scratch, st);
+    if (e != cudaSuccess) return map_err(e);
     return map_err(launch_pack_w4(w_scratch, rows, K, group, q, s, st));
 }
 
@@ -590,19 +589,19 @@ moe_status_t moe_layer_forward_w8a8(const uint16_t* x, const float* W_r, const f
     cudaError_t e = launch_router(x, W_r, bias, d, topk_idx, topk_w, nullptr,
                                   ws_at<float>(ws, L.logits), L.router_ksplit,
                                   L.router_ksplit_large, ws_at<uint16_t>(ws, L.wr_planes), hdr, s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     // 256-token tiles: the fp8 kernel goes faster with more flops per weight byte
     e = launch_descriptors(topk_idx, d, ws_at<int32_t>(ws, L.counts), ws_at<int32_t>(ws, L.offsets),
                            perm, pos, ws_at<int32_t>(ws, L.sched), hdr, ws_at<int4>(ws, L.tiles),
                            L.max_tiles, ws_at<int32_t>(ws, L.hist), s, 256);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     e = launch_gateup_w8a8(x, d, perm, Wgu, Wgu_s, H, hdr, tiles, L.max_tiles,
                            ws_at<uint8_t>(ws, L.xs), ws_at<float>(ws, L.w8_xa),
                            ws_at<uint8_t>(ws, L.w8_xt), ws_at<float>(ws, L.w8_xta), s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     e = launch_down_w8a8(H, d, Wd, Wd_s, Y, hdr, tiles + L.max_tiles, L.max_tiles,
                          ws_at<uint8_t>(ws, L.w8_hq), ws_at<float>(ws, L.w8_ha), s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (e != cudaSuccess) return map_err(e);
     return map_err(launch_combine(Y, topk_w, pos, d, nullptr, out, s));
 }
 
@@ -620,13 +619,11 @@ moe_status_t moe_layer_forward_host(const uint16_t* x_host, const float* W_r, co
     const size_t bytes = sizeof(uint16_t) * (size_t)dims->T * dims->d;
     uint16_t* xd = ws_at<uint16_t>(ws, L.x_stage);
     uint16_t* od = ws_at<uint16_t>(ws, L.out_stage);
-    if (cudaMemcpyAsync(xd, x_host, bytes, cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    const cudaError_t e = cudaMemcpyAsync(xd, x_host, bytes, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return map_err(e);
     st = moe_layer_forward(xd, W_r, bias, dims, Wgu, Wd, Wgu_s, Wd_s, od, ws, ws_bytes, stream);
     if (st != MOE_OK) return st;
-    if (cudaMemcpyAsync(out_host, od, bytes, cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return MOE_OK;
+    return map_err(cudaMemcpyAsync(out_host, od, bytes, cudaMemcpyDeviceToHost, s));
 }
 
 moe_status_t moe_debug_set_waits(void* ws, size_t ws_bytes, uint64_t wait_ns,
@@ -642,17 +639,16 @@ moe_status_t moe_debug_set_waits(void* ws, size_t ws_bytes, uint64_t wait_ns,
 moe_status_t moe_check_device_status(void* ws, size_t ws_bytes, void* stream) {
     if (!ws || ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return map_err(e);
     int32_t flags = 0;
     WsHeader* hdr = static_cast<WsHeader*>(ws);
-    if (cudaMemcpy(&flags, &hdr->error_flags, sizeof(flags), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    e = cudaMemcpy(&flags, &hdr->error_flags, sizeof(flags), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return map_err(e);
     if (flags) {
         const int32_t zero = 0;
-        if (cudaMemcpy(&hdr->error_flags, &zero, sizeof(zero), cudaMemcpyHostToDevice) !=
-            cudaSuccess)
-            return MOE_ERR_CUDA;
-        return MOE_ERR_DEVICE_CHECK;
+        e = cudaMemcpy(&hdr->error_flags, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+        return e == cudaSuccess ? MOE_ERR_DEVICE_CHECK : map_err(e);
     }
     return MOE_OK;
 }

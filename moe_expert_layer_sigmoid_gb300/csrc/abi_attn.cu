@@ -44,8 +44,6 @@ moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need) {
                                                                            : MOE_OK;
 }
 
-moe_status_t map_err(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
 }  // namespace moe
 
 extern "C" {

@@ -224,6 +224,14 @@ int sm_count();
 // default (once per kernel and device; safe to call during stream capture).
 cudaError_t ensure_dynamic_smem(const void* kernel, size_t bytes);
 
+// A CUDA call's result as a status.  The runtime keeps an error until it is asked for; asked for here, it is not taken for
+// the next call's.
+inline moe_status_t map_err(cudaError_t e) {
+    if (e == cudaSuccess) return MOE_OK;
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------------------
 // Small device helpers.
 __device__ __forceinline__ float bf16_lo(uint32_t pair) { return __uint_as_float(pair << 16); }

@@ -53,6 +53,5 @@ moe_status_t check_kv_dims(const moe_kv_dims_t* d);
 bool kv_ok(const moe_kv_t* c, const moe_kv_dims_t& d);
 bool rows_ok(const void* p, int64_t ld, int32_t T, int64_t width);
 moe_status_t check_ws(const void* ws, size_t ws_bytes, size_t need);
-moe_status_t map_err(cudaError_t e);
 
 }  // namespace moe

@@ -64,11 +64,11 @@ extern "C" moe_status_t moe_router_topk_noalloc(const uint16_t* x, const float* 
     if (!moe::act_ok(x) || !moe::act_ok(W_r) || !bias || !topk_idx || !topk_w)
         return MOE_ERR_INVALID_ARG;
     float* scratch = nullptr;
-    if (scratch_on_current_device(&scratch) != cudaSuccess) return MOE_ERR_CUDA;
+    cudaError_t err = scratch_on_current_device(&scratch);
+    if (err != cudaSuccess) return moe::map_err(err);
     // The logits kernel writes every partial that the top-k kernel reads within
     // this call, so leftovers of an earlier call never leak into the result.
-    cudaError_t err = moe::launch_router(x, W_r, bias, *dims, topk_idx, topk_w, margin, scratch,
-                                         L.router_ksplit, 1, nullptr, nullptr,
-                                         static_cast<cudaStream_t>(stream));
-    return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    err = moe::launch_router(x, W_r, bias, *dims, topk_idx, topk_w, margin, scratch, L.router_ksplit, 1, nullptr, nullptr,
+                             static_cast<cudaStream_t>(stream));
+    return moe::map_err(err);
 }

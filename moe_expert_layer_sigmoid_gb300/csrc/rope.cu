@@ -110,8 +110,8 @@ __device__ __forceinline__ void store_key(const float (&f)[2][8], uint8_t* row, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = s > 0.0f ? __fdiv_rn(f[j][i], s) : 0.0f;
         // The recipe's clamp: a turned key may be so small that its scale is a few units of 2^-149, rounded by up to half of
-        // one, and quotients reach 10.  (NaN stays; E4M3's conversion saturates by itself.)
-        if (FMT == kKvInt4) {
+        // one, and quotients reach 10.  A normal scale needs none.  (NaN stays; E4M3's conversion saturates by itself.)
+        if (FMT == kKvInt4 && s < 0x1p-126f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = y[i] > 7.0f ? 7.0f : y[i] < -8.0f ? -8.0f : y[i];
         }

@@ -704,7 +704,7 @@ moe_status_t moe_rope_table(const moe_rope_config_t* config, int32_t pos0, int32
 /* How rows are turned.  rot: multiple of 16, at most D.  q_norm, k_norm (fp32 [D],
    16-byte aligned, or NULL): each head x becomes x / sqrt(mean(x^2) + eps) * norm first,
    in fp32; eps >= 0 (with 0, a head of zeros becomes NaN).  Heads whose squares add up
-   past the range of fp32 are outside what the norms are for. */
+   past the range of fp32, or with eps = 0 below it, are outside what the norms are for. */
 typedef struct {
     const float* table;
     const float* q_norm;
@@ -786,8 +786,8 @@ typedef struct {
  *   x            (device) out: bf16 [T][d]; may be y itself; NULL exactly when w_pre is
  * All contiguous and 16-byte aligned (a MOE_GATE_TOKEN gate 4-byte); but for what is
  * said above, outputs do not overlap inputs or each other.  With eps = 0 a row of
- * zeros becomes NaN; values whose squares add up past the range of fp32 are outside
- * what the norms are for. */
+ * zeros becomes NaN; values whose squares add up past the range of fp32, or with
+ * eps = 0 below it, are outside what the norms are for. */
 moe_status_t moe_block_norm(const uint16_t* y, const void* residual, const void* gate,
                             const float* w_post, const float* w_pre, const moe_norm_dims_t* dims,
                             void* residual_out, uint16_t* x, void* stream);

@@ -535,8 +535,6 @@ typedef struct {
  *          H_kv * D when T > 1 (so slices of a fused projection's output serve)
  *   slots  (device) int32 [T], each token's slot; negative: not written.  A
  *          slot past the pool is not written and sets the device check flag.
- *          The slots of a call differ: one that is named twice holds some of
- *          either token's row.
  *          Slots of one call are distinct.
  *   ws     a workspace of at least 256 bytes, zero-filled before its first use
  *          (its header takes the device check flags)
